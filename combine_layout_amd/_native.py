@@ -28,6 +28,9 @@ DISPATCH_MODES = {"auto": AFD_DISPATCH_AUTO, "split": AFD_DISPATCH_SPLIT, "one_l
 ROUTE_NONE, ROUTE_RANGE, ROUTE_NEG, ROUTE_DUP = 0, 1, 2, 3
 MAX_SOURCES, MAX_PARTITIONS, MAX_EXPERTS, MAX_TOPK = 16, 16, 512, 32
 STATIC_SCRATCH_BYTES = 64 << 20
+AFD_ACT_NONE, AFD_ACT_SWIGLU = 0, 1
+ACTIVATIONS = {None: AFD_ACT_NONE, "swiglu": AFD_ACT_SWIGLU}
+MAX_ADAPTERS, MAX_RANK = 65536, 128
 
 STATUS_NAMES = {0: "AFD_OK", -1: "AFD_E_ARG", -2: "AFD_E_SHAPE", -3: "AFD_E_ORDER",
                 -4: "AFD_E_CAPACITY", -5: "AFD_E_ROUTE", -6: "AFD_E_HIP", -7: "AFD_E_TIMEOUT"}
@@ -53,6 +56,23 @@ class RoundInfo(ctypes.Structure):
     _fields_ = [("round", ctypes.c_uint64), ("dispatch_path", ctypes.c_int32),
                 ("dispatch_kernels", ctypes.c_int32), ("combine_kernels", ctypes.c_int32),
                 ("tokens", ctypes.c_int32), ("layout_tiles", ctypes.c_int32), ("tile_tokens", ctypes.c_int32)]
+
+
+class ProductConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("alignment", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
+class ProductWeights(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scaling", ctypes.c_void_p)]
+
+
+class FfnConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("alignment", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("inner", ctypes.c_int32), ("dtype", ctypes.c_int32), ("num_adapters", ctypes.c_int32),
+                ("rank", ctypes.c_int32)]
 
 
 DISPATCH_PATHS = {0: "none", 1: "one_kernel", 2: "tiled", 3: "cached", 4: "empty", 5: "one_launch"}
@@ -84,6 +104,13 @@ SIGNATURES = {
     "afd_get_partials": ([_P, _I32, _I32, ctypes.POINTER(_P), ctypes.POINTER(_I64)], _I32),
     "afd_get_round_info": ([_P, ctypes.POINTER(RoundInfo)], _I32),
     "afd_set_dispatch_wait": ([_P, _I32], _I32),
+    "afd_product_query": ([ctypes.POINTER(ProductConfig), _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "afd_expert_product": ([ctypes.POINTER(ProductConfig), _I64, _P, _P, _P, _P, ctypes.POINTER(ProductWeights), _P, _P,
+                            _P, ctypes.c_size_t, _P], _I32),
+    "afd_ffn_query": ([ctypes.POINTER(FfnConfig), _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "afd_expert_ffn": ([ctypes.POINTER(FfnConfig), _I64, _P, _P, _P, _P, ctypes.POINTER(ProductWeights),
+                        ctypes.POINTER(ProductWeights), _P, _P, ctypes.c_size_t, _P], _I32),
+    "afd_worker_tags": ([_P, _I32, ctypes.POINTER(_P), _P, _I64, ctypes.POINTER(Receipt), _P], _I32),
     "afd_status_string": ([_I32], ctypes.c_char_p),
 }
 

@@ -15,6 +15,7 @@ from typing import List, NamedTuple, Optional
 import torch
 
 from . import _native as nat
+from . import experts as _experts
 
 topk_idx_dtype = torch.int32
 
@@ -221,6 +222,46 @@ class Buffer:
                                        _stream(self.device))
         nat.check(st, "worker_reply")
         self._round_refs[("reply", f)] = rows
+
+    # -- the experts' side of a partition, between its receive and its reply -----
+    def worker_tags(self, f, tags, received, *, out=None) -> torch.Tensor:
+        """Every token's int32 tag (its request's adapter) at the token's
+        receive rows of partition f: int32 [receive_rows].  tags: per source
+        an int32 [T] tensor (None for an empty source).  Rows of no choice
+        keep what `out` held; without `out` they are -1."""
+        if len(tags) != self.N:
+            raise ValueError("tags must hold one tensor per source")
+        ptrs = (ctypes.c_void_p * self.N)()
+        for s, t in enumerate(tags):
+            T = self._T[s]
+            if T == 0:
+                continue
+            if t is None or t.dtype != torch.int32 or tuple(t.shape) != (T,) or not t.is_contiguous() or \
+                    t.device != self.device:
+                raise ValueError("tags must be contiguous int32 [T] tensors on the buffer's device")
+            ptrs[s] = t.data_ptr()
+        n = received.receive_rows
+        if out is None:
+            out = torch.full((n,), -1, dtype=torch.int32, device=self.device)
+        elif out.dtype != torch.int32 or tuple(out.shape) != (n,) or not out.is_contiguous() or \
+                out.device != self.device:
+            raise ValueError("out must be contiguous int32 [receive_rows] on the buffer's device")
+        with _experts.on_device(self.device):
+            st = self.lib.afd_worker_tags(self.ctx, f, ptrs, _ptr(out), n, ctypes.byref(received.receipt),
+                                          _stream(self.device))
+        nat.check(st, "worker_tags")
+        self._round_refs[("tags", f)] = (tags, out)
+        return out
+
+    def worker_experts(self, f, received, experts, *, adapters=None, row_adapters=None, out=None) -> torch.Tensor:
+        """The reply of partition f: its experts' network over the received
+        rows (expert_ffn with the buffer's layout), [receive_rows, H] BF16,
+        ready for worker_reply.  row_adapters: worker_tags of the tokens'
+        adapters."""
+        if received.receipt.partition != f:
+            raise ValueError("received belongs to another partition")
+        return _experts.expert_ffn(received.rows, received.ends, experts, alignment=self.alpha,
+                                   x_scales=received.scales, adapters=adapters, row_adapters=row_adapters, out=out)
 
     def source_collect(self, s, *, view=False) -> torch.Tensor:
         res = ctypes.c_void_p(0)

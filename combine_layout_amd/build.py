@@ -42,7 +42,7 @@ def build_lib(extra=()):
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = LIB + ".tmp%d" % os.getpid()
     _run([HIPCC, *HIP_FLAGS, *extra, os.path.join(CSRC, "afd_core.cpp"),
-          os.path.join(CSRC, "afd_kernels.hip"), "-o", tmp])
+          os.path.join(CSRC, "afd_kernels.hip"), os.path.join(CSRC, "afd_experts.hip"), "-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 

@@ -139,6 +139,20 @@ int be_read_stall(uint32_t *, void *, int clear, int *stalled)
     return g_fail;
 }
 
+int be_launch_product(const ProductPlan &p, void *)
+{
+    logf("product E=%d alpha=%d k=%d n=%d fp8=%d out8=%d gated=%d nad=%d rank=%d rows=%lld x=%p out=%p outs=%p t=%p", p.E,
+         p.alpha, p.k, p.n, p.fp8, p.out8, p.gated, p.nad, p.rank, static_cast<long long>(p.rows), p.x, p.out,
+         static_cast<void *>(p.outs), static_cast<void *>(p.t));
+    return g_fail;
+}
+
+int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *, int32_t *out, void *)
+{
+    logf("tags f=%d ntok=%d out=%p", f, p.ntok, static_cast<void *>(out));
+    return g_fail;
+}
+
 int be_device_sync()
 {
     logf("sync");

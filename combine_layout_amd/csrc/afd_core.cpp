@@ -258,6 +258,92 @@ void record_info(afd_ctx *c)
     }
 }
 
+// ---- the experts' side ----
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+afd_status check_product(const afd_product_config *c, int64_t rows)
+{
+    if (!c || rows < 0 || rows >= (int64_t(1) << 24)) return AFD_E_ARG;
+    if (c->num_experts < 1 || c->num_experts > kMaxExperts || c->alignment < 1) return AFD_E_SHAPE;
+    if (c->dtype != AFD_BF16 && c->dtype != AFD_FP8_E4M3) return AFD_E_SHAPE;
+    if (c->activation != AFD_ACT_NONE && c->activation != AFD_ACT_SWIGLU) return AFD_E_SHAPE;
+    const bool fp8 = c->dtype == AFD_FP8_E4M3, gated = c->activation == AFD_ACT_SWIGLU;
+    if (c->out_dtype != AFD_BF16 && !(c->out_dtype == AFD_FP8_E4M3 && fp8 && gated)) return AFD_E_SHAPE;
+    if (c->k < 1 || c->k % (fp8 ? 128 : 64) != 0) return AFD_E_SHAPE;
+    if (c->n < 1 || c->n % (fp8 && gated ? 128 : 16) != 0) return AFD_E_SHAPE;
+    // byte offsets inside one expert's weights are 32-bit in the kernels
+    if (int64_t(c->n) * (gated ? 2 : 1) * c->k * (fp8 ? 1 : 2) >= (int64_t(1) << 31)) return AFD_E_SHAPE;
+    if (c->num_adapters < 0 || c->num_adapters > AFD_MAX_ADAPTERS) return AFD_E_SHAPE;
+    if (c->num_adapters == 0 ? c->rank != 0 : c->rank < 8 || c->rank > AFD_MAX_RANK || c->rank % 8 != 0)
+        return AFD_E_SHAPE;
+    return AFD_OK;
+}
+
+size_t product_workspace(const afd_product_config &c, int64_t rows)
+{
+    if (c.num_adapters == 0) return 0;
+    return align256(size_t(rows) * size_t(c.rank) * (c.activation == AFD_ACT_SWIGLU ? 2 : 1) * 4);
+}
+
+// Pointers of a product's weights; `fp8` and `adapters` say which there are.
+bool weights_ok(const afd_product_weights *w, bool fp8, bool adapters)
+{
+    if (!w || !w->w || !aligned(w->w, 16)) return false;
+    if (fp8 ? !w->w_scales || !aligned(w->w_scales, 4) : w->w_scales != nullptr) return false;
+    if (!adapters) return !w->a && !w->b && !w->scaling;
+    return w->a && w->b && w->scaling && aligned(w->a, 16) && aligned(w->b, 16) && aligned(w->scaling, 4);
+}
+
+ProductPlan plan_product(const afd_product_config &c, int64_t rows, const void *x, const float *xs,
+                         const int32_t *ends, const int32_t *tags, const afd_product_weights &w, void *out, float *outs,
+                         void *t)
+{
+    ProductPlan p;
+    p.E = c.num_experts;
+    p.alpha = c.alignment;
+    p.k = c.k;
+    p.n = c.n;
+    p.fp8 = c.dtype == AFD_FP8_E4M3;
+    p.out8 = c.out_dtype == AFD_FP8_E4M3;
+    p.gated = c.activation == AFD_ACT_SWIGLU;
+    p.nad = c.num_adapters;
+    p.rank = c.rank;
+    p.rows = rows;
+    p.x = x;
+    p.xs = xs;
+    p.ends = ends;
+    p.tags = tags;
+    p.w = w;
+    p.out = out;
+    p.outs = outs;
+    p.t = c.num_adapters ? static_cast<float *>(t) : nullptr;
+    return p;
+}
+
+// The network's two products and its workspace: h, its scales, the adapters' A x.
+struct FfnPlan {
+    afd_product_config up{}, down{};
+    size_t hs = 0, t = 0, total = 0;   // byte offsets behind h (at 0)
+};
+
+afd_status plan_ffn(const afd_ffn_config *c, int64_t rows, FfnPlan *f)
+{
+    if (!c || !f) return AFD_E_ARG;
+    const int fp8 = c->dtype == AFD_FP8_E4M3;
+    f->up = {c->num_experts, c->alignment,  c->hidden,      c->inner,       c->dtype,
+             c->dtype,       AFD_ACT_SWIGLU, c->num_adapters, c->rank};
+    f->down = {c->num_experts, c->alignment,  c->inner,       c->hidden,      c->dtype,
+               AFD_BF16,       AFD_ACT_NONE, c->num_adapters, c->rank};
+    afd_status st = check_product(&f->up, rows);
+    if (st == AFD_OK) st = check_product(&f->down, rows);
+    if (st != AFD_OK) return st;
+    f->hs = align256(size_t(rows) * size_t(c->inner) * (fp8 ? 1 : 2));
+    f->t = f->hs + (fp8 ? align256(size_t(rows) * size_t(c->inner / 128) * 4) : 0);
+    f->total = f->t + product_workspace(f->up, rows);
+    return AFD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -583,6 +669,85 @@ afd_status afd_source_collect(afd_ctx *c, int32_t s, int32_t view, const void **
     c->ncollected += 1;
     if (c->ncollected == g.num_sources) c->phase = kIdle;
     return AFD_OK;
+}
+
+afd_status afd_product_query(const afd_product_config *cfg, int64_t rows, size_t *workspace_bytes)
+{
+    if (!workspace_bytes) return AFD_E_ARG;
+    const afd_status st = check_product(cfg, rows);
+    if (st != AFD_OK) return st;
+    *workspace_bytes = product_workspace(*cfg, rows);
+    return AFD_OK;
+}
+
+afd_status afd_expert_product(const afd_product_config *cfg, int64_t rows, const void *x, const float *x_scales,
+                              const int32_t *ends, const int32_t *row_adapters, const afd_product_weights *weights,
+                              void *out, float *out_scales, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const afd_status st = check_product(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (rows == 0) return AFD_OK;
+    const bool fp8 = cfg->dtype == AFD_FP8_E4M3, out8 = cfg->out_dtype == AFD_FP8_E4M3, low = cfg->num_adapters > 0;
+    if (!x || !ends || !out || !aligned(x, 16) || !aligned(ends, 4) || !aligned(out, 16)) return AFD_E_ARG;
+    if (fp8 ? !x_scales || !aligned(x_scales, 4) : x_scales != nullptr) return AFD_E_ARG;
+    if (out8 ? !out_scales || !aligned(out_scales, 4) : out_scales != nullptr) return AFD_E_ARG;
+    if (low ? !row_adapters || !aligned(row_adapters, 4) : row_adapters != nullptr) return AFD_E_ARG;
+    if (!weights_ok(weights, fp8, low)) return AFD_E_ARG;
+    const size_t need = product_workspace(*cfg, rows);
+    if (need > 0 && (!workspace || !aligned(workspace, 256))) return AFD_E_ARG;
+    if (workspace_bytes < need) return AFD_E_CAPACITY;
+    const ProductPlan p =
+        plan_product(*cfg, rows, x, x_scales, ends, row_adapters, *weights, out, out_scales, workspace);
+    return be_launch_product(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_ffn_query(const afd_ffn_config *cfg, int64_t rows, size_t *workspace_bytes)
+{
+    if (!workspace_bytes) return AFD_E_ARG;
+    FfnPlan f;
+    const afd_status st = plan_ffn(cfg, rows, &f);
+    if (st != AFD_OK) return st;
+    *workspace_bytes = f.total;
+    return AFD_OK;
+}
+
+afd_status afd_expert_ffn(const afd_ffn_config *cfg, int64_t rows, const void *x, const float *x_scales,
+                          const int32_t *ends, const int32_t *row_adapters, const afd_product_weights *up,
+                          const afd_product_weights *down, void *out, void *workspace, size_t workspace_bytes,
+                          void *stream)
+{
+    FfnPlan f;
+    const afd_status st = plan_ffn(cfg, rows, &f);
+    if (st != AFD_OK) return st;
+    if (rows == 0) return AFD_OK;
+    const bool fp8 = cfg->dtype == AFD_FP8_E4M3, low = cfg->num_adapters > 0;
+    if (!x || !ends || !out || !aligned(x, 16) || !aligned(ends, 4) || !aligned(out, 16)) return AFD_E_ARG;
+    if (fp8 ? !x_scales || !aligned(x_scales, 4) : x_scales != nullptr) return AFD_E_ARG;
+    if (low ? !row_adapters || !aligned(row_adapters, 4) : row_adapters != nullptr) return AFD_E_ARG;
+    if (!weights_ok(up, fp8, low) || !weights_ok(down, fp8, low)) return AFD_E_ARG;
+    if (!workspace || !aligned(workspace, 256)) return AFD_E_ARG;
+    if (workspace_bytes < f.total) return AFD_E_CAPACITY;
+    char *ws = static_cast<char *>(workspace);
+    float *hs = fp8 ? reinterpret_cast<float *>(ws + f.hs) : nullptr;
+    const ProductPlan pu = plan_product(f.up, rows, x, x_scales, ends, row_adapters, *up, ws, hs, ws + f.t);
+    const ProductPlan pd = plan_product(f.down, rows, ws, hs, ends, row_adapters, *down, out, nullptr, ws + f.t);
+    if (be_launch_product(pu, stream) != 0) return AFD_E_HIP;
+    return be_launch_product(pd, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_worker_tags(afd_ctx *c, int32_t f, const int32_t *const *tags, int32_t *out, int64_t receive_rows,
+                           const afd_receipt *receipt, void *stream)
+{
+    if (!c || !receipt || !tags) return AFD_E_ARG;
+    if (f < 0 || f >= c->cfg.num_partitions) return AFD_E_ARG;
+    if (c->phase != kExchanging || !c->received[f] || c->replied[f]) return AFD_E_ORDER;
+    if (receipt->round != c->round || receipt->partition != f) return AFD_E_ORDER;
+    if (receive_rows != c->recv_rows[f]) return AFD_E_SHAPE;
+    if (receive_rows > 0 && (!out || !aligned(out, 4))) return AFD_E_ARG;
+    for (int s = 0; s < c->cfg.num_sources; ++s)
+        if (c->T[s] > 0 && (!tags[s] || !aligned(tags[s], 4))) return AFD_E_ARG;
+    if (c->plan.ntok == 0) return AFD_OK;
+    return be_launch_tags(c->plan, f, tags, out, stream) == 0 ? AFD_OK : AFD_E_HIP;
 }
 
 afd_status afd_get_partials(afd_ctx *c, int32_t s, int32_t f, const void **rows, int64_t *row_bytes)

@@ -1,0 +1,608 @@
+// afd_experts.hip -- gfx950 kernels of the experts' side of a round: products
+// grouped by expert, their low-rank adapters, and the row tags; and the HIP
+// executor behind their be_* hooks.
+//
+// Mathematics.  Expert j owns rows [align_up(ends[j-1], alpha), ends[j]).
+//   product   out[r, n] = act( sum_k x[r, k] W[j, n, k] )
+//   FP8       x = q * xs[r, k/128] and W = p * ws[j, n/128, k/128]: the codes of
+//             one 128-column block are multiplied and summed by the matrix unit,
+//             and each block's sum enters the float32 sum times xs * ws
+//   adapters  t[r, :] = scaling[a] * A[a, j] x[r] (k_shrink, float32), then
+//             B[a, j] t[r] is added to row r's sums before the activation
+//
+// Orientation.  The matrix unit's A operand holds weight rows and its B operand
+// rows of x, so that D's column, and with it everything a lane holds of a
+// result, belongs to ONE row of x: a lane needs one row scale, one adapter and
+// one bounds check, and rows cannot reach each other's results, whatever their
+// values.
+
+#include <hip/hip_runtime.h>
+
+#include "afd_plan.h"
+
+namespace afd {
+namespace {
+
+constexpr int kWave = 64;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+template <typename T>
+using gptr = __attribute__((address_space(1))) T *;
+
+// One lane's operand of a 128-byte step of k: two 16-byte pieces (two bf16
+// products of 32 columns, or one E4M3 product of 128).  Both operands hold the
+// same columns in the same places, so the order of the columns inside a step
+// is free; lane group g (16 lanes) takes bytes 32g .. 32g + 31 of the step.
+struct Frag {
+    u32x4 p[2];
+};
+
+__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
+// E4M3 x E4M3 over 128 columns; the block exponents are 127 (times one).
+__device__ __forceinline__ f32x4 mfma_fp8(const Frag &a, const Frag &b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a), __builtin_bit_cast(i32x8, b), c,
+                                                            0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+}
+
+// float32 to bf16, nearest even, in the low half (NaN stays NaN).
+__device__ __forceinline__ uint32_t to_bf16(float v)
+{
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return to_bf16(lo) | (to_bf16(hi) << 16); }
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+
+// ------------------------------------------------------------- row tiles ----
+
+// The experts' rows as tiles, built by every workgroup in LDS from ends[]
+// (512 experts at most: a few hundred bytes read, one wavefront's prefix sum).
+struct Tiles {
+    int first[kMaxExperts + 1];   // tiles before expert e
+    int start[kMaxExperts];       // first row
+    int count[kMaxExperts];       // rows
+};
+
+// Wavefront 0 of the workgroup; the caller places a barrier behind it.
+__device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int rows, int height)
+{
+    const int lane = threadIdx.x;
+    const int per = (E + kWave - 1) / kWave, lo = lane * per;
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = lo + i;
+        if (e >= E) break;
+        const uint32_t prev = e == 0 ? 0u : uint32_t(min(max(ends[e - 1], 0), rows));
+        const uint32_t st = (prev + uint32_t(alpha) - 1u) / uint32_t(alpha) * uint32_t(alpha);
+        const int end = min(ends[e], rows);
+        const int start = int(min(st, uint32_t(rows)));
+        const int count = max(end - start, 0);
+        s.start[e] = start;
+        s.count[e] = count;
+        mine += (count + height - 1) / height;
+    }
+    int sum = mine;
+    for (int d = 1; d < kWave; d *= 2) {
+        const int o = __shfl_up(sum, d);
+        if (lane >= d) sum += o;
+    }
+    int run = sum - mine;
+    for (int i = 0; i < per; ++i) {
+        const int e = lo + i;
+        if (e >= E) break;
+        s.first[e] = run;
+        run += (s.count[e] + height - 1) / height;
+    }
+    if (lane == kWave - 1) s.first[E] = sum;
+}
+
+// The expert of tile t (t below s.first[E]): the last one whose first tile is
+// at or before t (experts without tiles share their successor's).
+__device__ __forceinline__ int tile_expert(const Tiles &s, int E, int t)
+{
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (s.first[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Persistent workgroups: workgroup b runs on XCD b % 8, and each XCD takes a
+// contiguous eighth of the items, so that the column tiles of one row tile
+// find its rows (and the row tiles of one expert its weights) in one L2.
+struct Items {
+    int at, end, step;
+};
+__device__ __forceinline__ Items my_items(int total)
+{
+    const int nb = gridDim.x, b = blockIdx.x;   // nb is a multiple of 8
+    const int per = (total + 7) / 8, x = b & 7;
+    Items it;
+    it.at = x * per + (b >> 3);
+    it.end = min((x + 1) * per, total);
+    it.step = nb >> 3;
+    return it;
+}
+
+// --------------------------------------------------------------- product ----
+
+struct ProductArgs {
+    const uint8_t *x;
+    const uint8_t *w;
+    const float *xs, *ws;
+    const int32_t *ends, *tags;
+    const float *t;
+    const uint8_t *b;
+    void *out;
+    float *outs;
+    int rows, E, alpha;
+    int n;         // columns of out
+    int m;         // weight rows of an expert: n, or 2n gated
+    int kb;        // bytes of a row of x and of W
+    int nad, rank;
+    int ntiles;    // column tiles
+};
+
+// Column of the 16-row block q of G that a wavefront holds, A-operand row r:
+// D gives lane group r/4 the rows 4(r/4) .. + 3, so this order makes one lane's
+// G results 4G consecutive columns.
+template <int G>
+__device__ __forceinline__ int col_of(int q, int r)
+{
+    return (r >> 2) * (4 * G) + q * 4 + (r & 3);
+}
+
+// Adds B t of the row blocks' adapters to v[kind] (4 consecutive columns of one
+// row per lane).  wrow[kind] is the weight row of this lane's A-operand row.
+// Adapters are taken one after the other and each lane adds only its own row's,
+// by selection, so an adapter's infinities reach no other request.  t enters the
+// matrix unit as two bf16 parts, t - hi - lo below 2^-17 of t.
+template <int KINDS>
+__device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int row, int tag, const int (&wrow)[2],
+                                             f32x4 (&v)[2])
+{
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    uint32_t left = uint32_t(__ballot(tag >= 0)) & 0xFFFFu;
+    const gptr<const float> trow = (gptr<const float>)a.t + int64_t(row) * (KINDS * a.rank);
+    while (left) {
+        const int ad = __builtin_amdgcn_readlane(tag, __builtin_ctz(left));
+        const bool mine = tag == ad;
+        left &= ~uint32_t(__ballot(mine));
+        const gptr<const uint8_t> base = (gptr<const uint8_t>)a.b + (int64_t(ad) * a.E + e) * (int64_t(a.m) * a.rank * 2);
+#pragma unroll
+        for (int c = 0; c < KINDS; ++c) {
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+            for (int j0 = 0; j0 < a.rank; j0 += 32) {
+                const int j = j0 + g * 8;
+                u32x4 bf = {0u, 0u, 0u, 0u}, hi = bf, lo = bf;
+                if (j < a.rank) {
+                    bf = *(gptr<const u32x4>)(base + (int64_t(wrow[c]) * a.rank + j) * 2);
+                    const f32x4 t0 = *(gptr<const f32x4>)(trow + c * a.rank + j);
+                    const f32x4 t1 = *(gptr<const f32x4>)(trow + c * a.rank + j + 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p0 = i < 2 ? t0[2 * i] : t1[2 * i - 4], p1 = i < 2 ? t0[2 * i + 1] : t1[2 * i - 3];
+                        const uint32_t h0 = to_bf16(p0), h1 = to_bf16(p1);
+                        float r0 = p0 - __uint_as_float(h0 << 16), r1 = p1 - __uint_as_float(h1 << 16);
+                        if (!(fabsf(r0) < INFINITY)) r0 = 0.f;   // an infinite t has no remainder
+                        if (!(fabsf(r1) < INFINITY)) r1 = 0.f;
+                        hi[i] = h0 | (h1 << 16);
+                        lo[i] = pack_bf16(r0, r1);
+                    }
+                }
+                d = mfma_bf16(bf, lo, d);
+                d = mfma_bf16(bf, hi, d);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[c][i] = mine ? v[c][i] + d[i] : v[c][i];
+        }
+    }
+}
+
+// Products of few rows per expert: bound by reading every expert's weights
+// once.  A workgroup computes up to 16 MB rows by 16 NB weight rows; its KS
+// wavefronts split k (step u of 128 bytes goes to wavefront u % KS), so every
+// byte of W and x is loaded straight into the registers of the one wavefront that
+// uses it, with no staging and no barrier until the sums are joined in LDS.
+template <bool FP8, bool GATED, bool OUT8, int MB, int NB, int KS>
+__global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
+{
+    constexpr int G = GATED ? NB / 2 : NB;   // blocks of one kind
+    constexpr int BN = G * 16;               // columns of out per tile
+    __shared__ Tiles tiles;
+    __shared__ f32x4 red[KS][MB * NB][kWave];
+    __shared__ float amax[OUT8 ? KS : 1][MB][16];
+    const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave == 0) build_tiles(tiles, a.ends, a.E, a.alpha, a.rows, 16 * MB);
+    __syncthreads();
+    const int nu = a.kb / 128;               // steps of k (FP8: scale blocks)
+    for (Items it = my_items(tiles.first[a.E] * a.ntiles); it.at < it.end; it.at += it.step) {
+        const int tile = it.at / a.ntiles, c0 = (it.at - tile * a.ntiles) * BN;
+        const int e = tile_expert(tiles, a.E, tile);
+        const int done = (tile - tiles.first[e]) * (16 * MB);
+        const int row0 = tiles.start[e] + done, nrows = min(16 * MB, tiles.count[e] - done);
+        const gptr<const uint8_t> wb = (gptr<const uint8_t>)a.w + int64_t(e) * a.m * a.kb;
+        const gptr<const uint8_t> xb = (gptr<const uint8_t>)a.x + int64_t(row0) * a.kb;
+        uint32_t wo[NB], xo[MB];
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+            const int c = min(c0 + col_of<G>(q % G, r16), a.n - 1);
+            wo[q] = uint32_t((q < G ? c : a.n + c) * a.kb + g * 32);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) xo[i] = uint32_t(min(i * 16 + r16, nrows - 1)) * uint32_t(a.kb) + g * 32;
+        f32x4 acc[MB][NB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int q = 0; q < NB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const gptr<const float> wsp =
+            FP8 ? (gptr<const float>)a.ws + (int64_t(e) * ((a.m + 127) / 128) + c0 / 128) * nu : nullptr;
+        for (int u = wave; u < nu; u += KS) {
+            Frag wf[NB], xf[MB];
+#pragma unroll
+            for (int q = 0; q < NB; ++q)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) wf[q].p[p] = *(gptr<const u32x4>)(wb + wo[q] + u * 128 + p * 16);
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) xf[i].p[p] = *(gptr<const u32x4>)(xb + xo[i] + u * 128 + p * 16);
+            if constexpr (FP8) {
+                const float s0 = wsp[u], s1 = GATED ? wsp[(a.n / 128) * nu + u] : 0.f;
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    const float sx = ((gptr<const float>)a.xs)[int64_t(row0 + min(i * 16 + r16, nrows - 1)) * nu + u];
+#pragma unroll
+                    for (int q = 0; q < NB; ++q) {
+                        const f32x4 d = mfma_fp8(wf[q], xf[i], f32x4{0.f, 0.f, 0.f, 0.f});
+                        const float s = sx * (q < G ? s0 : s1);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][q][j] = fmaf(d[j], s, acc[i][q][j]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int q = 0; q < NB; ++q)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) acc[i][q] = mfma_bf16(wf[q].p[p], xf[i].p[p], acc[i][q]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int q = 0; q < NB; ++q) red[wave][i * NB + q][lane] = acc[i][q];
+        __syncthreads();
+        constexpr int kOwn = (MB * G + KS - 1) / KS;   // (row block, column block) pairs per wavefront
+        f32x4 res[kOwn];
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int idx = o * KS + wave, i = idx / G, q = idx - i * G;
+            if (idx < MB * G) {
+                f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const f32x4 p = red[s][i * NB + q][lane];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[0][j] += p[j];
+                    if (GATED) {
+                        const f32x4 p1 = red[s][i * NB + (GATED ? G : 0) + q][lane];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[1][j] += p1[j];
+                    }
+                }
+                const bool in = i * 16 + r16 < nrows;
+                const int row = row0 + min(i * 16 + r16, nrows - 1);
+                if (a.nad > 0) {
+                    int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
+                    if (tag >= a.nad) tag = -1;
+                    const int c = min(c0 + col_of<G>(q, r16), a.n - 1);
+                    const int wrow[2] = {c, a.n + c};
+                    add_adapters<GATED ? 2 : 1>(a, e, row, tag, wrow, v);
+                }
+                if (GATED)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[1][j];
+                const int c = c0 + g * (4 * G) + q * 4;
+                if constexpr (!OUT8) {
+                    if (in && c < a.n)
+                        *(gptr<u32x2>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + c) =
+                            u32x2{pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3])};
+                } else {
+                    res[o] = v[0];
+                }
+            }
+        }
+        if constexpr (OUT8) {
+            // one scale per row and tile (a tile is one 128-column block); a
+            // wavefront's pairs are of one row block each, KS of them per G / KS
+            static_assert(BN == 128 && G % KS == 0, "a tile is one scale block");
+            constexpr int per = G / KS;   // pairs of one row block per wavefront
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                float m = 0.f;
+#pragma unroll
+                for (int p = 0; p < per; ++p)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(res[i * per + p][j]));
+                m = fmaxf(m, __shfl_xor(m, 16));
+                m = fmaxf(m, __shfl_xor(m, 32));
+                if (g == 0) amax[wave][i][r16] = m;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                float m = 0.f;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) m = fmaxf(m, amax[s][i][r16]);
+                const float sc = m / 448.0f;
+                const bool in = i * 16 + r16 < nrows;
+                const int64_t row = row0 + i * 16 + r16;
+                if (in && wave == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
+#pragma unroll
+                for (int p = 0; p < per; ++p) {
+                    const int q = p * KS + wave, c = c0 + g * (4 * G) + q * 4;
+                    float d[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? res[i * per + p][j] / sc : 0.f;
+                    int code = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
+                    code = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], code, true);
+                    if (in) *(gptr<int>)((gptr<uint8_t>)a.out + row * a.n + c) = code;
+                }
+            }
+        }
+        __syncthreads();   // the next item writes red and amax again
+    }
+}
+
+// -------------------------------------------------------------- adapters ----
+
+struct ShrinkArgs {
+    const uint8_t *x;
+    const float *xs;
+    const int32_t *ends, *tags;
+    const uint8_t *a;
+    const float *scaling;
+    float *t;
+    int rows, E, alpha;
+    int k;
+    int c;       // rank rows of one adapter's A: rank, or 2 rank gated
+    int nad;
+    int split;   // items per row block: item y takes the block's distinct adapters y, y + split, ..
+};
+
+// Eight E4M3 codes to bf16 (exact: four significant bits).
+__device__ __forceinline__ u32x4 fp8_to_bf16(u32x2 q)
+{
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(q[i]), false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(q[i]), true);
+        r[2 * i] = (__float_as_uint(lo[0]) >> 16) | (__float_as_uint(lo[1]) & 0xFFFF0000u);
+        r[2 * i + 1] = (__float_as_uint(hi[0]) >> 16) | (__float_as_uint(hi[1]) & 0xFFFF0000u);
+    }
+    return r;
+}
+
+// t[r, :] = scaling[a] A[a, j] x[r] for every row r with an adapter a.  An item is
+// 16 rows of one expert; the distinct adapters among them are taken one after
+// the other, the A operand holding rows of A and the B operand the 16 rows of x,
+// and each lane stores the columns of its own row's adapter.  The workgroup's
+// KS wavefronts split k and join their sums in LDS.  Bound by reading A.
+template <bool FP8, int KS>
+__global__ __launch_bounds__(KS * kWave) void k_shrink(ShrinkArgs a)
+{
+    constexpr int kStep = FP8 ? 128 : 64;   // columns of a step
+    __shared__ Tiles tiles;
+    __shared__ f32x4 red[2][KS][kWave];
+    const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave == 0) build_tiles(tiles, a.ends, a.E, a.alpha, a.rows, 16);
+    __syncthreads();
+    const int nu = a.k / kStep;
+    int buf = 0;
+    for (Items it = my_items(tiles.first[a.E] * a.split); it.at < it.end; it.at += it.step) {
+        const int tile = it.at / a.split, y = it.at - tile * a.split;
+        const int e = tile_expert(tiles, a.E, tile);
+        const int done = (tile - tiles.first[e]) * 16;
+        const int row0 = tiles.start[e] + done, nrows = min(16, tiles.count[e] - done);
+        const int row = row0 + min(r16, nrows - 1);
+        int tag = r16 < nrows ? ((gptr<const int32_t>)a.tags)[row] : -1;
+        if (tag >= a.nad) tag = -1;
+        uint32_t left = uint32_t(__ballot(tag >= 0)) & 0xFFFFu;
+        const gptr<const uint8_t> xp = (gptr<const uint8_t>)a.x + int64_t(row) * a.k * (FP8 ? 1 : 2);
+        const gptr<const float> sp = FP8 ? (gptr<const float>)a.xs + int64_t(row) * nu : nullptr;
+        for (int d = 0; left; ++d) {
+            const int ad = __builtin_amdgcn_readlane(tag, __builtin_ctz(left));
+            const bool mine = tag == ad;
+            left &= ~uint32_t(__ballot(mine));
+            if (d % a.split != y) continue;
+            const gptr<const uint8_t> ab = (gptr<const uint8_t>)a.a + (int64_t(ad) * a.E + e) * (int64_t(a.c) * a.k * 2);
+            for (int c0 = 0; c0 < a.c; c0 += 16) {
+                const gptr<const uint8_t> ap = ab + int64_t(min(c0 + r16, a.c - 1)) * a.k * 2;
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                for (int u = wave; u < nu; u += KS) {
+                    if constexpr (FP8) {
+                        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const int col = u * 128 + p * 32 + g * 8;
+                            s = mfma_bf16(*(gptr<const u32x4>)(ap + col * 2), fp8_to_bf16(*(gptr<const u32x2>)(xp + col)), s);
+                        }
+                        const float f = sp[u];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[j] = fmaf(s[j], f, acc[j]);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const int col = u * 64 + p * 32 + g * 8;
+                            acc = mfma_bf16(*(gptr<const u32x4>)(ap + col * 2), *(gptr<const u32x4>)(xp + col * 2), acc);
+                        }
+                    }
+                }
+                red[buf][wave][lane] = acc;
+                __syncthreads();   // two buffers: one barrier separates the writes of a buffer from its last reads
+                if (wave == 0) {
+                    f32x4 v = red[buf][0][lane];
+#pragma unroll
+                    for (int s = 1; s < KS; ++s)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] += red[buf][s][lane][j];
+                    const int c = c0 + g * 4;
+                    if (mine && c < a.c) {
+                        const float f = ((gptr<const float>)a.scaling)[ad];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] *= f;
+                        *(gptr<f32x4>)((gptr<float>)a.t + int64_t(row) * a.c + c) = v;
+                    }
+                }
+                buf ^= 1;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ tags ----
+
+struct TagArgs {
+    const int32_t *slot;   // [ntok][K] {part << 24 | row, weight bits}, -1 skipped
+    int32_t *out;
+    const int32_t *tags[kMaxSources];
+    int off[kMaxSources + 1];
+    int n;                 // ntok * K
+    int K, N, f;
+};
+
+// One thread per choice: bound by one dependent pair of loads.
+__global__ __launch_bounds__(256) void k_tags(TagArgs a)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.n) return;
+    const int sl = a.slot[2 * int64_t(i)];
+    if (sl < 0 || (sl >> 24) != a.f) return;
+    const int g = i / a.K;
+    const int32_t *p = a.tags[0] + g;
+    for (int s = 1; s < a.N; ++s)
+        if (g >= a.off[s]) p = a.tags[s] + (g - a.off[s]);
+    a.out[sl & 0xFFFFFF] = *p;
+}
+
+int launched() { return hipGetLastError() == hipSuccess ? 0 : 1; }
+
+// Workgroups of a persistent launch: one per item, at most `most`, a multiple
+// of 8 (my_items).  The host knows only the bound of the items: every expert can
+// end inside a tile.
+unsigned persistent_grid(int64_t tiles, int64_t per_tile, int most)
+{
+    const int64_t items = (tiles * per_tile + 7) / 8 * 8;
+    return unsigned(items < most ? items : most);
+}
+int64_t tile_bound(const ProductPlan &p, int height)
+{
+    const int64_t t = p.E + p.rows / height;
+    return t < p.rows ? t : p.rows;
+}
+
+constexpr int kComputeUnits = 256;
+
+template <bool FP8, bool GATED, bool OUT8, int MB, int NB, int KS>
+void launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
+{
+    constexpr int BN = (GATED ? NB / 2 : NB) * 16;
+    a.ntiles = (p.n + BN - 1) / BN;
+    const unsigned grid = persistent_grid(tile_bound(p, 16 * MB), a.ntiles, kComputeUnits * 4);
+    hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, MB, NB, KS>), dim3(grid), dim3(KS * kWave), 0, st, a);
+}
+
+}  // namespace
+
+int be_launch_product(const ProductPlan &p, void *stream)
+{
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (p.nad > 0) {
+        ShrinkArgs s{};
+        s.x = static_cast<const uint8_t *>(p.x);
+        s.xs = p.xs;
+        s.ends = p.ends;
+        s.tags = p.tags;
+        s.a = static_cast<const uint8_t *>(p.w.a);
+        s.scaling = p.w.scaling;
+        s.t = p.t;
+        s.rows = int(p.rows);
+        s.E = p.E;
+        s.alpha = p.alpha;
+        s.k = p.k;
+        s.c = p.rank * (p.gated ? 2 : 1);
+        s.nad = p.nad;
+        s.split = 4;
+        const unsigned grid = persistent_grid(tile_bound(p, 16), s.split, kComputeUnits * 4);
+        if (p.fp8) hipLaunchKernelGGL((k_shrink<true, 8>), dim3(grid), dim3(512), 0, st, s);
+        else hipLaunchKernelGGL((k_shrink<false, 8>), dim3(grid), dim3(512), 0, st, s);
+        if (launched() != 0) return 1;
+    }
+    ProductArgs a{};
+    a.x = static_cast<const uint8_t *>(p.x);
+    a.w = static_cast<const uint8_t *>(p.w.w);
+    a.xs = p.xs;
+    a.ws = p.w.w_scales;
+    a.ends = p.ends;
+    a.tags = p.tags;
+    a.t = p.t;
+    a.b = static_cast<const uint8_t *>(p.w.b);
+    a.out = p.out;
+    a.outs = p.outs;
+    a.rows = int(p.rows);
+    a.E = p.E;
+    a.alpha = p.alpha;
+    a.n = p.n;
+    a.m = p.n * (p.gated ? 2 : 1);
+    a.kb = p.k * (p.fp8 ? 1 : 2);
+    a.nad = p.nad;
+    a.rank = p.rank;
+    if (!p.fp8) {
+        if (p.gated) launch_few<false, true, false, 1, 4, 8>(p, a, st);
+        else launch_few<false, false, false, 1, 4, 8>(p, a, st);
+    } else if (p.out8) {
+        launch_few<true, true, true, 1, 16, 4>(p, a, st);
+    } else {
+        if (p.gated) launch_few<true, true, false, 1, 4, 8>(p, a, st);
+        else launch_few<true, false, false, 1, 4, 8>(p, a, st);
+    }
+    return launched();
+}
+
+int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *tags, int32_t *out, void *stream)
+{
+    TagArgs a{};
+    a.slot = p.slot;
+    a.out = out;
+    for (int s = 0; s < p.N; ++s) {
+        a.tags[s] = tags[s];
+        a.off[s] = p.tok_off[s];
+    }
+    a.n = p.ntok * p.K;
+    a.K = p.K;
+    a.N = p.N;
+    a.f = f;
+    hipLaunchKernelGGL(k_tags, dim3(unsigned((a.n + 255) / 256)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+    return launched();
+}
+
+}  // namespace afd

@@ -181,6 +181,23 @@ inline int layout_tiles(const RoundPlan &p, TileRec *out)
     return p.nblk;
 }
 
+// One grouped product (and its adapters' first halves); pointers are device
+// addresses recorded from the caller.
+struct ProductPlan {
+    int E = 0, alpha = 1, k = 0, n = 0;
+    bool fp8 = false, out8 = false, gated = false;
+    int nad = 0, rank = 0;           // adapters (0: none) and their rank
+    int64_t rows = 0;
+    const void *x = nullptr;
+    const float *xs = nullptr;
+    const int32_t *ends = nullptr;
+    const int32_t *tags = nullptr;   // [rows] adapter of every row
+    afd_product_weights w{};
+    void *out = nullptr;
+    float *outs = nullptr;
+    float *t = nullptr;              // [rows][(gated ? 2 : 1) * rank] scaling * A x of every row
+};
+
 // Contexts made by afd_create_static use a static scratch array of this many
 // bytes per GPU as their workspace (one such context per device at a time).
 constexpr size_t kStaticScratchBytes = size_t(AFD_STATIC_SCRATCH_BYTES);
@@ -199,6 +216,10 @@ int be_launch_copy(const void *src, void *dst, int64_t bytes, void *stream);
 int be_read_error(uint64_t *dev_err, void *stream, int clear, uint64_t *word);
 // The one-launch dispatch's gave-up flag (and clears it when asked).
 int be_read_stall(uint32_t *dev_sync, void *stream, int clear, int *stalled);
+// A grouped product: with adapters a launch for A x, then the product.
+int be_launch_product(const ProductPlan &p, void *stream);
+// tags[s][t] to the receive rows of partition f, from the round's slot map.
+int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *tags, int32_t *out, void *stream);
 int be_device_sync();
 // The current device and the address of its static scratch array (found
 // once per device); no allocation.

@@ -1,0 +1,201 @@
+"""Python binding of the experts' side of a round: products grouped by expert,
+the experts' network, and low-rank adapters beside their projections.
+
+Argument checks and marshalling only: the arithmetic runs in the HIP library.
+Rows are laid out as ``Buffer.worker_receive`` hands them out: expert j owns
+rows [align_up(ends[j-1], alignment), ends[j]).  Rows inside no expert's range
+are neither read nor written.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import functools
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _native as nat
+
+SCALE_BLOCK = 128
+
+
+class LowRank(NamedTuple):
+    """One projection's adapters: scaling[i] * B_ij (A_ij x) beside expert j's.
+    For a gated projection A holds the gate's rank rows, then the up's."""
+    a: torch.Tensor        # [S, E, rank or 2*rank, k] bf16
+    b: torch.Tensor        # [S, E, rows of the weight, rank] bf16
+    scaling: torch.Tensor  # [S] float32
+
+
+class Experts(NamedTuple):
+    """Weights of a partition's experts, bf16, or float8_e4m3fn with float32
+    scales per 128 x 128 block."""
+    up: torch.Tensor                           # [E, 2*inner, hidden]: gate rows, then up rows
+    down: torch.Tensor                         # [E, hidden, inner]
+    up_scales: Optional[torch.Tensor] = None   # [E, 2*inner/128, hidden/128]
+    down_scales: Optional[torch.Tensor] = None  # [E, hidden/128, inner/128]
+
+
+class ExpertAdapters(NamedTuple):
+    up: LowRank
+    down: LowRank
+
+
+def on_device(device):
+    """The current device for a launch, changed only where it differs."""
+    return contextlib.nullcontext() if device.index in (None, torch.cuda.current_device()) else torch.cuda.device(device)
+
+
+@functools.lru_cache(maxsize=256)
+def _product_plan(rows, *cfg):
+    c, ws = nat.ProductConfig(*cfg), ctypes.c_size_t(0)
+    nat.check(nat.load().afd_product_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_product")
+    return c, ws.value
+
+
+@functools.lru_cache(maxsize=256)
+def _ffn_plan(rows, *cfg):
+    c, ws = nat.FfnConfig(*cfg), ctypes.c_size_t(0)
+    nat.check(nat.load().afd_ffn_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_ffn")
+    return c, ws.value
+
+
+def _want(t, what, dtype, shape, device):
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}, got " + (
+            "None" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}"))
+    return t.data_ptr()
+
+
+def _act_dtype(x):
+    """(dtype code, torch dtype) of activations and weights."""
+    if x.dtype is torch.bfloat16:
+        return nat.AFD_BF16, torch.bfloat16
+    if x.dtype is torch.float8_e4m3fn:
+        return nat.AFD_FP8_E4M3, torch.float8_e4m3fn
+    raise TypeError("x must be bfloat16 or float8_e4m3fn")
+
+
+def _weights(what, w, scales, low, E, m, k, code, dtype, gated, device):
+    """The checked pointers of one product's weights."""
+    p = nat.ProductWeights()
+    p.w = _want(w, f"{what} weight", dtype, (E, m, k), device)
+    if code == nat.AFD_FP8_E4M3:
+        p.w_scales = _want(scales, f"{what} weight scales", torch.float32, (E, -(-m // SCALE_BLOCK), k // SCALE_BLOCK),
+                           device)
+    elif scales is not None:
+        raise ValueError("weight scales belong to float8_e4m3fn weights")
+    if low is not None:
+        S, rank = low.scaling.shape[0], low.b.shape[-1]
+        p.a = _want(low.a, f"{what} adapters' A", torch.bfloat16, (S, E, rank * (2 if gated else 1), k), device)
+        p.b = _want(low.b, f"{what} adapters' B", torch.bfloat16, (S, E, m, rank), device)
+        p.scaling = _want(low.scaling, f"{what} adapters' scaling", torch.float32, (S,), device)
+    return p
+
+
+def _rows(x, ends, x_scales, code, adapters, row_adapters, device):
+    """The checked pointers of ends, the row scales and the rows' adapters."""
+    R, k = x.shape
+    pe = _want(ends, "ends", torch.int32, (ends.shape[0],), device)
+    ps = pa = None
+    if code == nat.AFD_FP8_E4M3:
+        ps = _want(x_scales, "x_scales", torch.float32, (R, k // SCALE_BLOCK), device)
+    elif x_scales is not None:
+        raise ValueError("x_scales belong to float8_e4m3fn rows")
+    if adapters is not None:
+        pa = _want(row_adapters, "row_adapters", torch.int32, (R,), device)
+    elif row_adapters is not None:
+        raise ValueError("row_adapters without adapters")
+    return pe, ps, pa
+
+
+def _x(x):
+    if x.dim() != 2 or not x.is_contiguous() or x.device.type != "cuda":
+        raise ValueError("x must be a contiguous [rows, k] tensor on a GPU")
+    return x.device
+
+
+def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales=None, activation=None, adapters=None,
+                   row_adapters=None, out=None, out_scales=None):
+    """out[r] = act(x[r] W_j^T) for the rows r of expert j, [rows, n] bf16.
+
+    x [rows, k] bf16, or float8_e4m3fn with x_scales float32 [rows, k/128];
+    weight [E, m, k] of the same type (float8: weight_scales float32
+    [E, ceil(m/128), k/128]); activation None (n = m) or "swiglu" (m = 2n, gate
+    rows first).  k is a multiple of 64 (bf16) or 128, n of 16 (float8 swiglu:
+    128).  adapters: a LowRank, with row_adapters int32 [rows] naming each
+    row's (any value outside [0, S): none); rank a multiple of 8 up to 128.
+    A float8 swiglu product writes float8 rows when `out` is a float8_e4m3fn
+    tensor, with their scales in out_scales float32 [rows, n/128].
+    Without `out` the result is new memory, its padding rows undefined.
+    """
+    dev = _x(x)
+    R, k = x.shape
+    code, dtype = _act_dtype(x)
+    if activation not in nat.ACTIVATIONS:
+        raise ValueError('activation must be None or "swiglu"')
+    gated = activation == "swiglu"
+    if weight.dim() != 3 or gated and weight.shape[1] % 2:
+        raise ValueError("weight must be [E, m, k], m even with swiglu")
+    E, m, _ = weight.shape
+    n = m // 2 if gated else m
+    if ends.dim() != 1 or ends.shape[0] != E:
+        raise ValueError("ends must be int32 [E]")
+    pe, ps, pa = _rows(x, ends, x_scales, code, adapters, row_adapters, dev)
+    w = _weights("the", weight, weight_scales, adapters, E, m, k, code, dtype, gated, dev)
+    out8 = out is not None and out.dtype is torch.float8_e4m3fn
+    S, rank = (adapters.scaling.shape[0], adapters.b.shape[-1]) if adapters is not None else (0, 0)
+    cfg, need = _product_plan(R, E, alignment, k, n, code, nat.AFD_FP8_E4M3 if out8 else nat.AFD_BF16,
+                              nat.ACTIVATIONS[activation], S, rank)
+    if out is None:
+        out = torch.empty((R, n), dtype=torch.bfloat16, device=dev)
+    po = _want(out, "out", torch.float8_e4m3fn if out8 else torch.bfloat16, (R, n), dev)
+    pos = None
+    if out8:
+        pos = _want(out_scales, "out_scales", torch.float32, (R, n // SCALE_BLOCK), dev)
+    elif out_scales is not None:
+        raise ValueError("out_scales belong to a float8_e4m3fn out")
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    with on_device(dev):
+        st = nat.load().afd_expert_product(cfg, R, x.data_ptr(), ps, pe, pa, w, po, pos,
+                                           ws.data_ptr() if need else None, need,
+                                           torch.cuda.current_stream(dev).cuda_stream)
+    nat.check(st, "expert_product")
+    return out
+
+
+def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapters: Optional[ExpertAdapters] = None,
+               row_adapters=None, out=None):
+    """The experts' network, swiglu(x Wup^T) Wdown^T per expert, [rows, hidden]
+    bf16.  Arguments as expert_product; the hidden layer is rounded to the
+    rows' own format (bf16, or float8_e4m3fn with a scale per row and 128
+    columns).  adapters: pairs beside both projections, of one rank and number.
+    """
+    dev = _x(x)
+    R, hidden = x.shape
+    code, dtype = _act_dtype(x)
+    if experts.up.dim() != 3 or experts.up.shape[1] % 2:
+        raise ValueError("up must be [E, 2*inner, hidden]")
+    E, inner = experts.up.shape[0], experts.up.shape[1] // 2
+    if ends.dim() != 1 or ends.shape[0] != E:
+        raise ValueError("ends must be int32 [E]")
+    pe, ps, pa = _rows(x, ends, x_scales, code, adapters, row_adapters, dev)
+    S = rank = 0
+    if adapters is not None:
+        S, rank = adapters.up.scaling.shape[0], adapters.up.b.shape[-1]
+        if adapters.down.scaling.shape[0] != S or adapters.down.b.shape[-1] != rank:
+            raise ValueError("both projections' adapters must have one number and rank")
+    lu, ld = (adapters.up, adapters.down) if adapters is not None else (None, None)
+    wu = _weights("up", experts.up, experts.up_scales, lu, E, 2 * inner, hidden, code, dtype, True, dev)
+    wd = _weights("down", experts.down, experts.down_scales, ld, E, hidden, inner, code, dtype, False, dev)
+    cfg, need = _ffn_plan(R, E, alignment, hidden, inner, code, S, rank)
+    if out is None:
+        out = torch.empty((R, hidden), dtype=torch.bfloat16, device=dev)
+    po = _want(out, "out", torch.bfloat16, (R, hidden), dev)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    with on_device(dev):
+        st = nat.load().afd_expert_ffn(cfg, R, x.data_ptr(), ps, pe, pa, wu, wd, po, ws.data_ptr() if need else None, need,
+                                       torch.cuda.current_stream(dev).cuda_stream)
+    nat.check(st, "expert_ffn")
+    return out

@@ -393,6 +393,145 @@ typedef struct {
  */
 afd_status afd_get_round_info(const afd_ctx *ctx, afd_round_info *info);
 
+/*
+ * ---- the experts' side of a round -----------------------------------------
+ *
+ * Between a partition's receive and its reply stands the experts' arithmetic.
+ * These calls compute it on expert-major rows as afd_worker_receive hands
+ * them out, or on any rows laid out the same: expert j owns rows
+ * [align_up(ends[j-1], alignment), ends[j]), ends[-1] = 0.  The GPU reads
+ * ends[]; the host needs no counts.  They take no context, keep no state,
+ * enqueue on `stream` (of the current device) and may run at the same time
+ * on several streams with different workspaces.  Rows inside no expert's
+ * range are neither read nor written; ends[] beyond `rows` is cut there.
+ * They are forward calls: a round has no gradients.
+ */
+
+/* What a product does with its sums. */
+typedef enum {
+    AFD_ACT_NONE = 0,   /* y = x W^T */
+    AFD_ACT_SWIGLU = 1  /* W holds n gate rows, then n up rows: y = g / (1 + exp(-g)) * u */
+} afd_activation;
+
+#define AFD_MAX_ADAPTERS 65536
+#define AFD_MAX_RANK 128
+
+/*
+ * A product grouped by expert, out[r,:] = act(x[r,:] W_j^T) for the rows r of
+ * expert j.
+ *   num_experts   experts of the partition, 1..AFD_MAX_EXPERTS
+ *   alignment     alpha of the rows' layout, >= 1
+ *   k             columns of x: a positive multiple of 64 (BF16) or 128 (FP8)
+ *   n             columns of out: a positive multiple of 16; of 128 for an FP8
+ *                 product with AFD_ACT_SWIGLU
+ *   dtype         of x and W: BF16, or E4M3 with FP32 scales, x per row and 128
+ *                 columns, W per 128 x 128 block
+ *   out_dtype     AFD_BF16; AFD_FP8_E4M3 only for an FP8 product with
+ *                 AFD_ACT_SWIGLU: per row and 128 columns scale = amax / 448
+ *                 and code = e4m3(v / scale) to nearest even; an all-zero
+ *                 block has scale 0 and codes 0
+ *   activation    afd_activation
+ *   num_adapters  0, or the number of adapters, at most AFD_MAX_ADAPTERS
+ *   rank          of every adapter, a multiple of 8 up to AFD_MAX_RANK (smaller
+ *                 ones are padded with zero rows of A); 0 without adapters
+ * One expert's W may hold at most 2^31 - 1 bytes; rows is below 2^24.  Sums
+ * are float32; a BF16 output is rounded once.
+ */
+typedef struct {
+    int32_t num_experts;
+    int32_t alignment;
+    int32_t k;
+    int32_t n;
+    int32_t dtype;      /* afd_dtype */
+    int32_t out_dtype;  /* afd_dtype */
+    int32_t activation; /* afd_activation */
+    int32_t num_adapters;
+    int32_t rank;
+} afd_product_config;
+
+/*
+ * A product's weights, all device memory (16-byte aligned; scales and scaling
+ * 4-byte aligned).  m = n, or 2n with AFD_ACT_SWIGLU; c = 1, or 2.
+ *   w         [num_experts, m, k]
+ *   w_scales  [num_experts, ceil(m/128), k/128] FP32 (FP8, else NULL)
+ *   a         [num_adapters, num_experts, c*rank, k] BF16: A of the gate, then of the up rows
+ *   b         [num_adapters, num_experts, m, rank] BF16
+ *   scaling   [num_adapters] FP32
+ * A row r of expert j with adapter i = row_adapters[r] in [0, num_adapters)
+ * adds scaling[i] * B_ij (A_ij x[r]) to its sums before the activation (with
+ * SwiGLU the gate rows of B take the gate's A, the up rows the up's); a row
+ * with any other value has no adapter.  An adapter reaches no row but its own.
+ */
+typedef struct {
+    const void *w;
+    const float *w_scales;
+    const void *a;
+    const void *b;
+    const float *scaling;
+} afd_product_weights;
+
+/* afd_product_query: workspace bytes of afd_expert_product (0 without
+ * adapters).  Pure host computation.  Errors: AFD_E_ARG (NULL, rows outside
+ * [0, 2^24)), AFD_E_SHAPE. */
+afd_status afd_product_query(const afd_product_config *cfg, int64_t rows, size_t *workspace_bytes);
+
+/*
+ * afd_expert_product: one grouped product.
+ *   rows          rows of x and out (afd_receive.receive_rows); 0 does nothing
+ *   x, x_scales   device [rows, k]; [rows, k/128] FP32 (FP8, else NULL)
+ *   ends          device [num_experts]
+ *   row_adapters  device [rows] (with adapters, else NULL; see afd_worker_tags)
+ *   out           device [rows, n], not overlapping the inputs
+ *   out_scales    device [rows, n/128] FP32 (FP8 output, else NULL)
+ *   workspace     device, at least afd_product_query bytes, 256-byte aligned;
+ *                 in use until the call's work has run
+ * Errors: AFD_E_ARG (pointers, alignment), AFD_E_SHAPE, AFD_E_CAPACITY
+ * (workspace), AFD_E_HIP.
+ */
+afd_status afd_expert_product(const afd_product_config *cfg, int64_t rows, const void *x, const float *x_scales,
+                              const int32_t *ends, const int32_t *row_adapters, const afd_product_weights *weights,
+                              void *out, float *out_scales, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The experts' network: h = swiglu(x Wup^T) [rows, inner], out = h Wdown^T
+ * [rows, hidden] BF16, each product as above, both with the adapters' pairs
+ * when num_adapters > 0.  h is kept in the workspace in the rows' format:
+ * BF16, or E4M3 with scales.  hidden and inner are positive multiples of 64
+ * (BF16) or 128 (FP8).
+ */
+typedef struct {
+    int32_t num_experts;
+    int32_t alignment;
+    int32_t hidden;
+    int32_t inner;
+    int32_t dtype; /* afd_dtype of x and the weights */
+    int32_t num_adapters;
+    int32_t rank;
+} afd_ffn_config;
+
+/* afd_ffn_query: workspace bytes of afd_expert_ffn; errors as afd_product_query. */
+afd_status afd_ffn_query(const afd_ffn_config *cfg, int64_t rows, size_t *workspace_bytes);
+
+/* afd_expert_ffn: arguments and errors as afd_expert_product; out is a whole
+ * reply for afd_worker_reply. */
+afd_status afd_expert_ffn(const afd_ffn_config *cfg, int64_t rows, const void *x, const float *x_scales,
+                          const int32_t *ends, const int32_t *row_adapters, const afd_product_weights *up,
+                          const afd_product_weights *down, void *out, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * afd_worker_tags: carry one int32 of every token (its request's adapter) to
+ * the receive rows of partition f: out[row] = tags[s][t] for every live
+ * choice of token t of source s in f.  Between the partition's
+ * afd_worker_receive and its reply; rows of no choice keep what they held.
+ *   tags  host array of num_sources device pointers, [T_s] each (NULL where T_s = 0)
+ *   out   device [receive_rows]
+ * Enqueued on `stream`, which has to be ordered after the receive's.
+ * Errors: AFD_E_ARG, AFD_E_ORDER, AFD_E_SHAPE (receive_rows), AFD_E_HIP.
+ */
+afd_status afd_worker_tags(afd_ctx *ctx, int32_t f, const int32_t *const *tags, int32_t *out, int64_t receive_rows,
+                           const afd_receipt *receipt, void *stream);
+
 /* afd_status_string: a static description of a status. */
 const char *afd_status_string(afd_status st);
 

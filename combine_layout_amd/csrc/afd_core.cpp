@@ -270,9 +270,10 @@ afd_status check_product(const afd_product_config *c, int64_t rows)
     if (c->activation != AFD_ACT_NONE && c->activation != AFD_ACT_SWIGLU) return AFD_E_SHAPE;
     const bool fp8 = c->dtype == AFD_FP8_E4M3, gated = c->activation == AFD_ACT_SWIGLU;
     if (c->out_dtype != AFD_BF16 && !(c->out_dtype == AFD_FP8_E4M3 && fp8 && gated)) return AFD_E_SHAPE;
-    if (c->k < 1 || c->k % (fp8 ? 128 : 64) != 0) return AFD_E_SHAPE;
+    if (c->k < 1 || c->k > (1 << 21) || c->k % (fp8 ? 128 : 64) != 0) return AFD_E_SHAPE;
     if (c->n < 1 || c->n % (fp8 && gated ? 128 : 16) != 0) return AFD_E_SHAPE;
-    // byte offsets inside one expert's weights are 32-bit in the kernels
+    // byte offsets inside one expert's weights, and inside 256 rows of x, are
+    // 32-bit in the kernels
     if (int64_t(c->n) * (gated ? 2 : 1) * c->k * (fp8 ? 1 : 2) >= (int64_t(1) << 31)) return AFD_E_SHAPE;
     if (c->num_adapters < 0 || c->num_adapters > AFD_MAX_ADAPTERS) return AFD_E_SHAPE;
     if (c->num_adapters == 0 ? c->rank != 0 : c->rank < 8 || c->rank > AFD_MAX_RANK || c->rank % 8 != 0)

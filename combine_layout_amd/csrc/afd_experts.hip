@@ -33,6 +33,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 template <typename T>
 using gptr = __attribute__((address_space(1))) T *;
+template <typename T>
+using lptr = __attribute__((address_space(3))) T *;
 
 // One lane's operand of a 128-byte step of k: two 16-byte pieces (two bf16
 // products of 32 columns, or one E4M3 product of 128).  Both operands hold the
@@ -68,14 +70,29 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g));
 
 // The experts' rows as tiles, built by every workgroup in LDS from ends[]
 // (512 experts at most: a few hundred bytes read, one wavefront's prefix sum).
+// An expert's rows are split into as few tiles of at most MAX rows as hold
+// them, of even heights in steps of STEP: 260 rows are two tiles of 160 and
+// 100 rows, not of 256 and 4.
 struct Tiles {
     int first[kMaxExperts + 1];   // tiles before expert e
     int start[kMaxExperts];       // first row
     int count[kMaxExperts];       // rows
 };
 
+struct Tile {
+    int e, row0, nrows;
+};
+
+template <int MAX, int STEP>
+__device__ __forceinline__ int tile_height(int count)
+{
+    const int n = (count + MAX - 1) / MAX;
+    return n <= 1 ? MAX : ((count + n - 1) / n + STEP - 1) / STEP * STEP;
+}
+
 // Wavefront 0 of the workgroup; the caller places a barrier behind it.
-__device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int rows, int height)
+template <int MAX>
+__device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int rows)
 {
     const int lane = threadIdx.x;
     const int per = (E + kWave - 1) / kWave, lo = lane * per;
@@ -90,7 +107,7 @@ __device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int
         const int count = max(end - start, 0);
         s.start[e] = start;
         s.count[e] = count;
-        mine += (count + height - 1) / height;
+        mine += (count + MAX - 1) / MAX;
     }
     int sum = mine;
     for (int d = 1; d < kWave; d *= 2) {
@@ -102,14 +119,15 @@ __device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int
         const int e = lo + i;
         if (e >= E) break;
         s.first[e] = run;
-        run += (s.count[e] + height - 1) / height;
+        run += (s.count[e] + MAX - 1) / MAX;
     }
     if (lane == kWave - 1) s.first[E] = sum;
 }
 
-// The expert of tile t (t below s.first[E]): the last one whose first tile is
+// Tile t (t below s.first[E]) and its expert: the last one whose first tile is
 // at or before t (experts without tiles share their successor's).
-__device__ __forceinline__ int tile_expert(const Tiles &s, int E, int t)
+template <int MAX, int STEP>
+__device__ __forceinline__ Tile find_tile(const Tiles &s, int E, int t)
 {
     int lo = 0, hi = E;
     while (hi - lo > 1) {
@@ -117,7 +135,12 @@ __device__ __forceinline__ int tile_expert(const Tiles &s, int E, int t)
         if (s.first[mid] <= t) lo = mid;
         else hi = mid;
     }
-    return __builtin_amdgcn_readfirstlane(lo);
+    const int count = s.count[lo], h = tile_height<MAX, STEP>(count), done = (t - s.first[lo]) * h;
+    Tile r;
+    r.e = __builtin_amdgcn_readfirstlane(lo);
+    r.row0 = __builtin_amdgcn_readfirstlane(s.start[lo] + done);
+    r.nrows = __builtin_amdgcn_readfirstlane(min(h, count - done));
+    return r;
 }
 
 // Persistent workgroups: workgroup b runs on XCD b % 8, and each XCD takes a
@@ -126,8 +149,9 @@ __device__ __forceinline__ int tile_expert(const Tiles &s, int E, int t)
 struct Items {
     int at, end, step;
 };
-__device__ __forceinline__ Items my_items(int total)
+__device__ __forceinline__ Items my_items(int total_)
 {
+    const int total = __builtin_amdgcn_readfirstlane(total_);   // read from LDS: the same in every lane
     const int nb = gridDim.x, b = blockIdx.x;   // nb is a multiple of 8
     const int per = (total + 7) / 8, x = b & 7;
     Items it;
@@ -165,14 +189,14 @@ __device__ __forceinline__ int col_of(int q, int r)
     return (r >> 2) * (4 * G) + q * 4 + (r & 3);
 }
 
-// Adds B t of the row blocks' adapters to v[kind] (4 consecutive columns of one
-// row per lane).  wrow[kind] is the weight row of this lane's A-operand row.
-// Adapters are taken one after the other and each lane adds only its own row's,
-// by selection, so an adapter's infinities reach no other request.  t enters the
-// matrix unit as two bf16 parts, t - hi - lo below 2^-17 of t.
-template <int KINDS>
-__device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int row, int tag, const int (&wrow)[2],
-                                             f32x4 (&v)[2])
+// Adds B t of a row block's adapters to v: NQ blocks per kind of 4 consecutive
+// columns of one row per lane.  wrow[] are the weight rows of this lane's
+// A-operand rows.  Adapters are taken one after the other and each lane adds only
+// its own row's, by selection, so an adapter's infinities reach no other request.
+// t enters the matrix unit as two bf16 parts, t - hi - lo below 2^-16 of t.
+template <int KINDS, int NQ>
+__device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int row, int tag, const int (&wrow)[KINDS * NQ],
+                                             f32x4 (&v)[KINDS * NQ])
 {
     const int lane = threadIdx.x & 63, g = lane >> 4;
     uint32_t left = uint32_t(__ballot(tag >= 0)) & 0xFFFFu;
@@ -184,12 +208,18 @@ __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int ro
         const gptr<const uint8_t> base = (gptr<const uint8_t>)a.b + (int64_t(ad) * a.E + e) * (int64_t(a.m) * a.rank * 2);
 #pragma unroll
         for (int c = 0; c < KINDS; ++c) {
-            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+            f32x4 d[NQ];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
             for (int j0 = 0; j0 < a.rank; j0 += 32) {
                 const int j = j0 + g * 8;
-                u32x4 bf = {0u, 0u, 0u, 0u}, hi = bf, lo = bf;
+                u32x4 bf[NQ], hi = {0u, 0u, 0u, 0u}, lo = hi;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) bf[q] = u32x4{0u, 0u, 0u, 0u};
                 if (j < a.rank) {
-                    bf = *(gptr<const u32x4>)(base + (int64_t(wrow[c]) * a.rank + j) * 2);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+                        bf[q] = *(gptr<const u32x4>)(base + (int64_t(wrow[c * NQ + q]) * a.rank + j) * 2);
                     const f32x4 t0 = *(gptr<const f32x4>)(trow + c * a.rank + j);
                     const f32x4 t1 = *(gptr<const f32x4>)(trow + c * a.rank + j + 4);
 #pragma unroll
@@ -203,11 +233,13 @@ __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int ro
                         lo[i] = pack_bf16(r0, r1);
                     }
                 }
-                d = mfma_bf16(bf, lo, d);
-                d = mfma_bf16(bf, hi, d);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) d[q] = mfma_bf16(bf[q], hi, mfma_bf16(bf[q], lo, d[q]));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[c][i] = mine ? v[c][i] + d[i] : v[c][i];
+            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[c * NQ + q][i] = mine ? v[c * NQ + q][i] + d[q][i] : v[c * NQ + q][i];
         }
     }
 }
@@ -227,14 +259,12 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
     __shared__ float amax[OUT8 ? KS : 1][MB][16];
     const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave == 0) build_tiles(tiles, a.ends, a.E, a.alpha, a.rows, 16 * MB);
+    if (wave == 0) build_tiles<16 * MB>(tiles, a.ends, a.E, a.alpha, a.rows);
     __syncthreads();
     const int nu = a.kb / 128;               // steps of k (FP8: scale blocks)
     for (Items it = my_items(tiles.first[a.E] * a.ntiles); it.at < it.end; it.at += it.step) {
         const int tile = it.at / a.ntiles, c0 = (it.at - tile * a.ntiles) * BN;
-        const int e = tile_expert(tiles, a.E, tile);
-        const int done = (tile - tiles.first[e]) * (16 * MB);
-        const int row0 = tiles.start[e] + done, nrows = min(16 * MB, tiles.count[e] - done);
+        const auto [e, row0, nrows] = find_tile<16 * MB, 16>(tiles, a.E, tile);
         const gptr<const uint8_t> wb = (gptr<const uint8_t>)a.w + int64_t(e) * a.m * a.kb;
         const gptr<const uint8_t> xb = (gptr<const uint8_t>)a.x + int64_t(row0) * a.kb;
         uint32_t wo[NB], xo[MB];
@@ -295,14 +325,16 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
         for (int o = 0; o < kOwn; ++o) {
             const int idx = o * KS + wave, i = idx / G, q = idx - i * G;
             if (idx < MB * G) {
-                f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                f32x4 v[GATED ? 2 : 1];
+#pragma unroll
+                for (auto &z : v) z = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     const f32x4 p = red[s][i * NB + q][lane];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[0][j] += p[j];
-                    if (GATED) {
-                        const f32x4 p1 = red[s][i * NB + (GATED ? G : 0) + q][lane];
+                    if constexpr (GATED) {
+                        const f32x4 p1 = red[s][i * NB + G + q][lane];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v[1][j] += p1[j];
                     }
@@ -313,10 +345,15 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
                     int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
                     if (tag >= a.nad) tag = -1;
                     const int c = min(c0 + col_of<G>(q, r16), a.n - 1);
-                    const int wrow[2] = {c, a.n + c};
-                    add_adapters<GATED ? 2 : 1>(a, e, row, tag, wrow, v);
+                    if constexpr (GATED) {
+                        const int wrow[2] = {c, a.n + c};
+                        add_adapters<2, 1>(a, e, row, tag, wrow, v);
+                    } else {
+                        const int wrow[1] = {c};
+                        add_adapters<1, 1>(a, e, row, tag, wrow, v);
+                    }
                 }
-                if (GATED)
+                if constexpr (GATED)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[1][j];
                 const int c = c0 + g * (4 * G) + q * 4;
@@ -371,6 +408,291 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
     }
 }
 
+// Products of many rows per expert: a workgroup of eight wavefronts computes up to
+// 256 rows by 256 weight rows, two wavefronts along the rows and four along the
+// weights, so that each holds MB (at most 8) by 4 blocks of 16 x 16.  Steps of 128
+// bytes of k of both operands go from global memory straight into LDS (no
+// registers, no address arithmetic: per-lane offsets are fixed, each item is a
+// pair of buffer descriptors, and rows behind the tile read as zero by the
+// descriptor's bound); one step is computed while the next one, or the next
+// item's first, is on its way.
+//
+// In LDS a row's step is eight 16-byte pieces, piece p at p ^ (row / 2 % 8): the
+// sixteen rows a read of one piece touches then lie in sixteen different bank
+// groups, while the writes, whose order the hardware fixes, stay whole rows.
+constexpr int kManyThreads = 512;
+constexpr int kManyRows = 256;                       // rows, and weight rows, of a tile
+constexpr uint32_t kManyHalf = kManyRows * 128;      // bytes of one operand's step
+constexpr uint32_t kManyScales = 2 * kManyHalf;      // FP8: the step's scales behind the operands
+constexpr uint32_t kManyStage = 2 * kManyHalf + 8 * 256;
+constexpr uint32_t kManyLds = 2 * kManyStage;
+
+struct ManyItem {
+    Tile t;
+    int c0;
+    u32x4 xr, wr, sr;   // buffer descriptors of the tile's rows, weight rows and (by wavefront) scales
+};
+
+__device__ __forceinline__ u32x4 buffer_of(const void *p, uint32_t bytes)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(v)))),
+                 uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(v >> 32) & 0xFFFFu))),
+                 uint32_t(__builtin_amdgcn_readfirstlane(int(bytes))), 0x00020000u};
+}
+
+// 64 lanes x 16 (or 4) bytes of buffer `r`, lane by lane at voff + soff, to LDS
+// from `lds` on.  In assembly, because the compiler waits for every such load it
+// knows of before any LDS read that it cannot tell apart, which would end the
+// overlap of one step's arithmetic with the next one's loads; the waits are
+// written out where a stage is first read.  (These kernels use M0 nowhere else.)
+__device__ __forceinline__ void to_lds16(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(r),
+                 "s"(soff));
+}
+__device__ __forceinline__ void to_lds4(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(r),
+                 "s"(soff));
+}
+
+template <bool FP8, bool GATED, bool OUT8, bool LOW>
+struct Many {
+    static constexpr int G = GATED ? 2 : 4;      // blocks of one kind per wavefront
+    static constexpr int BN = GATED ? 128 : 256; // columns of out per tile
+
+    const ProductArgs &a;
+    Tiles &tiles;
+    float *amax;                   // LDS [4][256]
+    lptr<unsigned char> stages;
+    uint32_t lds;                  // LDS address of the first stage
+    int lane, g, r16, wave, wm, wn;
+    uint32_t xo[4], wo[4], so;     // this lane's offsets of a step's pieces
+    int nu;
+
+    __device__ __forceinline__ Many(const ProductArgs &a_, Tiles &t_, float *amax_, lptr<unsigned char> stages_)
+        : a(a_), tiles(t_), amax(amax_), stages(stages_)
+    {
+        lds = uint32_t(reinterpret_cast<uintptr_t>(stages));
+        lane = threadIdx.x & 63;
+        g = lane >> 4;
+        r16 = lane & 15;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wm = wave >> 2;
+        wn = wave & 3;
+        nu = a.kb / 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (i * 8 + wave) * 8 + (lane >> 3);   // of the stage
+            const uint32_t piece = uint32_t(((lane & 7) ^ (row >> 1 & 7)) * 16);
+            xo[i] = uint32_t(row) * uint32_t(a.kb) + piece;
+            // wavefront wn's rows of the stage are its four blocks in order
+            const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + col_of<G>(q % G, row & 15);
+            wo[i] = uint32_t(q < G ? c : a.n + c) * uint32_t(a.kb) + piece;
+        }
+        // wavefronts 0-3 bring 64 row scales each, the others the weights' two
+        if (FP8) so = wave < 4 ? uint32_t(wave * 64 + lane) * uint32_t(nu) * 4u
+                               : uint32_t(GATED ? (lane & 1) * (a.n / 128) : (lane & 1)) * uint32_t(nu) * 4u;
+    }
+
+    __device__ __forceinline__ ManyItem item(int at) const
+    {
+        ManyItem m;
+        const int tile = at / a.ntiles;
+        m.t = find_tile<kManyRows, 32>(tiles, a.E, tile);
+        m.c0 = (at - tile * a.ntiles) * BN;
+        m.xr = buffer_of(a.x + int64_t(m.t.row0) * a.kb, uint32_t(m.t.nrows) * uint32_t(a.kb));
+        m.wr = buffer_of(a.w + (int64_t(m.t.e) * a.m + m.c0) * a.kb, uint32_t(a.m - m.c0) * uint32_t(a.kb));
+        if (FP8) {
+            const int mb = (a.m + 127) / 128;   // scale rows of an expert
+            if (wave < 4) m.sr = buffer_of(a.xs + int64_t(m.t.row0) * nu, uint32_t(m.t.nrows) * uint32_t(nu) * 4u);
+            else m.sr = buffer_of(a.ws + (int64_t(m.t.e) * mb + m.c0 / 128) * nu, uint32_t(mb - m.c0 / 128) * uint32_t(nu) * 4u);
+        }
+        return m;
+    }
+
+    // Step u of the item into stage `buf`.
+    __device__ __forceinline__ void issue(const ManyItem &m, int u, int buf) const
+    {
+        const uint32_t at = lds + uint32_t(buf) * kManyStage, so_u = uint32_t(u) * 128u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to_lds16(m.wr, wo[i], so_u, at + kManyHalf + uint32_t(i * 8 + wave) * 1024u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to_lds16(m.xr, xo[i], so_u, at + uint32_t(i * 8 + wave) * 1024u);
+        if (FP8) to_lds4(m.sr, so, uint32_t(u) * 4u, at + kManyScales + uint32_t(wave) * 256u);
+    }
+
+    __device__ __forceinline__ u32x4 piece(lptr<const unsigned char> base, int row, int p) const
+    {
+        return *(lptr<const u32x4>)(base + row * 128 + (p ^ (row >> 1 & 7)) * 16);
+    }
+
+    // The item's tile of MB blocks per wavefront along the rows; its first step is
+    // in flight to stage `buf`.  Brings `next`'s first step on its way.
+    template <int MB>
+    __device__ __forceinline__ void tile(const ManyItem &m, const ManyItem &next, bool more, int &buf) const
+    {
+        f32x4 acc[MB][4];
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < nu; ++u) {
+            // this wavefront's part of the step has come; behind the barrier all of
+            // it has, and every read of the other stage is over
+            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+            if (u + 1 < nu) issue(m, u + 1, buf ^ 1);
+            else if (more) issue(next, 0, buf ^ 1);
+            const lptr<const unsigned char> xb = stages + buf * kManyStage, wb = xb + kManyHalf + wn * 64 * 128;
+            if constexpr (FP8) {
+                Frag wf[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) wf[q].p[p] = piece(wb, q * 16 + r16, 2 * g + p);
+                const lptr<const float> sc = (lptr<const float>)(xb + kManyScales);
+                const float s0 = sc[256 + (GATED ? 0 : wn >> 1)], s1 = sc[257];
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    const int row = (wm * MB + i) * 16 + r16;
+                    Frag xf;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) xf.p[p] = piece(xb, row, 2 * g + p);
+                    const float sx = sc[row];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 d = mfma_fp8(wf[q], xf, f32x4{0.f, 0.f, 0.f, 0.f});
+                        const float s = sx * (q < G ? s0 : s1);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][q][j] = fmaf(d[j], s, acc[i][q][j]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    u32x4 wf[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) wf[q] = piece(wb, q * 16 + r16, 2 * g + p);
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) {
+                        const u32x4 xf = piece(xb, (wm * MB + i) * 16 + r16, 2 * g + p);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[i][q] = mfma_bf16(wf[q], xf, acc[i][q]);
+                    }
+                }
+            }
+            buf ^= 1;
+        }
+        finish<MB>(m, acc);
+    }
+
+    template <int MB>
+    __device__ __forceinline__ void finish(const ManyItem &m, f32x4 (&acc)[MB][4]) const
+    {
+        const int cw = m.c0 + wn * (16 * G) + g * (4 * G);   // this lane's first column
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            const int r = (wm * MB + i) * 16 + r16;
+            const bool in = r < m.t.nrows;
+            const int row = m.t.row0 + min(r, m.t.nrows - 1);
+            if constexpr (LOW) {
+                int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
+                if (tag >= a.nad) tag = -1;
+                int wrow[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int c = min(m.c0 + wn * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
+                    wrow[q] = q < G ? c : a.n + c;
+                }
+                add_adapters<GATED ? 2 : 1, G>(a, m.t.e, row, tag, wrow, acc[i]);
+            }
+            if constexpr (GATED)
+#pragma unroll
+                for (int q = 0; q < G; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][q][j] = silu(acc[i][q][j]) * acc[i][q + G][j];
+            if constexpr (!OUT8) {
+#pragma unroll
+                for (int h = 0; h < G / 2; ++h)
+                    if (in && cw + h * 8 < a.n)
+                        *(gptr<u32x4>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + cw + h * 8) =
+                            u32x4{pack_bf16(acc[i][2 * h][0], acc[i][2 * h][1]), pack_bf16(acc[i][2 * h][2], acc[i][2 * h][3]),
+                                  pack_bf16(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
+                                  pack_bf16(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
+            } else {
+                float v = 0.f;
+#pragma unroll
+                for (int q = 0; q < G; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v = fmaxf(v, fabsf(acc[i][q][j]));
+                v = fmaxf(v, __shfl_xor(v, 16));
+                v = fmaxf(v, __shfl_xor(v, 32));
+                if (g == 0) amax[wn * kManyRows + r] = v;
+            }
+        }
+        if constexpr (OUT8) {
+            // the tile's 128 columns are one scale block, spread over the four
+            // wavefronts along the weights
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                const int r = (wm * MB + i) * 16 + r16;
+                float v = amax[r];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) v = fmaxf(v, amax[w * kManyRows + r]);
+                const float sc = v / 448.0f;
+                if (r < m.t.nrows) {
+                    const int64_t row = m.t.row0 + r;
+                    if (wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + m.c0 / 128] = sc;
+                    u32x2 code;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float d[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? acc[i][q][j] / sc : 0.f;
+                        int c = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
+                        code[q] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], c, true));
+                    }
+                    *(gptr<u32x2>)((gptr<uint8_t>)a.out + row * a.n + cw) = code;
+                }
+            }
+            // (amax is written again behind the next item's step barriers)
+        }
+    }
+};
+
+template <bool FP8, bool GATED, bool OUT8, bool LOW>
+__global__ __launch_bounds__(kManyThreads) void k_product_many(ProductArgs a)
+{
+    extern __shared__ __align__(16) unsigned char stages[];
+    __shared__ Tiles tiles;
+    __shared__ float amax[OUT8 ? 4 * kManyRows : 1];
+    if (threadIdx.x < kWave) build_tiles<kManyRows>(tiles, a.ends, a.E, a.alpha, a.rows);
+    __syncthreads();
+    Many<FP8, GATED, OUT8, LOW> k(a, tiles, amax, (lptr<unsigned char>)stages);
+    Items it = my_items(tiles.first[a.E] * a.ntiles);
+    if (it.at >= it.end) return;
+    int buf = 0;
+    ManyItem m = k.item(it.at);
+    k.issue(m, 0, 0);
+    for (; it.at < it.end; it.at += it.step) {
+        const bool more = it.at + it.step < it.end;
+        const ManyItem next = more ? k.item(it.at + it.step) : m;
+        switch ((m.t.nrows + 31) / 32) {
+        case 1: k.template tile<1>(m, next, more, buf); break;
+        case 2: k.template tile<2>(m, next, more, buf); break;
+        case 3: k.template tile<3>(m, next, more, buf); break;
+        case 4: k.template tile<4>(m, next, more, buf); break;
+        case 5: k.template tile<5>(m, next, more, buf); break;
+        case 6: k.template tile<6>(m, next, more, buf); break;
+        case 7: k.template tile<7>(m, next, more, buf); break;
+        default: k.template tile<8>(m, next, more, buf); break;
+        }
+        m = next;
+    }
+}
+
 // -------------------------------------------------------------- adapters ----
 
 struct ShrinkArgs {
@@ -414,15 +736,13 @@ __global__ __launch_bounds__(KS * kWave) void k_shrink(ShrinkArgs a)
     __shared__ f32x4 red[2][KS][kWave];
     const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave == 0) build_tiles(tiles, a.ends, a.E, a.alpha, a.rows, 16);
+    if (wave == 0) build_tiles<16>(tiles, a.ends, a.E, a.alpha, a.rows);
     __syncthreads();
     const int nu = a.k / kStep;
     int buf = 0;
     for (Items it = my_items(tiles.first[a.E] * a.split); it.at < it.end; it.at += it.step) {
         const int tile = it.at / a.split, y = it.at - tile * a.split;
-        const int e = tile_expert(tiles, a.E, tile);
-        const int done = (tile - tiles.first[e]) * 16;
-        const int row0 = tiles.start[e] + done, nrows = min(16, tiles.count[e] - done);
+        const auto [e, row0, nrows] = find_tile<16, 16>(tiles, a.E, tile);
         const int row = row0 + min(r16, nrows - 1);
         int tag = r16 < nrows ? ((gptr<const int32_t>)a.tags)[row] : -1;
         if (tag >= a.nad) tag = -1;
@@ -531,6 +851,24 @@ void launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
     hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, MB, NB, KS>), dim3(grid), dim3(KS * kWave), 0, st, a);
 }
 
+// A launch whose dynamic LDS exceeds 64 KiB; the kernel is told once per device.
+template <bool FP8, bool GATED, bool OUT8, bool LOW>
+int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
+{
+    constexpr int BN = GATED ? 128 : 256;
+    a.ntiles = (p.n + BN - 1) / BN;
+    static const hipError_t set =
+        hipFuncSetAttribute(reinterpret_cast<const void *>(&k_product_many<FP8, GATED, OUT8, LOW>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kManyLds));
+    if (set != hipSuccess) return 1;
+    const unsigned grid = persistent_grid(tile_bound(p, kManyRows), a.ntiles, kComputeUnits);
+    hipLaunchKernelGGL((k_product_many<FP8, GATED, OUT8, LOW>), dim3(grid), dim3(kManyThreads), kManyLds, st, a);
+    return launched();
+}
+
+// Rows per expert (by the host's bound) from which the tiled product runs.
+constexpr int64_t kManyFrom = 64;
+
 }  // namespace
 
 int be_launch_product(const ProductPlan &p, void *stream)
@@ -576,6 +914,21 @@ int be_launch_product(const ProductPlan &p, void *stream)
     a.kb = p.k * (p.fp8 ? 1 : 2);
     a.nad = p.nad;
     a.rank = p.rank;
+    // the rows' bound without what alignment alone can add
+    const int64_t per_expert = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E;
+    if (per_expert >= kManyFrom) {
+        const bool low = p.nad > 0;
+        if (!p.fp8) {
+            if (p.gated)
+                return low ? launch_many<false, true, false, true>(p, a, st) : launch_many<false, true, false, false>(p, a, st);
+            return low ? launch_many<false, false, false, true>(p, a, st) : launch_many<false, false, false, false>(p, a, st);
+        }
+        if (p.out8)
+            return low ? launch_many<true, true, true, true>(p, a, st) : launch_many<true, true, true, false>(p, a, st);
+        if (p.gated)
+            return low ? launch_many<true, true, false, true>(p, a, st) : launch_many<true, true, false, false>(p, a, st);
+        return low ? launch_many<true, false, false, true>(p, a, st) : launch_many<true, false, false, false>(p, a, st);
+    }
     if (!p.fp8) {
         if (p.gated) launch_few<false, true, false, 1, 4, 8>(p, a, st);
         else launch_few<false, false, false, 1, 4, 8>(p, a, st);

@@ -421,7 +421,8 @@ typedef enum {
  * expert j.
  *   num_experts   experts of the partition, 1..AFD_MAX_EXPERTS
  *   alignment     alpha of the rows' layout, >= 1
- *   k             columns of x: a positive multiple of 64 (BF16) or 128 (FP8)
+ *   k             columns of x: a positive multiple of 64 (BF16) or 128 (FP8), at
+ *                 most 2^21
  *   n             columns of out: a positive multiple of 16; of 128 for an FP8
  *                 product with AFD_ACT_SWIGLU
  *   dtype         of x and W: BF16, or E4M3 with FP32 scales, x per row and 128

@@ -69,7 +69,7 @@ def test_accepted(lib, kw):
 
 @pytest.mark.parametrize("kw", [
     dict(num_experts=0), dict(num_experts=513), dict(alignment=0), dict(k=0), dict(k=32), dict(k=-64), dict(dtype=1, k=64),
-    dict(n=0), dict(n=8), dict(n=24), dict(dtype=2), dict(dtype=-1), dict(activation=2), dict(out_dtype=1),
+    dict(k=(1 << 21) + 64, n=16), dict(n=0), dict(n=8), dict(n=24), dict(dtype=2), dict(dtype=-1), dict(activation=2), dict(out_dtype=1),
     dict(dtype=1, out_dtype=1), dict(FP8G, out_dtype=2), dict(activation=1, out_dtype=1), dict(FP8G, n=64),
     dict(num_adapters=-1), dict(num_adapters=3), dict(rank=16), dict(LOW, rank=4), dict(LOW, rank=20), dict(LOW, rank=136),
     dict(num_adapters=65537, rank=16), dict(k=1 << 20, n=1 << 10), dict(k=1 << 19, n=1 << 10, activation=1),

@@ -18,6 +18,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "afd_plan.h"
 
 namespace afd {
@@ -180,13 +182,13 @@ struct ProductArgs {
     int ntiles;    // column tiles
 };
 
-// Column of the 16-row block q of G that a wavefront holds, A-operand row r:
-// D gives lane group r/4 the rows 4(r/4) .. + 3, so this order makes one lane's
-// G results 4G consecutive columns.
-template <int G>
+// Column of A-operand row r of a wavefront's block q.  D gives lane group r / 4 the
+// rows 4(r / 4) .. + 3, so this order makes a lane's results of two blocks eight
+// consecutive columns and the four lane groups' thirty-two: one store of 16 bytes
+// per lane then writes whole 64-byte pieces of a row.
 __device__ __forceinline__ int col_of(int q, int r)
 {
-    return (r >> 2) * (4 * G) + q * 4 + (r & 3);
+    return (q >> 1) * 32 + (r >> 2) * 8 + (q & 1) * 4 + (r & 3);
 }
 
 // Adds B t of a row block's adapters to v: NQ blocks per kind of 4 consecutive
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
         uint32_t wo[NB], xo[MB];
 #pragma unroll
         for (int q = 0; q < NB; ++q) {
-            const int c = min(c0 + col_of<G>(q % G, r16), a.n - 1);
+            const int c = min(c0 + col_of(q % G, r16), a.n - 1);
             wo[q] = uint32_t((q < G ? c : a.n + c) * a.kb + g * 32);
         }
 #pragma unroll
@@ -344,7 +346,7 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
                 if (a.nad > 0) {
                     int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
                     if (tag >= a.nad) tag = -1;
-                    const int c = min(c0 + col_of<G>(q, r16), a.n - 1);
+                    const int c = min(c0 + col_of(q, r16), a.n - 1);
                     if constexpr (GATED) {
                         const int wrow[2] = {c, a.n + c};
                         add_adapters<2, 1>(a, e, row, tag, wrow, v);
@@ -356,7 +358,7 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
                 if constexpr (GATED)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[1][j];
-                const int c = c0 + g * (4 * G) + q * 4;
+                const int c = c0 + col_of(q, g * 4);
                 if constexpr (!OUT8) {
                     if (in && c < a.n)
                         *(gptr<u32x2>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + c) =
@@ -394,7 +396,7 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
                 if (in && wave == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
 #pragma unroll
                 for (int p = 0; p < per; ++p) {
-                    const int q = p * KS + wave, c = c0 + g * (4 * G) + q * 4;
+                    const int q = p * KS + wave, c = c0 + col_of(q, g * 4);
                     float d[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? res[i * per + p][j] / sc : 0.f;
@@ -408,25 +410,17 @@ __global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
     }
 }
 
-// Products of many rows per expert: a workgroup of eight wavefronts computes up to
-// 256 rows by 256 weight rows, two wavefronts along the rows and four along the
-// weights, so that each holds MB (at most 8) by 4 blocks of 16 x 16.  Steps of 128
-// bytes of k of both operands go from global memory straight into LDS (no
-// registers, no address arithmetic: per-lane offsets are fixed, each item is a
-// pair of buffer descriptors, and rows behind the tile read as zero by the
-// descriptor's bound); one step is computed while the next one, or the next
-// item's first, is on its way.
+// Products of many rows per expert: WM x WN wavefronts compute a tile of up to
+// 32 MX rows by 64 WN weight rows, each MB (at most MX) by 4 blocks of 16 x 16.
+// Steps of 128 bytes of k of both operands go from global memory straight into a
+// ring of ST stages in LDS (no registers, no address arithmetic: per-lane offsets
+// are fixed, each item is a few buffer descriptors, and rows behind the tile read
+// as zero by the descriptor's bound).  ST - 1 steps are on their way while one is
+// computed, across the borders of items.
 //
-// In LDS a row's step is eight 16-byte pieces, piece p at p ^ (row / 2 % 8): the
-// sixteen rows a read of one piece touches then lie in sixteen different bank
-// groups, while the writes, whose order the hardware fixes, stay whole rows.
-constexpr int kManyThreads = 512;
-constexpr int kManyRows = 256;                       // rows, and weight rows, of a tile
-constexpr uint32_t kManyHalf = kManyRows * 128;      // bytes of one operand's step
-constexpr uint32_t kManyScales = 2 * kManyHalf;      // FP8: the step's scales behind the operands
-constexpr uint32_t kManyStage = 2 * kManyHalf + 8 * 256;
-constexpr uint32_t kManyLds = 2 * kManyStage;
-
+// In LDS a row's step is eight pieces of 16 bytes, piece p of row r at p ^ (r % 8):
+// the rows that one cycle of a 16-byte read touches then lie in different banks,
+// while the writes, whose order the hardware fixes, stay whole rows.
 struct ManyItem {
     Tile t;
     int c0;
@@ -441,6 +435,14 @@ __device__ __forceinline__ u32x4 buffer_of(const void *p, uint32_t bytes)
                  uint32_t(__builtin_amdgcn_readfirstlane(int(bytes))), 0x00020000u};
 }
 
+// The same in every lane, told to the compiler.
+__device__ __forceinline__ u32x4 uniform(u32x4 v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = uint32_t(__builtin_amdgcn_readfirstlane(int(v[i])));
+    return v;
+}
+
 // 64 lanes x 16 (or 4) bytes of buffer `r`, lane by lane at voff + soff, to LDS
 // from `lds` on.  In assembly, because the compiler waits for every such load it
 // knows of before any LDS read that it cannot tell apart, which would end the
@@ -448,28 +450,47 @@ __device__ __forceinline__ u32x4 buffer_of(const void *p, uint32_t bytes)
 // written out where a stage is first read.  (These kernels use M0 nowhere else.)
 __device__ __forceinline__ void to_lds16(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(r),
-                 "s"(soff));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(uniform(r)),
+                 "s"(__builtin_amdgcn_readfirstlane(int(soff))));
 }
 __device__ __forceinline__ void to_lds4(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(r),
-                 "s"(soff));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(uniform(r)),
+                 "s"(__builtin_amdgcn_readfirstlane(int(soff))));
 }
 
-template <bool FP8, bool GATED, bool OUT8, bool LOW>
+template <int WM_, int WN_, int MX_, int ST_>
+struct Shape {
+    static constexpr int WM = WM_, WN = WN_, MX = MX_, ST = ST_, SB = 128;
+    static constexpr int waves = WM * WN, threads = waves * kWave;
+    static constexpr int rows = WM * MX * 16, wrows = WN * 64;
+    static constexpr int nx = rows * SB / 1024 / waves, nw = wrows * SB / 1024 / waves;   // loads of a wavefront and step
+    static constexpr uint32_t xbytes = rows * SB, scales = (rows + wrows) * SB;
+    static_assert(nx * waves * 1024 == rows * SB && nw * waves * 1024 == wrows * SB, "whole loads");
+};
+
+template <class S, bool FP8, bool GATED, bool OUT8, bool LOW>
 struct Many {
-    static constexpr int G = GATED ? 2 : 4;      // blocks of one kind per wavefront
-    static constexpr int BN = GATED ? 128 : 256; // columns of out per tile
+    static constexpr int G = GATED ? 2 : 4;               // blocks of one kind per wavefront
+    static constexpr int BN = S::wrows / (GATED ? 2 : 1); // columns of out per tile
+    static constexpr uint32_t stage_bytes = S::scales + (FP8 ? S::waves * 256 : 0);
+    static constexpr int loads = S::nx + S::nw + (FP8 ? 1 : 0);
+    static_assert(!FP8 || (S::SB == 128 && S::rows <= 128 * S::waves / 2), "FP8 steps are scale blocks");
 
     const ProductArgs &a;
     Tiles &tiles;
-    float *amax;                   // LDS [4][256]
+    float *amax;                   // LDS [WN][rows]
     lptr<unsigned char> stages;
     uint32_t lds;                  // LDS address of the first stage
     int lane, g, r16, wave, wm, wn;
-    uint32_t xo[4], wo[4], so;     // this lane's offsets of a step's pieces
+    uint32_t xo[S::nx], wo[S::nw], so;     // this lane's offsets of a step's pieces
     int nu;
+
+    // the steps' loads run ahead of the products
+    ManyItem ahead;
+    int ahead_u, ahead_at, ahead_stage;
+
+    static __device__ __forceinline__ int key(int row) { return row & 7; }
 
     __device__ __forceinline__ Many(const ProductArgs &a_, Tiles &t_, float *amax_, lptr<unsigned char> stages_)
         : a(a_), tiles(t_), amax(amax_), stages(stages_)
@@ -479,133 +500,156 @@ struct Many {
         g = lane >> 4;
         r16 = lane & 15;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        wm = wave >> 2;
-        wn = wave & 3;
-        nu = a.kb / 128;
+        wm = wave / S::WN;
+        wn = wave % S::WN;
+        nu = a.kb / S::SB;
+        constexpr int np = S::SB / 16;   // pieces of a row
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = (i * 8 + wave) * 8 + (lane >> 3);   // of the stage
-            const uint32_t piece = uint32_t(((lane & 7) ^ (row >> 1 & 7)) * 16);
-            xo[i] = uint32_t(row) * uint32_t(a.kb) + piece;
-            // wavefront wn's rows of the stage are its four blocks in order
-            const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + col_of<G>(q % G, row & 15);
-            wo[i] = uint32_t(q < G ? c : a.n + c) * uint32_t(a.kb) + piece;
+        for (int i = 0; i < S::nx; ++i) {
+            const int row = ((i * S::waves + wave) * 64 + lane) / np;
+            xo[i] = uint32_t(row) * uint32_t(a.kb) + uint32_t(((lane % np) ^ key(row)) * 16);
         }
-        // wavefronts 0-3 bring 64 row scales each, the others the weights' two
-        if (FP8) so = wave < 4 ? uint32_t(wave * 64 + lane) * uint32_t(nu) * 4u
-                               : uint32_t(GATED ? (lane & 1) * (a.n / 128) : (lane & 1)) * uint32_t(nu) * 4u;
+#pragma unroll
+        for (int i = 0; i < S::nw; ++i) {
+            const int row = ((i * S::waves + wave) * 64 + lane) / np;
+            // wavefront wn's rows of the stage are its four blocks in order
+            const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + col_of(q % G, row & 15);
+            wo[i] = uint32_t(q < G ? c : a.n + c) * uint32_t(a.kb) + uint32_t(((lane % np) ^ key(row)) * 16);
+        }
+        // the first half of the wavefronts bring 64 row scales each, the others the weights' two
+        if (FP8) so = wave < S::waves / 2 ? uint32_t(wave * 64 + lane) * uint32_t(nu) * 4u
+                                          : uint32_t(GATED ? (lane & 1) * (a.n / 128) : (lane & 1)) * uint32_t(nu) * 4u;
     }
 
-    __device__ __forceinline__ ManyItem item(int at) const
+    __device__ __forceinline__ Tile tile_of(int at, int &c0) const
     {
-        ManyItem m;
         const int tile = at / a.ntiles;
-        m.t = find_tile<kManyRows, 32>(tiles, a.E, tile);
-        m.c0 = (at - tile * a.ntiles) * BN;
-        m.xr = buffer_of(a.x + int64_t(m.t.row0) * a.kb, uint32_t(m.t.nrows) * uint32_t(a.kb));
-        m.wr = buffer_of(a.w + (int64_t(m.t.e) * a.m + m.c0) * a.kb, uint32_t(a.m - m.c0) * uint32_t(a.kb));
+        c0 = (at - tile * a.ntiles) * BN;
+        return find_tile<S::rows, 16 * S::WM>(tiles, a.E, tile);
+    }
+
+    __device__ __forceinline__ void load_item(int at, bool live)
+    {
+        ahead.t = tile_of(at, ahead.c0);
+        const Tile &t = ahead.t;
+        const int c0 = ahead.c0;
+        // behind the last item the loads go on without a byte, so that their number stays the same
+        ahead.xr = buffer_of(a.x + int64_t(t.row0) * a.kb, live ? uint32_t(t.nrows) * uint32_t(a.kb) : 0u);
+        ahead.wr = buffer_of(a.w + (int64_t(t.e) * a.m + c0) * a.kb, live ? uint32_t(a.m - c0) * uint32_t(a.kb) : 0u);
         if (FP8) {
             const int mb = (a.m + 127) / 128;   // scale rows of an expert
-            if (wave < 4) m.sr = buffer_of(a.xs + int64_t(m.t.row0) * nu, uint32_t(m.t.nrows) * uint32_t(nu) * 4u);
-            else m.sr = buffer_of(a.ws + (int64_t(m.t.e) * mb + m.c0 / 128) * nu, uint32_t(mb - m.c0 / 128) * uint32_t(nu) * 4u);
+            if (wave < S::waves / 2)
+                ahead.sr = buffer_of(a.xs + int64_t(t.row0) * nu, live ? uint32_t(t.nrows) * uint32_t(nu) * 4u : 0u);
+            else
+                ahead.sr = buffer_of(a.ws + (int64_t(t.e) * mb + c0 / 128) * nu,
+                                     live ? uint32_t(mb - c0 / 128) * uint32_t(nu) * 4u : 0u);
         }
-        return m;
+        ahead_u = 0;
     }
 
-    // Step u of the item into stage `buf`.
-    __device__ __forceinline__ void issue(const ManyItem &m, int u, int buf) const
+    // The next step's loads on their way.
+    __device__ __forceinline__ void issue(const Items &it)
     {
-        const uint32_t at = lds + uint32_t(buf) * kManyStage, so_u = uint32_t(u) * 128u;
+        const uint32_t at = lds + uint32_t(ahead_stage) * stage_bytes, so_u = uint32_t(ahead_u) * uint32_t(S::SB);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to_lds16(m.wr, wo[i], so_u, at + kManyHalf + uint32_t(i * 8 + wave) * 1024u);
+        for (int i = 0; i < S::nw; ++i) to_lds16(ahead.wr, wo[i], so_u, at + S::xbytes + uint32_t(i * S::waves + wave) * 1024u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to_lds16(m.xr, xo[i], so_u, at + uint32_t(i * 8 + wave) * 1024u);
-        if (FP8) to_lds4(m.sr, so, uint32_t(u) * 4u, at + kManyScales + uint32_t(wave) * 256u);
+        for (int i = 0; i < S::nx; ++i) to_lds16(ahead.xr, xo[i], so_u, at + uint32_t(i * S::waves + wave) * 1024u);
+        if (FP8) to_lds4(ahead.sr, so, uint32_t(ahead_u) * 4u, at + S::scales + uint32_t(wave) * 256u);
+        ahead_stage = ahead_stage + 1 == S::ST ? 0 : ahead_stage + 1;
+        if (++ahead_u == nu) {
+            const bool live = ahead_at + it.step < it.end;
+            if (live) ahead_at += it.step;
+            load_item(ahead_at, live);
+        }
     }
 
-    __device__ __forceinline__ u32x4 piece(lptr<const unsigned char> base, int row, int p) const
+    __device__ __forceinline__ void begin(const Items &it)
     {
-        return *(lptr<const u32x4>)(base + row * 128 + (p ^ (row >> 1 & 7)) * 16);
+        ahead_at = it.at;
+        ahead_stage = 0;
+        load_item(it.at, true);
+#pragma unroll
+        for (int i = 0; i < S::ST - 1; ++i) issue(it);
     }
 
-    // The item's tile of MB blocks per wavefront along the rows; its first step is
-    // in flight to stage `buf`.  Brings `next`'s first step on its way.
+    __device__ __forceinline__ Frag read(lptr<const unsigned char> base, int row) const
+    {
+        Frag o;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) o.p[p] = *(lptr<const u32x4>)(base + row * S::SB + (((2 * g + p) ^ key(row)) * 16));
+        return o;
+    }
+
     template <int MB>
-    __device__ __forceinline__ void tile(const ManyItem &m, const ManyItem &next, bool more, int &buf) const
+    __device__ __forceinline__ void tile(const Tile &t, int c0, const Items &it, int &stage)
     {
         f32x4 acc[MB][4];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int row = wm * MB * 16 + r16;
         for (int u = 0; u < nu; ++u) {
             // this wavefront's part of the step has come; behind the barrier all of
-            // it has, and every read of the other stage is over
-            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-            if (u + 1 < nu) issue(m, u + 1, buf ^ 1);
-            else if (more) issue(next, 0, buf ^ 1);
-            const lptr<const unsigned char> xb = stages + buf * kManyStage, wb = xb + kManyHalf + wn * 64 * 128;
-            if constexpr (FP8) {
-                Frag wf[4];
+            // it has, and every read of the stage that is loaded next is over
+            asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 2) * loads) : "memory");
+            issue(it);
+            const lptr<const unsigned char> xb = stages + stage * stage_bytes, wb = xb + S::xbytes + wn * 64 * S::SB;
+            Frag wf[4], xf[MB];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) wf[q] = read(wb, q * 16 + r16);
+            float s0 = 0.f, s1 = 0.f, sx[MB];
+            const lptr<const float> sc = (lptr<const float>)(xb + S::scales);
+            if (FP8) {
+                s0 = sc[S::waves * 32 + (GATED ? 0 : wn >> 1)];
+                s1 = sc[S::waves * 32 + 1];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) wf[q].p[p] = piece(wb, q * 16 + r16, 2 * g + p);
-                const lptr<const float> sc = (lptr<const float>)(xb + kManyScales);
-                const float s0 = sc[256 + (GATED ? 0 : wn >> 1)], s1 = sc[257];
+                for (int i = 0; i < MB; ++i) sx[i] = sc[row + i * 16];
+            }
+            xf[0] = read(xb, row);
 #pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    const int row = (wm * MB + i) * 16 + r16;
-                    Frag xf;
+            for (int i = 0; i < MB; ++i) {
+                if (i + 1 < MB) xf[i + 1] = read(xb, row + (i + 1) * 16);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) xf.p[p] = piece(xb, row, 2 * g + p);
-                    const float sx = sc[row];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f32x4 d = mfma_fp8(wf[q], xf, f32x4{0.f, 0.f, 0.f, 0.f});
-                        const float s = sx * (q < G ? s0 : s1);
+                for (int q = 0; q < 4; ++q) {
+                    if constexpr (FP8) {
+                        const f32x4 d = mfma_fp8(wf[q], xf[i], f32x4{0.f, 0.f, 0.f, 0.f});
+                        const float s = sx[i] * (q < G ? s0 : s1);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) acc[i][q][j] = fmaf(d[j], s, acc[i][q][j]);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) acc[i][q] = mfma_bf16(wf[q].p[p], xf[i].p[p], acc[i][q]);
                     }
                 }
-            } else {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    u32x4 wf[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) wf[q] = piece(wb, q * 16 + r16, 2 * g + p);
-#pragma unroll
-                    for (int i = 0; i < MB; ++i) {
-                        const u32x4 xf = piece(xb, (wm * MB + i) * 16 + r16, 2 * g + p);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[i][q] = mfma_bf16(wf[q], xf, acc[i][q]);
-                    }
-                }
+                if (!FP8) __builtin_amdgcn_sched_barrier(0);
             }
-            buf ^= 1;
+            stage = stage + 1 == S::ST ? 0 : stage + 1;
         }
-        finish<MB>(m, acc);
+        finish<MB>(t, c0, acc);
     }
 
     template <int MB>
-    __device__ __forceinline__ void finish(const ManyItem &m, f32x4 (&acc)[MB][4]) const
+    __device__ __forceinline__ void finish(const Tile &t, int c0, f32x4 (&acc)[MB][4]) const
     {
-        const int cw = m.c0 + wn * (16 * G) + g * (4 * G);   // this lane's first column
+        const int cw = c0 + wn * (16 * G) + g * 8;   // this lane's first column
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             const int r = (wm * MB + i) * 16 + r16;
-            const bool in = r < m.t.nrows;
-            const int row = m.t.row0 + min(r, m.t.nrows - 1);
+            const bool in = r < t.nrows;
+            const int row = t.row0 + min(r, t.nrows - 1);
             if constexpr (LOW) {
                 int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
                 if (tag >= a.nad) tag = -1;
                 int wrow[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int c = min(m.c0 + wn * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
+                    const int c = min(c0 + wn * (16 * G) + col_of(q % G, r16), a.n - 1);
                     wrow[q] = q < G ? c : a.n + c;
                 }
-                add_adapters<GATED ? 2 : 1, G>(a, m.t.e, row, tag, wrow, acc[i]);
+                add_adapters<GATED ? 2 : 1, G>(a, t.e, row, tag, wrow, acc[i]);
             }
             if constexpr (GATED)
 #pragma unroll
@@ -615,8 +659,8 @@ struct Many {
             if constexpr (!OUT8) {
 #pragma unroll
                 for (int h = 0; h < G / 2; ++h)
-                    if (in && cw + h * 8 < a.n)
-                        *(gptr<u32x4>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + cw + h * 8) =
+                    if (in && cw + h * 32 < a.n)
+                        *(gptr<u32x4>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + cw + h * 32) =
                             u32x4{pack_bf16(acc[i][2 * h][0], acc[i][2 * h][1]), pack_bf16(acc[i][2 * h][2], acc[i][2 * h][3]),
                                   pack_bf16(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
                                   pack_bf16(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
@@ -628,10 +672,11 @@ struct Many {
                     for (int j = 0; j < 4; ++j) v = fmaxf(v, fabsf(acc[i][q][j]));
                 v = fmaxf(v, __shfl_xor(v, 16));
                 v = fmaxf(v, __shfl_xor(v, 32));
-                if (g == 0) amax[wn * kManyRows + r] = v;
+                if (g == 0) amax[wn * S::rows + r] = v;
             }
         }
         if constexpr (OUT8) {
+            static_assert(BN == 128, "a tile is one scale block");
             // the tile's 128 columns are one scale block, spread over the four
             // wavefronts along the weights
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -640,11 +685,11 @@ struct Many {
                 const int r = (wm * MB + i) * 16 + r16;
                 float v = amax[r];
 #pragma unroll
-                for (int w = 1; w < 4; ++w) v = fmaxf(v, amax[w * kManyRows + r]);
+                for (int w = 1; w < S::WN; ++w) v = fmaxf(v, amax[w * S::rows + r]);
                 const float sc = v / 448.0f;
-                if (r < m.t.nrows) {
-                    const int64_t row = m.t.row0 + r;
-                    if (wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + m.c0 / 128] = sc;
+                if (r < t.nrows) {
+                    const int64_t row = t.row0 + r;
+                    if (wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
                     u32x2 code;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
@@ -662,36 +707,52 @@ struct Many {
     }
 };
 
-template <bool FP8, bool GATED, bool OUT8, bool LOW>
-__global__ __launch_bounds__(kManyThreads) void k_product_many(ProductArgs a)
+template <class S, bool FP8, bool GATED, bool OUT8, bool LOW>
+__global__ __launch_bounds__(S::threads, 2) void k_product_many(ProductArgs a)
 {
     extern __shared__ __align__(16) unsigned char stages[];
     __shared__ Tiles tiles;
-    __shared__ float amax[OUT8 ? 4 * kManyRows : 1];
-    if (threadIdx.x < kWave) build_tiles<kManyRows>(tiles, a.ends, a.E, a.alpha, a.rows);
+    __shared__ float amax[OUT8 ? S::WN * S::rows : 1];
+    if (threadIdx.x < kWave) build_tiles<S::rows>(tiles, a.ends, a.E, a.alpha, a.rows);
     __syncthreads();
-    Many<FP8, GATED, OUT8, LOW> k(a, tiles, amax, (lptr<unsigned char>)stages);
+    Many<S, FP8, GATED, OUT8, LOW> k(a, tiles, amax, (lptr<unsigned char>)stages);
     Items it = my_items(tiles.first[a.E] * a.ntiles);
     if (it.at >= it.end) return;
-    int buf = 0;
-    ManyItem m = k.item(it.at);
-    k.issue(m, 0, 0);
+    const Items all = it;
+    k.begin(all);
+    int stage = 0;
     for (; it.at < it.end; it.at += it.step) {
-        const bool more = it.at + it.step < it.end;
-        const ManyItem next = more ? k.item(it.at + it.step) : m;
-        switch ((m.t.nrows + 31) / 32) {
-        case 1: k.template tile<1>(m, next, more, buf); break;
-        case 2: k.template tile<2>(m, next, more, buf); break;
-        case 3: k.template tile<3>(m, next, more, buf); break;
-        case 4: k.template tile<4>(m, next, more, buf); break;
-        case 5: k.template tile<5>(m, next, more, buf); break;
-        case 6: k.template tile<6>(m, next, more, buf); break;
-        case 7: k.template tile<7>(m, next, more, buf); break;
-        default: k.template tile<8>(m, next, more, buf); break;
+        int c0;
+        const Tile t = k.tile_of(it.at, c0);
+        const int mb = (t.nrows + 16 * S::WM - 1) / (16 * S::WM);
+        if constexpr (S::MX == 4) {
+            switch (mb) {
+            case 1: k.template tile<1>(t, c0, all, stage); break;
+            case 2: k.template tile<2>(t, c0, all, stage); break;
+            case 3: k.template tile<3>(t, c0, all, stage); break;
+            default: k.template tile<4>(t, c0, all, stage); break;
+            }
+        } else {
+            switch (mb) {
+            case 1: k.template tile<1>(t, c0, all, stage); break;
+            case 2: k.template tile<2>(t, c0, all, stage); break;
+            case 3: k.template tile<3>(t, c0, all, stage); break;
+            case 4: k.template tile<4>(t, c0, all, stage); break;
+            case 5: k.template tile<5>(t, c0, all, stage); break;
+            case 6: k.template tile<6>(t, c0, all, stage); break;
+            case 7: k.template tile<7>(t, c0, all, stage); break;
+            default: k.template tile<8>(t, c0, all, stage); break;
+            }
         }
-        m = next;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may come after the LDS is another workgroup's
 }
+
+// One workgroup per CU.  BF16: 256 x 256 tiles, two stages.  FP8: 128 x 256 tiles,
+// three stages; its sums of one scale block and the scaled ones are held side by
+// side, which 256-row tiles leave no registers for.
+typedef Shape<2, 4, 8, 2> ManyBf16;
+typedef Shape<2, 4, 4, 3> ManyFp8;
 
 // -------------------------------------------------------------- adapters ----
 
@@ -851,18 +912,20 @@ void launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
     hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, MB, NB, KS>), dim3(grid), dim3(KS * kWave), 0, st, a);
 }
 
-// A launch whose dynamic LDS exceeds 64 KiB; the kernel is told once per device.
+// A launch whose dynamic LDS exceeds 64 KiB; the kernel is told once.
 template <bool FP8, bool GATED, bool OUT8, bool LOW>
 int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
 {
-    constexpr int BN = GATED ? 128 : 256;
-    a.ntiles = (p.n + BN - 1) / BN;
+    typedef std::conditional_t<FP8, ManyFp8, ManyBf16> S;
+    typedef Many<S, FP8, GATED, OUT8, LOW> M;
+    constexpr int lds = S::ST * M::stage_bytes;
+    a.ntiles = (p.n + M::BN - 1) / M::BN;
     static const hipError_t set =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(&k_product_many<FP8, GATED, OUT8, LOW>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kManyLds));
+        hipFuncSetAttribute(reinterpret_cast<const void *>(&k_product_many<S, FP8, GATED, OUT8, LOW>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (set != hipSuccess) return 1;
-    const unsigned grid = persistent_grid(tile_bound(p, kManyRows), a.ntiles, kComputeUnits);
-    hipLaunchKernelGGL((k_product_many<FP8, GATED, OUT8, LOW>), dim3(grid), dim3(kManyThreads), kManyLds, st, a);
+    const unsigned grid = persistent_grid(tile_bound(p, S::rows), a.ntiles, kComputeUnits);
+    hipLaunchKernelGGL((k_product_many<S, FP8, GATED, OUT8, LOW>), dim3(grid), dim3(S::threads), lds, st, a);
     return launched();
 }
 

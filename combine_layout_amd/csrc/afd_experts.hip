@@ -185,10 +185,11 @@ struct ProductArgs {
 // Column of A-operand row r of a wavefront's block q.  D gives lane group r / 4 the
 // rows 4(r / 4) .. + 3, so this order makes a lane's results of two blocks eight
 // consecutive columns and the four lane groups' thirty-two: one store of 16 bytes
-// per lane then writes whole 64-byte pieces of a row.
+// per lane then writes whole 64-byte pieces of a row.  (G: blocks of one kind.)
+template <int G>
 __device__ __forceinline__ int col_of(int q, int r)
 {
-    return (q >> 1) * 32 + (r >> 2) * 8 + (q & 1) * 4 + (r & 3);
+    return G == 1 ? r : (q >> 1) * 32 + (r >> 2) * 8 + (q & 1) * 4 + (r & 3);
 }
 
 // Adds B t of a row block's adapters to v: NQ blocks per kind of 4 consecutive
@@ -247,166 +248,222 @@ __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int ro
 }
 
 // Products of few rows per expert: bound by reading every expert's weights
-// once.  A workgroup computes up to 16 MB rows by 16 NB weight rows; its KS
-// wavefronts split k (step u of 128 bytes goes to wavefront u % KS), so every
-// byte of W and x is loaded straight into the registers of the one wavefront that
-// uses it, with no staging and no barrier until the sums are joined in LDS.
-template <bool FP8, bool GATED, bool OUT8, int MB, int NB, int KS>
-__global__ __launch_bounds__(KS * kWave) void k_product_few(ProductArgs a)
-{
-    constexpr int G = GATED ? NB / 2 : NB;   // blocks of one kind
-    constexpr int BN = G * 16;               // columns of out per tile
-    __shared__ Tiles tiles;
-    __shared__ f32x4 red[KS][MB * NB][kWave];
-    __shared__ float amax[OUT8 ? KS : 1][MB][16];
-    const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave == 0) build_tiles<16 * MB>(tiles, a.ends, a.E, a.alpha, a.rows);
-    __syncthreads();
-    const int nu = a.kb / 128;               // steps of k (FP8: scale blocks)
-    for (Items it = my_items(tiles.first[a.E] * a.ntiles); it.at < it.end; it.at += it.step) {
-        const int tile = it.at / a.ntiles, c0 = (it.at - tile * a.ntiles) * BN;
-        const auto [e, row0, nrows] = find_tile<16 * MB, 16>(tiles, a.E, tile);
-        const gptr<const uint8_t> wb = (gptr<const uint8_t>)a.w + int64_t(e) * a.m * a.kb;
-        const gptr<const uint8_t> xb = (gptr<const uint8_t>)a.x + int64_t(row0) * a.kb;
+// once.  A workgroup computes up to 32 rows by 16 CS NB weight rows; its KS x CS
+// wavefronts split k (step u of 128 bytes goes to wavefront u % KS) and the
+// weight rows, so every byte of W is loaded straight into the registers of the
+// one wavefront that uses it, with no staging and no barrier until the sums are
+// joined in LDS.  A step is loaded while the one before is multiplied.
+template <bool FP8, bool GATED, bool OUT8, int NB, int KS, int CS>
+struct Few {
+    static constexpr int G = GATED ? NB / 2 : NB;   // blocks of one kind of a wavefront
+    static constexpr int BN = CS * G * 16;          // columns of out per tile
+    static constexpr int waves = KS * CS, threads = waves * kWave;
+    static constexpr int rows = 32;
+
+    struct Shared {
+        Tiles tiles;
+        f32x4 red[KS][CS * NB][kWave];
+        float amax[OUT8 ? waves : 1][16];
+    };
+    template <int MB>
+    struct Step {
+        Frag w[NB], x[MB];
+        float sx[MB], s0, s1;
+    };
+
+    const ProductArgs &a;
+    Shared &sh;
+    int lane, g, r16, wave, kw, cw, nu;
+
+    __device__ __forceinline__ Few(const ProductArgs &a_, Shared &s_) : a(a_), sh(s_)
+    {
+        lane = threadIdx.x & 63;
+        g = lane >> 4;
+        r16 = lane & 15;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        kw = wave % KS;
+        cw = wave / KS;
+        nu = a.kb / 128;   // steps of k (FP8: scale blocks)
+    }
+
+    template <int MB>
+    __device__ __forceinline__ void run(const Tile &t, int c0)
+    {
+        const gptr<const uint8_t> wb = (gptr<const uint8_t>)a.w + int64_t(t.e) * a.m * a.kb;
+        const gptr<const uint8_t> xb = (gptr<const uint8_t>)a.x + int64_t(t.row0) * a.kb;
         uint32_t wo[NB], xo[MB];
 #pragma unroll
         for (int q = 0; q < NB; ++q) {
-            const int c = min(c0 + col_of(q % G, r16), a.n - 1);
-            wo[q] = uint32_t((q < G ? c : a.n + c) * a.kb + g * 32);
+            const int c = min(c0 + cw * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
+            wo[q] = uint32_t(q < G ? c : a.n + c) * uint32_t(a.kb) + g * 32;
         }
 #pragma unroll
-        for (int i = 0; i < MB; ++i) xo[i] = uint32_t(min(i * 16 + r16, nrows - 1)) * uint32_t(a.kb) + g * 32;
+        for (int i = 0; i < MB; ++i) xo[i] = uint32_t(min(i * 16 + r16, t.nrows - 1)) * uint32_t(a.kb) + g * 32;
         f32x4 acc[MB][NB];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int q = 0; q < NB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
         const gptr<const float> wsp =
-            FP8 ? (gptr<const float>)a.ws + (int64_t(e) * ((a.m + 127) / 128) + c0 / 128) * nu : nullptr;
-        for (int u = wave; u < nu; u += KS) {
-            Frag wf[NB], xf[MB];
+            FP8 ? (gptr<const float>)a.ws + (int64_t(t.e) * ((a.m + 127) / 128) + c0 / 128) * nu : nullptr;
+        auto load = [&](Step<MB> &st, int u) {
 #pragma unroll
             for (int q = 0; q < NB; ++q)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) wf[q].p[p] = *(gptr<const u32x4>)(wb + wo[q] + u * 128 + p * 16);
+                for (int p = 0; p < 2; ++p)
+                    st.w[q].p[p] = *(gptr<const u32x4>)(wb + wo[q] + u * 128 + p * 16);
 #pragma unroll
             for (int i = 0; i < MB; ++i)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) xf[i].p[p] = *(gptr<const u32x4>)(xb + xo[i] + u * 128 + p * 16);
+                for (int p = 0; p < 2; ++p) st.x[i].p[p] = *(gptr<const u32x4>)(xb + xo[i] + u * 128 + p * 16);
             if constexpr (FP8) {
-                const float s0 = wsp[u], s1 = GATED ? wsp[(a.n / 128) * nu + u] : 0.f;
-#pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    const float sx = ((gptr<const float>)a.xs)[int64_t(row0 + min(i * 16 + r16, nrows - 1)) * nu + u];
-#pragma unroll
-                    for (int q = 0; q < NB; ++q) {
-                        const f32x4 d = mfma_fp8(wf[q], xf[i], f32x4{0.f, 0.f, 0.f, 0.f});
-                        const float s = sx * (q < G ? s0 : s1);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[i][q][j] = fmaf(d[j], s, acc[i][q][j]);
-                    }
-                }
-            } else {
+                st.s0 = wsp[u];
+                st.s1 = GATED ? wsp[(a.n / 128) * nu + u] : 0.f;
 #pragma unroll
                 for (int i = 0; i < MB; ++i)
+                    st.sx[i] = ((gptr<const float>)a.xs)[int64_t(t.row0 + min(i * 16 + r16, t.nrows - 1)) * nu + u];
+            }
+        };
+        auto multiply = [&](const Step<MB> &st) {
 #pragma unroll
-                    for (int q = 0; q < NB; ++q)
+            for (int q = 0; q < NB; ++q)
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) acc[i][q] = mfma_bf16(wf[q].p[p], xf[i].p[p], acc[i][q]);
+                for (int i = 0; i < MB; ++i) {
+                    if constexpr (FP8) {
+                        const f32x4 d = mfma_fp8(st.w[q], st.x[i], f32x4{0.f, 0.f, 0.f, 0.f});
+                        const float f = st.sx[i] * (q < G ? st.s0 : st.s1);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][q][j] = fmaf(d[j], f, acc[i][q][j]);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) acc[i][q] = mfma_bf16(st.w[q].p[p], st.x[i].p[p], acc[i][q]);
+                    }
+                }
+        };
+        if (kw < nu) {
+            // the steps two at a time, so that each has registers of its own
+            Step<MB> s0, s1;
+            int u = kw;
+            load(s0, u);
+            for (; u + 2 * KS < nu; u += 2 * KS) {
+                load(s1, u + KS);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(s0);
+                load(s0, u + 2 * KS);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(s1);
+            }
+            if (u + KS < nu) {
+                load(s1, u + KS);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(s0);
+                multiply(s1);
+            } else {
+                multiply(s0);
             }
         }
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+        for (int i = 0; i < MB; ++i) join(t, c0, i, acc[i]);
+    }
+
+    // Row block i: the wavefronts' sums joined, and on to out.
+    __device__ __forceinline__ void join(const Tile &t, int c0, int i, const f32x4 (&acc)[NB])
+    {
 #pragma unroll
-            for (int q = 0; q < NB; ++q) red[wave][i * NB + q][lane] = acc[i][q];
+        for (int q = 0; q < NB; ++q) sh.red[kw][cw * NB + q][lane] = acc[q];
         __syncthreads();
-        constexpr int kOwn = (MB * G + KS - 1) / KS;   // (row block, column block) pairs per wavefront
-        f32x4 res[kOwn];
+        constexpr int own = (CS * G + waves - 1) / waves;   // column blocks per wavefront
+        f32x4 res[own];
+        const int r = i * 16 + r16;
+        const bool in = r < t.nrows;
+        const int row = t.row0 + min(r, t.nrows - 1);
+        float big = 0.f;
 #pragma unroll
-        for (int o = 0; o < kOwn; ++o) {
-            const int idx = o * KS + wave, i = idx / G, q = idx - i * G;
-            if (idx < MB * G) {
+        for (int o = 0; o < own; ++o) {
+            const int idx = o * waves + wave, s = idx / G, q = idx - s * G;
+            if (idx < CS * G) {
                 f32x4 v[GATED ? 2 : 1];
 #pragma unroll
                 for (auto &z : v) z = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const f32x4 p = red[s][i * NB + q][lane];
+                for (int k = 0; k < KS; ++k) {
+                    const f32x4 p = sh.red[k][s * NB + q][lane];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[0][j] += p[j];
                     if constexpr (GATED) {
-                        const f32x4 p1 = red[s][i * NB + G + q][lane];
+                        const f32x4 p1 = sh.red[k][s * NB + G + q][lane];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v[1][j] += p1[j];
                     }
                 }
-                const bool in = i * 16 + r16 < nrows;
-                const int row = row0 + min(i * 16 + r16, nrows - 1);
                 if (a.nad > 0) {
                     int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
                     if (tag >= a.nad) tag = -1;
-                    const int c = min(c0 + col_of(q, r16), a.n - 1);
+                    const int c = min(c0 + s * (16 * G) + col_of<G>(q, r16), a.n - 1);
                     if constexpr (GATED) {
                         const int wrow[2] = {c, a.n + c};
-                        add_adapters<2, 1>(a, e, row, tag, wrow, v);
+                        add_adapters<2, 1>(a, t.e, row, tag, wrow, v);
                     } else {
                         const int wrow[1] = {c};
-                        add_adapters<1, 1>(a, e, row, tag, wrow, v);
+                        add_adapters<1, 1>(a, t.e, row, tag, wrow, v);
                     }
                 }
                 if constexpr (GATED)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[1][j];
-                const int c = c0 + col_of(q, g * 4);
+                const int c = c0 + s * (16 * G) + col_of<G>(q, g * 4);
                 if constexpr (!OUT8) {
                     if (in && c < a.n)
                         *(gptr<u32x2>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + c) =
                             u32x2{pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3])};
                 } else {
                     res[o] = v[0];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(v[0][j]));
                 }
             }
         }
         if constexpr (OUT8) {
-            // one scale per row and tile (a tile is one 128-column block); a
-            // wavefront's pairs are of one row block each, KS of them per G / KS
-            static_assert(BN == 128 && G % KS == 0, "a tile is one scale block");
-            constexpr int per = G / KS;   // pairs of one row block per wavefront
-#pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                float m = 0.f;
-#pragma unroll
-                for (int p = 0; p < per; ++p)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(res[i * per + p][j]));
-                m = fmaxf(m, __shfl_xor(m, 16));
-                m = fmaxf(m, __shfl_xor(m, 32));
-                if (g == 0) amax[wave][i][r16] = m;
-            }
+            // one scale per row and tile (a tile is one 128-column block)
+            static_assert(BN == 128 && CS * G % waves == 0, "a tile is one scale block");
+            big = fmaxf(big, __shfl_xor(big, 16));
+            big = fmaxf(big, __shfl_xor(big, 32));
+            if (g == 0) sh.amax[wave][r16] = big;
             __syncthreads();
+            float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                float m = 0.f;
+            for (int w = 0; w < waves; ++w) m = fmaxf(m, sh.amax[w][r16]);
+            const float sc = m / 448.0f;
+            if (in && wave == 0 && g == 0) ((gptr<float>)a.outs)[int64_t(row) * (a.n / 128) + c0 / 128] = sc;
 #pragma unroll
-                for (int s = 0; s < KS; ++s) m = fmaxf(m, amax[s][i][r16]);
-                const float sc = m / 448.0f;
-                const bool in = i * 16 + r16 < nrows;
-                const int64_t row = row0 + i * 16 + r16;
-                if (in && wave == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
+            for (int o = 0; o < own; ++o) {
+                const int idx = o * waves + wave, s = idx / G, q = idx - s * G;
+                float d[4];
 #pragma unroll
-                for (int p = 0; p < per; ++p) {
-                    const int q = p * KS + wave, c = c0 + col_of(q, g * 4);
-                    float d[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? res[i * per + p][j] / sc : 0.f;
-                    int code = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
-                    code = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], code, true);
-                    if (in) *(gptr<int>)((gptr<uint8_t>)a.out + row * a.n + c) = code;
-                }
+                for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? res[o][j] / sc : 0.f;
+                int code = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
+                code = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], code, true);
+                if (in) *(gptr<int>)((gptr<uint8_t>)a.out + int64_t(row) * a.n + c0 + s * (16 * G) + col_of<G>(q, g * 4)) = code;
             }
         }
-        __syncthreads();   // the next item writes red and amax again
+        __syncthreads();   // red and amax are written again
+    }
+};
+
+template <bool FP8, bool GATED, bool OUT8, int NB, int KS, int CS>
+__global__ __launch_bounds__(KS * CS * kWave) void k_product_few(ProductArgs a)
+{
+    typedef Few<FP8, GATED, OUT8, NB, KS, CS> F;
+    __shared__ typename F::Shared sh;
+    if (threadIdx.x < kWave) build_tiles<F::rows>(sh.tiles, a.ends, a.E, a.alpha, a.rows);
+    __syncthreads();
+    F f(a, sh);
+    for (Items it = my_items(sh.tiles.first[a.E] * a.ntiles); it.at < it.end; it.at += it.step) {
+        const int tile = it.at / a.ntiles;
+        const Tile t = find_tile<F::rows, 16>(sh.tiles, a.E, tile);
+        const int c0 = (it.at - tile * a.ntiles) * F::BN;
+        if (t.nrows <= 16) f.template run<1>(t, c0);
+        else f.template run<2>(t, c0);
     }
 }
 
@@ -513,7 +570,7 @@ struct Many {
         for (int i = 0; i < S::nw; ++i) {
             const int row = ((i * S::waves + wave) * 64 + lane) / np;
             // wavefront wn's rows of the stage are its four blocks in order
-            const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + col_of(q % G, row & 15);
+            const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + col_of<G>(q % G, row & 15);
             wo[i] = uint32_t(q < G ? c : a.n + c) * uint32_t(a.kb) + uint32_t(((lane % np) ^ key(row)) * 16);
         }
         // the first half of the wavefronts bring 64 row scales each, the others the weights' two
@@ -646,7 +703,7 @@ struct Many {
                 int wrow[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int c = min(c0 + wn * (16 * G) + col_of(q % G, r16), a.n - 1);
+                    const int c = min(c0 + wn * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
                     wrow[q] = q < G ? c : a.n + c;
                 }
                 add_adapters<GATED ? 2 : 1, G>(a, t.e, row, tag, wrow, acc[i]);
@@ -903,13 +960,14 @@ int64_t tile_bound(const ProductPlan &p, int height)
 
 constexpr int kComputeUnits = 256;
 
-template <bool FP8, bool GATED, bool OUT8, int MB, int NB, int KS>
-void launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
+template <bool FP8, bool GATED, bool OUT8, int NB, int KS, int CS>
+int launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
 {
-    constexpr int BN = (GATED ? NB / 2 : NB) * 16;
-    a.ntiles = (p.n + BN - 1) / BN;
-    const unsigned grid = persistent_grid(tile_bound(p, 16 * MB), a.ntiles, kComputeUnits * 4);
-    hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, MB, NB, KS>), dim3(grid), dim3(KS * kWave), 0, st, a);
+    typedef Few<FP8, GATED, OUT8, NB, KS, CS> F;
+    a.ntiles = (p.n + F::BN - 1) / F::BN;
+    const unsigned grid = persistent_grid(tile_bound(p, F::rows), a.ntiles, kComputeUnits * 8);
+    hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, NB, KS, CS>), dim3(grid), dim3(F::threads), 0, st, a);
+    return launched();
 }
 
 // A launch whose dynamic LDS exceeds 64 KiB; the kernel is told once.
@@ -992,16 +1050,14 @@ int be_launch_product(const ProductPlan &p, void *stream)
             return low ? launch_many<true, true, false, true>(p, a, st) : launch_many<true, true, false, false>(p, a, st);
         return low ? launch_many<true, false, false, true>(p, a, st) : launch_many<true, false, false, false>(p, a, st);
     }
-    if (!p.fp8) {
-        if (p.gated) launch_few<false, true, false, 1, 4, 8>(p, a, st);
-        else launch_few<false, false, false, 1, 4, 8>(p, a, st);
-    } else if (p.out8) {
-        launch_few<true, true, true, 1, 16, 4>(p, a, st);
-    } else {
-        if (p.gated) launch_few<true, true, false, 1, 4, 8>(p, a, st);
-        else launch_few<true, false, false, 1, 4, 8>(p, a, st);
-    }
-    return launched();
+    // Workgroups of four wavefronts leave the most loads in flight per CU: 32
+    // weight rows (BF16; 64 take 133 us instead of 129 for 1024 rows over 64
+    // experts, H 2048, inner 768) or 64 (FP8: 32 take 35 us instead of 32 for the
+    // second product).  An FP8 output needs 256 weight rows, one scale block.
+    if (!p.fp8)
+        return p.gated ? launch_few<false, true, false, 2, 4, 1>(p, a, st) : launch_few<false, false, false, 2, 4, 1>(p, a, st);
+    if (p.out8) return launch_few<true, true, true, 4, 2, 4>(p, a, st);
+    return p.gated ? launch_few<true, true, false, 4, 4, 1>(p, a, st) : launch_few<true, false, false, 4, 4, 1>(p, a, st);
 }
 
 int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *tags, int32_t *out, void *stream)

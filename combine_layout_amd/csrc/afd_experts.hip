@@ -18,6 +18,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "afd_plan.h"
@@ -192,58 +193,96 @@ __device__ __forceinline__ int col_of(int q, int r)
     return G == 1 ? r : (q >> 1) * 32 + (r >> 2) * 8 + (q & 1) * 4 + (r & 3);
 }
 
-// Adds B t of a row block's adapters to v: NQ blocks per kind of 4 consecutive
-// columns of one row per lane.  wrow[] are the weight rows of this lane's
-// A-operand rows.  Adapters are taken one after the other and each lane adds only
-// its own row's, by selection, so an adapter's infinities reach no other request.
-// t enters the matrix unit as two bf16 parts, t - hi - lo below 2^-16 of t.
-template <int KINDS, int NQ>
-__device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int row, int tag, const int (&wrow)[KINDS * NQ],
-                                             f32x4 (&v)[KINDS * NQ])
+// Adds B t of the adapters of MB row blocks to v: per block, NQ column blocks per
+// kind of 4 consecutive columns of one row per lane.  wrow[] are the weight rows of
+// this lane's A-operand rows.  The distinct adapters number sub, sub + nsub, .. are
+// taken one after the other, the next one's B on its way meanwhile, and each lane
+// adds only its own row's, by selection, so an adapter's infinities reach no other
+// request.  t enters the matrix unit as two bf16 parts, t - hi - lo below 2^-16 of t.
+template <int KINDS, int NQ, int MB>
+__device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, const int (&row)[MB], const int (&tag)[MB],
+                                             const int (&wrow)[KINDS * NQ], f32x4 (&v)[MB][KINDS * NQ], int sub, int nsub)
 {
     const int lane = threadIdx.x & 63, g = lane >> 4;
-    uint32_t left = uint32_t(__ballot(tag >= 0)) & 0xFFFFu;
-    const gptr<const float> trow = (gptr<const float>)a.t + int64_t(row) * (KINDS * a.rank);
-    while (left) {
-        const int ad = __builtin_amdgcn_readlane(tag, __builtin_ctz(left));
-        const bool mine = tag == ad;
-        left &= ~uint32_t(__ballot(mine));
+    uint32_t left[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) left[i] = uint32_t(__ballot(tag[i] >= 0)) & 0xFFFFu;
+    struct Pick {
+        int ad;              // -1: none
+        uint32_t hit[MB];    // its rows
+    };
+    int skip = sub;
+    auto pick = [&]() {
+        Pick p;
+        for (;;) {
+            p.ad = -1;
+#pragma unroll
+            for (int i = MB - 1; i >= 0; --i)
+                if (left[i]) p.ad = __builtin_amdgcn_readlane(tag[i], __builtin_ctz(left[i]));
+            if (p.ad < 0) break;
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                p.hit[i] = uint32_t(__ballot(tag[i] == p.ad)) & 0xFFFFu;
+                left[i] &= ~p.hit[i];
+            }
+            if (skip == 0) {
+                skip = nsub - 1;
+                break;
+            }
+            --skip;
+        }
+        return p;
+    };
+    auto load_b = [&](u32x4 (&bf)[KINDS * NQ], int ad, int j) {
         const gptr<const uint8_t> base = (gptr<const uint8_t>)a.b + (int64_t(ad) * a.E + e) * (int64_t(a.m) * a.rank * 2);
 #pragma unroll
-        for (int c = 0; c < KINDS; ++c) {
-            f32x4 d[NQ];
+        for (int q = 0; q < KINDS * NQ; ++q)
+            bf[q] = j < a.rank ? *(gptr<const u32x4>)(base + (int64_t(wrow[q]) * a.rank + j) * 2) : u32x4{0u, 0u, 0u, 0u};
+    };
+    Pick p = pick();
+    u32x4 bf[KINDS * NQ];
+    if (p.ad >= 0) load_b(bf, p.ad, g * 8);
+    while (p.ad >= 0) {
+        const Pick next = pick();
+        u32x4 bn[KINDS * NQ];
+        if (next.ad >= 0) load_b(bn, next.ad, g * 8);
+        for (int j0 = 0; j0 < a.rank; j0 += 32) {
+            const int j = j0 + g * 8;
+            if (j0 > 0) load_b(bf, p.ad, j);
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int j0 = 0; j0 < a.rank; j0 += 32) {
-                const int j = j0 + g * 8;
-                u32x4 bf[NQ], hi = {0u, 0u, 0u, 0u}, lo = hi;
+            for (int i = 0; i < MB; ++i) {
+                if (!p.hit[i]) continue;
+                const bool mine = tag[i] == p.ad;
+                const gptr<const float> trow = (gptr<const float>)a.t + int64_t(row[i]) * (KINDS * a.rank);
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) bf[q] = u32x4{0u, 0u, 0u, 0u};
-                if (j < a.rank) {
+                for (int c = 0; c < KINDS; ++c) {
+                    u32x4 hi = {0u, 0u, 0u, 0u}, lo = hi;
+                    if (mine && j < a.rank) {
+                        const f32x4 t0 = *(gptr<const f32x4>)(trow + c * a.rank + j);
+                        const f32x4 t1 = *(gptr<const f32x4>)(trow + c * a.rank + j + 4);
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q)
-                        bf[q] = *(gptr<const u32x4>)(base + (int64_t(wrow[c * NQ + q]) * a.rank + j) * 2);
-                    const f32x4 t0 = *(gptr<const f32x4>)(trow + c * a.rank + j);
-                    const f32x4 t1 = *(gptr<const f32x4>)(trow + c * a.rank + j + 4);
+                        for (int k = 0; k < 4; ++k) {
+                            const float p0 = k < 2 ? t0[2 * k] : t1[2 * k - 4], p1 = k < 2 ? t0[2 * k + 1] : t1[2 * k - 3];
+                            const uint32_t h0 = to_bf16(p0), h1 = to_bf16(p1);
+                            float r0 = p0 - __uint_as_float(h0 << 16), r1 = p1 - __uint_as_float(h1 << 16);
+                            if (!(fabsf(r0) < INFINITY)) r0 = 0.f;   // an infinite t has no remainder
+                            if (!(fabsf(r1) < INFINITY)) r1 = 0.f;
+                            hi[k] = h0 | (h1 << 16);
+                            lo[k] = pack_bf16(r0, r1);
+                        }
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p0 = i < 2 ? t0[2 * i] : t1[2 * i - 4], p1 = i < 2 ? t0[2 * i + 1] : t1[2 * i - 3];
-                        const uint32_t h0 = to_bf16(p0), h1 = to_bf16(p1);
-                        float r0 = p0 - __uint_as_float(h0 << 16), r1 = p1 - __uint_as_float(h1 << 16);
-                        if (!(fabsf(r0) < INFINITY)) r0 = 0.f;   // an infinite t has no remainder
-                        if (!(fabsf(r1) < INFINITY)) r1 = 0.f;
-                        hi[i] = h0 | (h1 << 16);
-                        lo[i] = pack_bf16(r0, r1);
+                    for (int q = 0; q < NQ; ++q) {
+                        const f32x4 d = mfma_bf16(bf[c * NQ + q], hi, mfma_bf16(bf[c * NQ + q], lo, f32x4{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[i][c * NQ + q][k] = mine ? v[i][c * NQ + q][k] + d[k] : v[i][c * NQ + q][k];
                     }
                 }
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) d[q] = mfma_bf16(bf[q], hi, mfma_bf16(bf[q], lo, d[q]));
             }
-#pragma unroll
-            for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[c * NQ + q][i] = mine ? v[c * NQ + q][i] + d[q][i] : v[c * NQ + q][i];
         }
+        p = next;
+#pragma unroll
+        for (int q = 0; q < KINDS * NQ; ++q) bf[q] = bn[q];
     }
 }
 
@@ -253,7 +292,7 @@ __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, int ro
 // weight rows, so every byte of W is loaded straight into the registers of the
 // one wavefront that uses it, with no staging and no barrier until the sums are
 // joined in LDS.  A step is loaded while the one before is multiplied.
-template <bool FP8, bool GATED, bool OUT8, int NB, int KS, int CS>
+template <bool FP8, bool GATED, bool OUT8, bool LOW, int NB, int KS, int CS>
 struct Few {
     static constexpr int G = GATED ? NB / 2 : NB;   // blocks of one kind of a wavefront
     static constexpr int BN = CS * G * 16;          // columns of out per tile
@@ -362,6 +401,22 @@ struct Few {
                 multiply(s0);
             }
         }
+        if constexpr (LOW) {
+            // each of the KS wavefronts along k adds its share of the adapters
+            int row[MB], tag[MB], wrow[NB];
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                row[i] = t.row0 + min(i * 16 + r16, t.nrows - 1);
+                tag[i] = i * 16 + r16 < t.nrows ? ((gptr<const int32_t>)a.tags)[row[i]] : -1;
+                if (tag[i] >= a.nad) tag[i] = -1;
+            }
+#pragma unroll
+            for (int q = 0; q < NB; ++q) {
+                const int c = min(c0 + cw * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
+                wrow[q] = q < G ? c : a.n + c;
+            }
+            add_adapters<GATED ? 2 : 1, G, MB>(a, t.e, row, tag, wrow, acc, kw, KS);
+        }
 #pragma unroll
         for (int i = 0; i < MB; ++i) join(t, c0, i, acc[i]);
     }
@@ -394,18 +449,6 @@ struct Few {
                         const f32x4 p1 = sh.red[k][s * NB + G + q][lane];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v[1][j] += p1[j];
-                    }
-                }
-                if (a.nad > 0) {
-                    int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
-                    if (tag >= a.nad) tag = -1;
-                    const int c = min(c0 + s * (16 * G) + col_of<G>(q, r16), a.n - 1);
-                    if constexpr (GATED) {
-                        const int wrow[2] = {c, a.n + c};
-                        add_adapters<2, 1>(a, t.e, row, tag, wrow, v);
-                    } else {
-                        const int wrow[1] = {c};
-                        add_adapters<1, 1>(a, t.e, row, tag, wrow, v);
                     }
                 }
                 if constexpr (GATED)
@@ -450,10 +493,10 @@ struct Few {
     }
 };
 
-template <bool FP8, bool GATED, bool OUT8, int NB, int KS, int CS>
+template <bool FP8, bool GATED, bool OUT8, bool LOW, int NB, int KS, int CS>
 __global__ __launch_bounds__(KS * CS * kWave) void k_product_few(ProductArgs a)
 {
-    typedef Few<FP8, GATED, OUT8, NB, KS, CS> F;
+    typedef Few<FP8, GATED, OUT8, LOW, NB, KS, CS> F;
     __shared__ typename F::Shared sh;
     if (threadIdx.x < kWave) build_tiles<F::rows>(sh.tiles, a.ends, a.E, a.alpha, a.rows);
     __syncthreads();
@@ -692,22 +735,27 @@ struct Many {
     __device__ __forceinline__ void finish(const Tile &t, int c0, f32x4 (&acc)[MB][4]) const
     {
         const int cw = c0 + wn * (16 * G) + g * 8;   // this lane's first column
+        if constexpr (LOW) {
+            int row[MB], tag[MB], wrow[4];
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                const int r = (wm * MB + i) * 16 + r16;
+                row[i] = t.row0 + min(r, t.nrows - 1);
+                tag[i] = r < t.nrows ? ((gptr<const int32_t>)a.tags)[row[i]] : -1;
+                if (tag[i] >= a.nad) tag[i] = -1;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = min(c0 + wn * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
+                wrow[q] = q < G ? c : a.n + c;
+            }
+            add_adapters<GATED ? 2 : 1, G, MB>(a, t.e, row, tag, wrow, acc, 0, 1);
+        }
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             const int r = (wm * MB + i) * 16 + r16;
             const bool in = r < t.nrows;
             const int row = t.row0 + min(r, t.nrows - 1);
-            if constexpr (LOW) {
-                int tag = in ? ((gptr<const int32_t>)a.tags)[row] : -1;
-                if (tag >= a.nad) tag = -1;
-                int wrow[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int c = min(c0 + wn * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
-                    wrow[q] = q < G ? c : a.n + c;
-                }
-                add_adapters<GATED ? 2 : 1, G>(a, t.e, row, tag, wrow, acc[i]);
-            }
             if constexpr (GATED)
 #pragma unroll
                 for (int q = 0; q < G; ++q)
@@ -805,11 +853,11 @@ __global__ __launch_bounds__(S::threads, 2) void k_product_many(ProductArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may come after the LDS is another workgroup's
 }
 
-// One workgroup per CU.  BF16: 256 x 256 tiles, two stages.  FP8: 128 x 256 tiles,
-// three stages; its sums of one scale block and the scaled ones are held side by
-// side, which 256-row tiles leave no registers for.
-typedef Shape<2, 4, 8, 2> ManyBf16;
-typedef Shape<2, 4, 4, 3> ManyFp8;
+// One workgroup per CU: 256 x 256 tiles and two stages, or 128 x 256 and three
+// where the registers of 256 rows are not there: FP8 holds the sums of one scale
+// block beside the scaled ones, the adapters theirs.
+typedef Shape<2, 4, 8, 2> ManyTall;
+typedef Shape<2, 4, 4, 3> ManyLow;
 
 // -------------------------------------------------------------- adapters ----
 
@@ -822,15 +870,16 @@ struct ShrinkArgs {
     float *t;
     int rows, E, alpha;
     int k;
-    int c;       // rank rows of one adapter's A: rank, or 2 rank gated
+    int c;       // rows of one adapter's A: rank, or 2 rank gated
     int nad;
-    int split;   // items per row block: item y takes the block's distinct adapters y, y + split, ..
+    int share;   // workgroups per expert
 };
 
 // Eight E4M3 codes to bf16 (exact: four significant bits).
-__device__ __forceinline__ u32x4 fp8_to_bf16(u32x2 q)
+__device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t q0, uint32_t q1)
 {
     u32x4 r;
+    const uint32_t q[2] = {q0, q1};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(q[i]), false);
@@ -841,80 +890,245 @@ __device__ __forceinline__ u32x4 fp8_to_bf16(u32x2 q)
     return r;
 }
 
-// t[r, :] = scaling[a] A[a, j] x[r] for every row r with an adapter a.  An item is
-// 16 rows of one expert; the distinct adapters among them are taken one after
-// the other, the A operand holding rows of A and the B operand the 16 rows of x,
-// and each lane stores the columns of its own row's adapter.  The workgroup's
-// KS wavefronts split k and join their sums in LDS.  Bound by reading A.
-template <bool FP8, int KS>
-__global__ __launch_bounds__(KS * kWave) void k_shrink(ShrinkArgs a)
-{
-    constexpr int kStep = FP8 ? 128 : 64;   // columns of a step
-    __shared__ Tiles tiles;
-    __shared__ f32x4 red[2][KS][kWave];
-    const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave == 0) build_tiles<16>(tiles, a.ends, a.E, a.alpha, a.rows);
-    __syncthreads();
-    const int nu = a.k / kStep;
-    int buf = 0;
-    for (Items it = my_items(tiles.first[a.E] * a.split); it.at < it.end; it.at += it.step) {
-        const int tile = it.at / a.split, y = it.at - tile * a.split;
-        const auto [e, row0, nrows] = find_tile<16, 16>(tiles, a.E, tile);
-        const int row = row0 + min(r16, nrows - 1);
-        int tag = r16 < nrows ? ((gptr<const int32_t>)a.tags)[row] : -1;
-        if (tag >= a.nad) tag = -1;
-        uint32_t left = uint32_t(__ballot(tag >= 0)) & 0xFFFFu;
-        const gptr<const uint8_t> xp = (gptr<const uint8_t>)a.x + int64_t(row) * a.k * (FP8 ? 1 : 2);
-        const gptr<const float> sp = FP8 ? (gptr<const float>)a.xs + int64_t(row) * nu : nullptr;
-        for (int d = 0; left; ++d) {
-            const int ad = __builtin_amdgcn_readlane(tag, __builtin_ctz(left));
-            const bool mine = tag == ad;
-            left &= ~uint32_t(__ballot(mine));
-            if (d % a.split != y) continue;
-            const gptr<const uint8_t> ab = (gptr<const uint8_t>)a.a + (int64_t(ad) * a.E + e) * (int64_t(a.c) * a.k * 2);
-            for (int c0 = 0; c0 < a.c; c0 += 16) {
-                const gptr<const uint8_t> ap = ab + int64_t(min(c0 + r16, a.c - 1)) * a.k * 2;
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                for (int u = wave; u < nu; u += KS) {
-                    if constexpr (FP8) {
-                        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+// t[r, :] = scaling[i] A[i, j] x[r] for every row r of expert j with an adapter i.
+// Bound by reading the A of every (adapter, expert) pair once.  An expert's
+// workgroups find its distinct adapters from a bit map of the rows' tags; the
+// pairs of an adapter and 32 rows of its A go round them.  For each, the adapter's
+// rows are gathered, 32 at a time, and multiplied as in k_product_few: the
+// A operand holds rows of A, the wavefronts split k.
+template <bool FP8>
+struct Shrink {
+    static constexpr int KS = 4, threads = KS * kWave, NB = 2, CH = 16 * NB;
+    static constexpr int step = FP8 ? 128 : 64;         // columns of k
+    static constexpr int NP = FP8 ? 4 : 2;              // products of 32 columns per step
+    static constexpr int words = AFD_MAX_ADAPTERS / 32;
+
+    struct Shared {
+        uint32_t bits[words];
+        int sums[threads];
+        int list[threads + 32];   // gathered rows
+        int waves[KS], found;
+        f32x4 red[KS][2 * NB][kWave];
+    };
+    template <int MB>
+    struct Step {
+        u32x4 a[NB][NP];
+        Frag x[MB];
+        float s[MB];
+    };
+
+    const ShrinkArgs &a;
+    Shared &sh;
+    int lane, g, r16, wave, nu;
+
+    __device__ __forceinline__ Shrink(const ShrinkArgs &a_, Shared &s_) : a(a_), sh(s_)
+    {
+        lane = threadIdx.x & 63;
+        g = lane >> 4;
+        r16 = lane & 15;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        nu = a.k / step;
+    }
+
+    // n rows from list[first], columns c0 .. of the adapter.
+    template <int MB>
+    __device__ __forceinline__ void multiply(int e, int ad, int c0, int first, int n)
+    {
+        int row[MB];
+        gptr<const uint8_t> xp[MB];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            const int col = u * 128 + p * 32 + g * 8;
-                            s = mfma_bf16(*(gptr<const u32x4>)(ap + col * 2), fp8_to_bf16(*(gptr<const u32x2>)(xp + col)), s);
-                        }
-                        const float f = sp[u];
+        for (int i = 0; i < MB; ++i) {
+            row[i] = sh.list[first + min(i * 16 + r16, n - 1)];
+            xp[i] = (gptr<const uint8_t>)a.x + int64_t(row[i]) * a.k * (FP8 ? 1 : 2) + g * 32;
+        }
+        gptr<const uint8_t> ap[NB];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[j] = fmaf(s[j], f, acc[j]);
-                    } else {
+        for (int q = 0; q < NB; ++q)
+            ap[q] = (gptr<const uint8_t>)a.a +
+                    ((int64_t(ad) * a.E + e) * a.c + min(c0 + q * 16 + r16, a.c - 1)) * int64_t(a.k) * 2 + g * (FP8 ? 64 : 32);
+        f32x4 acc[MB][NB];
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const int col = u * 64 + p * 32 + g * 8;
-                            acc = mfma_bf16(*(gptr<const u32x4>)(ap + col * 2), *(gptr<const u32x4>)(xp + col * 2), acc);
-                        }
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int q = 0; q < NB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto load = [&](Step<MB> &st, int u) {
+#pragma unroll
+            for (int q = 0; q < NB; ++q)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) st.a[q][p] = *(gptr<const u32x4>)(ap[q] + u * (step * 2) + p * 16);
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) st.x[i].p[p] = *(gptr<const u32x4>)(xp[i] + u * 128 + p * 16);
+                if (FP8) st.s[i] = ((gptr<const float>)a.xs)[int64_t(row[i]) * nu + u];
+            }
+        };
+        auto use = [&](const Step<MB> &st) {
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                if constexpr (FP8) {
+                    f32x4 d[NB];
+#pragma unroll
+                    for (int q = 0; q < NB; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        const u32x4 h = st.x[i].p[p / 2];
+                        const u32x4 xv = p % 2 ? fp8_to_bf16(h[2], h[3]) : fp8_to_bf16(h[0], h[1]);
+#pragma unroll
+                        for (int q = 0; q < NB; ++q) d[q] = mfma_bf16(st.a[q][p], xv, d[q]);
                     }
+#pragma unroll
+                    for (int q = 0; q < NB; ++q)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][q][j] = fmaf(d[q][j], st.s[i], acc[i][q][j]);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+#pragma unroll
+                        for (int q = 0; q < NB; ++q) acc[i][q] = mfma_bf16(st.a[q][p], st.x[i].p[p], acc[i][q]);
                 }
-                red[buf][wave][lane] = acc;
-                __syncthreads();   // two buffers: one barrier separates the writes of a buffer from its last reads
-                if (wave == 0) {
-                    f32x4 v = red[buf][0][lane];
+            }
+        };
+        if (wave < nu) {
+            Step<MB> s0, s1;
+            int u = wave;
+            load(s0, u);
+            for (; u + 2 * KS < nu; u += 2 * KS) {
+                load(s1, u + KS);
+                __builtin_amdgcn_sched_barrier(0);
+                use(s0);
+                load(s0, u + 2 * KS);
+                __builtin_amdgcn_sched_barrier(0);
+                use(s1);
+            }
+            if (u + KS < nu) {
+                load(s1, u + KS);
+                __builtin_amdgcn_sched_barrier(0);
+                use(s0);
+                use(s1);
+            } else {
+                use(s0);
+            }
+        }
 #pragma unroll
-                    for (int s = 1; s < KS; ++s)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] += red[buf][s][lane][j];
-                    const int c = c0 + g * 4;
-                    if (mine && c < a.c) {
-                        const float f = ((gptr<const float>)a.scaling)[ad];
+            for (int q = 0; q < NB; ++q) sh.red[wave][i * NB + q][lane] = acc[i][q];
+        __syncthreads();
+        if (wave < MB * NB) {
+            const int i = wave / NB, q = wave % NB, c = c0 + q * 16 + g * 4;
+            f32x4 v = sh.red[0][wave][lane];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] *= f;
-                        *(gptr<f32x4>)((gptr<float>)a.t + int64_t(row) * a.c + c) = v;
-                    }
+            for (int w = 1; w < KS; ++w)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += sh.red[w][wave][lane][j];
+            const float f = ((gptr<const float>)a.scaling)[ad];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] *= f;
+            if (i * 16 + r16 < n && c < a.c)
+                *(gptr<f32x4>)((gptr<float>)a.t + int64_t(sh.list[first + i * 16 + r16]) * a.c + c) = v;
+        }
+        __syncthreads();   // red is written again, and the list may be
+    }
+
+    // The number (from 0) `want` of the set bits of the map.
+    __device__ __forceinline__ int nth_adapter(int want)
+    {
+        const int tid = threadIdx.x, per = words / threads;
+        const int before = tid ? sh.sums[tid - 1] : 0;
+        if (want >= before && want < sh.sums[tid]) {
+            int k = want - before;
+            for (int i = 0; i < per; ++i) {
+                uint32_t w = sh.bits[tid * per + i];
+                const int n = __popc(w);
+                if (k >= n) {
+                    k -= n;
+                    continue;
                 }
-                buf ^= 1;
+                while (k--) w &= w - 1;
+                sh.found = (tid * per + i) * 32 + __builtin_ctz(w);
+                break;
+            }
+        }
+        __syncthreads();
+        const int r = __builtin_amdgcn_readfirstlane(sh.found);
+        __syncthreads();
+        return r;
+    }
+
+    __device__ __forceinline__ void run(int e, int y, int start, int count)
+    {
+        const int tid = threadIdx.x, per = words / threads;
+        const gptr<const int32_t> tags = (gptr<const int32_t>)a.tags + start;
+        for (int i = tid; i < words; i += threads) sh.bits[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < count; i += threads) {
+            const int tag = tags[i];
+            if (tag >= 0 && tag < a.nad) atomicOr(&sh.bits[tag >> 5], 1u << (tag & 31));
+        }
+        __syncthreads();
+        int n = 0;
+        for (int i = 0; i < per; ++i) n += __popc(sh.bits[tid * per + i]);
+        for (int d = 1; d < kWave; d *= 2) {
+            const int o = __shfl_up(n, d);
+            if (lane >= d) n += o;
+        }
+        if (lane == kWave - 1) sh.waves[wave] = n;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) n += sh.waves[w];
+        sh.sums[tid] = n;
+        __syncthreads();
+        const int chunks = (a.c + CH - 1) / CH, total = __builtin_amdgcn_readfirstlane(sh.sums[threads - 1]) * chunks;
+        for (int z = y; z < total; z += a.share) {
+            const int ad = nth_adapter(z / chunks), c0 = (z % chunks) * CH;
+            int have = 0;
+            for (int base = 0; base < count; base += threads) {
+                const bool mine = base + tid < count && tags[base + tid] == ad;
+                const uint64_t m = __ballot(mine);
+                if (lane == 0) sh.waves[wave] = __popcll(m);
+                __syncthreads();
+                int at = have + __popcll(m & ((uint64_t(1) << lane) - 1)), all = have;
+                for (int w = 0; w < KS; ++w) {
+                    if (w < wave) at += sh.waves[w];
+                    all += sh.waves[w];
+                }
+                if (mine) sh.list[at] = start + base + tid;
+                have = __builtin_amdgcn_readfirstlane(all);
+                __syncthreads();
+                const bool last = base + threads >= count;
+                int first = 0;
+                while (have - first >= 32 || (last && have > first)) {
+                    const int n32 = min(have - first, 32);
+                    if (n32 <= 16) multiply<1>(e, ad, c0, first, n32);
+                    else multiply<2>(e, ad, c0, first, n32);
+                    first += n32;
+                }
+                // fewer than 32 rows left: to the front, for the next tags
+                const int rest = have - first;
+                int keep = 0;
+                if (tid < rest) keep = sh.list[first + tid];
+                __syncthreads();
+                if (tid < rest) sh.list[tid] = keep;
+                have = rest;
+                __syncthreads();
             }
         }
     }
+};
+
+// Workgroup b runs on XCD b % 8; an expert's share one L2 for its rows.
+template <bool FP8>
+__global__ __launch_bounds__(Shrink<FP8>::threads) void k_shrink(ShrinkArgs a)
+{
+    __shared__ typename Shrink<FP8>::Shared sh;
+    const int i = blockIdx.x >> 3, e = i / a.share * 8 + (blockIdx.x & 7), y = i % a.share;
+    if (e >= a.E) return;
+    const int prev = e == 0 ? 0 : min(max(a.ends[e - 1], 0), a.rows);
+    const uint32_t st = (uint32_t(prev) + uint32_t(a.alpha) - 1u) / uint32_t(a.alpha) * uint32_t(a.alpha);
+    const int start = int(min(st, uint32_t(a.rows))), count = min(a.ends[e], a.rows) - start;
+    if (count <= 0) return;
+    Shrink<FP8> k(a, sh);
+    k.run(e, y, start, count);
 }
 
 // ------------------------------------------------------------------ tags ----
@@ -960,13 +1174,13 @@ int64_t tile_bound(const ProductPlan &p, int height)
 
 constexpr int kComputeUnits = 256;
 
-template <bool FP8, bool GATED, bool OUT8, int NB, int KS, int CS>
+template <bool FP8, bool GATED, bool OUT8, bool LOW, int NB, int KS, int CS>
 int launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
 {
-    typedef Few<FP8, GATED, OUT8, NB, KS, CS> F;
+    typedef Few<FP8, GATED, OUT8, LOW, NB, KS, CS> F;
     a.ntiles = (p.n + F::BN - 1) / F::BN;
     const unsigned grid = persistent_grid(tile_bound(p, F::rows), a.ntiles, kComputeUnits * 8);
-    hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, NB, KS, CS>), dim3(grid), dim3(F::threads), 0, st, a);
+    hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, LOW, NB, KS, CS>), dim3(grid), dim3(F::threads), 0, st, a);
     return launched();
 }
 
@@ -974,7 +1188,7 @@ int launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
 template <bool FP8, bool GATED, bool OUT8, bool LOW>
 int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
 {
-    typedef std::conditional_t<FP8, ManyFp8, ManyBf16> S;
+    typedef std::conditional_t<FP8 || LOW, ManyLow, ManyTall> S;
     typedef Many<S, FP8, GATED, OUT8, LOW> M;
     constexpr int lds = S::ST * M::stage_bytes;
     a.ntiles = (p.n + M::BN - 1) / M::BN;
@@ -989,6 +1203,24 @@ int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
 
 // Rows per expert (by the host's bound) from which the tiled product runs.
 constexpr int64_t kManyFrom = 64;
+
+template <bool LOW>
+int launch_product(const ProductPlan &p, const ProductArgs &a, bool many, hipStream_t st)
+{
+    if (many) {
+        if (!p.fp8) return p.gated ? launch_many<false, true, false, LOW>(p, a, st) : launch_many<false, false, false, LOW>(p, a, st);
+        if (p.out8) return launch_many<true, true, true, LOW>(p, a, st);
+        return p.gated ? launch_many<true, true, false, LOW>(p, a, st) : launch_many<true, false, false, LOW>(p, a, st);
+    }
+    // Workgroups of four wavefronts leave the most loads in flight per CU: 32
+    // weight rows (BF16; 64 take 133 us instead of 129 for 1024 rows over 64
+    // experts, H 2048, inner 768) or 64 (FP8: 32 take 35 us instead of 32 for the
+    // second product).  An FP8 output needs 256 weight rows, one scale block.
+    if (!p.fp8)
+        return p.gated ? launch_few<false, true, false, LOW, 2, 4, 1>(p, a, st) : launch_few<false, false, false, LOW, 2, 4, 1>(p, a, st);
+    if (p.out8) return launch_few<true, true, true, LOW, 4, 2, 4>(p, a, st);
+    return p.gated ? launch_few<true, true, false, LOW, 4, 4, 1>(p, a, st) : launch_few<true, false, false, LOW, 4, 4, 1>(p, a, st);
+}
 
 }  // namespace
 
@@ -1010,10 +1242,13 @@ int be_launch_product(const ProductPlan &p, void *stream)
         s.k = p.k;
         s.c = p.rank * (p.gated ? 2 : 1);
         s.nad = p.nad;
-        s.split = 4;
-        const unsigned grid = persistent_grid(tile_bound(p, 16), s.split, kComputeUnits * 4);
-        if (p.fp8) hipLaunchKernelGGL((k_shrink<true, 8>), dim3(grid), dim3(512), 0, st, s);
-        else hipLaunchKernelGGL((k_shrink<false, 8>), dim3(grid), dim3(512), 0, st, s);
+        // about eight workgroups per CU, all resident at once; no more per expert
+        // than it can have pairs of an adapter and 32 rows of A
+        const int pairs = std::min(p.nad, int(std::min<int64_t>(p.rows, AFD_MAX_ADAPTERS))) * ((s.c + 31) / 32);
+        s.share = std::max(1, std::min(kComputeUnits * 8 / p.E, pairs));
+        const unsigned grid = unsigned((p.E + 7) / 8 * 8 * s.share);
+        if (p.fp8) hipLaunchKernelGGL(k_shrink<true>, dim3(grid), dim3(Shrink<true>::threads), 0, st, s);
+        else hipLaunchKernelGGL(k_shrink<false>, dim3(grid), dim3(Shrink<false>::threads), 0, st, s);
         if (launched() != 0) return 1;
     }
     ProductArgs a{};
@@ -1036,28 +1271,8 @@ int be_launch_product(const ProductPlan &p, void *stream)
     a.nad = p.nad;
     a.rank = p.rank;
     // the rows' bound without what alignment alone can add
-    const int64_t per_expert = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E;
-    if (per_expert >= kManyFrom) {
-        const bool low = p.nad > 0;
-        if (!p.fp8) {
-            if (p.gated)
-                return low ? launch_many<false, true, false, true>(p, a, st) : launch_many<false, true, false, false>(p, a, st);
-            return low ? launch_many<false, false, false, true>(p, a, st) : launch_many<false, false, false, false>(p, a, st);
-        }
-        if (p.out8)
-            return low ? launch_many<true, true, true, true>(p, a, st) : launch_many<true, true, true, false>(p, a, st);
-        if (p.gated)
-            return low ? launch_many<true, true, false, true>(p, a, st) : launch_many<true, true, false, false>(p, a, st);
-        return low ? launch_many<true, false, false, true>(p, a, st) : launch_many<true, false, false, false>(p, a, st);
-    }
-    // Workgroups of four wavefronts leave the most loads in flight per CU: 32
-    // weight rows (BF16; 64 take 133 us instead of 129 for 1024 rows over 64
-    // experts, H 2048, inner 768) or 64 (FP8: 32 take 35 us instead of 32 for the
-    // second product).  An FP8 output needs 256 weight rows, one scale block.
-    if (!p.fp8)
-        return p.gated ? launch_few<false, true, false, 2, 4, 1>(p, a, st) : launch_few<false, false, false, 2, 4, 1>(p, a, st);
-    if (p.out8) return launch_few<true, true, true, 4, 2, 4>(p, a, st);
-    return p.gated ? launch_few<true, true, false, 4, 4, 1>(p, a, st) : launch_few<true, false, false, 4, 4, 1>(p, a, st);
+    const bool many = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E >= kManyFrom;
+    return p.nad > 0 ? launch_product<true>(p, a, many, st) : launch_product<false>(p, a, many, st);
 }
 
 int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *tags, int32_t *out, void *stream)

@@ -195,94 +195,100 @@ __device__ __forceinline__ int col_of(int q, int r)
 
 // Adds B t of the adapters of MB row blocks to v: per block, NQ column blocks per
 // kind of 4 consecutive columns of one row per lane.  wrow[] are the weight rows of
-// this lane's A-operand rows.  The distinct adapters number sub, sub + nsub, .. are
-// taken one after the other, the next one's B on its way meanwhile, and each lane
-// adds only its own row's, by selection, so an adapter's infinities reach no other
-// request.  t enters the matrix unit as two bf16 parts, t - hi - lo below 2^-16 of t.
+// this lane's A-operand rows.  Per 32 ranks, every row's t is loaded once (each row
+// has one adapter) and enters the matrix unit as two bf16 parts, t - hi - lo below
+// 2^-16 of t; the distinct adapters number sub, sub + nsub, .. are taken one after
+// the other, the next one's B on its way meanwhile, and each lane adds only its own
+// row's, by selection, so an adapter's infinities reach no other request.
 template <int KINDS, int NQ, int MB>
 __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, const int (&row)[MB], const int (&tag)[MB],
                                              const int (&wrow)[KINDS * NQ], f32x4 (&v)[MB][KINDS * NQ], int sub, int nsub)
 {
     const int lane = threadIdx.x & 63, g = lane >> 4;
-    uint32_t left[MB];
+    for (int j0 = 0; j0 < a.rank; j0 += 32) {
+        const int j = j0 + g * 8;
+        f32x4 t[MB][KINDS][2];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) left[i] = uint32_t(__ballot(tag[i] >= 0)) & 0xFFFFu;
-    struct Pick {
-        int ad;              // -1: none
-        uint32_t hit[MB];    // its rows
-    };
-    int skip = sub;
-    auto pick = [&]() {
-        Pick p;
-        for (;;) {
-            p.ad = -1;
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int i = MB - 1; i >= 0; --i)
-                if (left[i]) p.ad = __builtin_amdgcn_readlane(tag[i], __builtin_ctz(left[i]));
-            if (p.ad < 0) break;
+            for (int c = 0; c < KINDS; ++c)
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                p.hit[i] = uint32_t(__ballot(tag[i] == p.ad)) & 0xFFFFu;
-                left[i] &= ~p.hit[i];
+                for (int h = 0; h < 2; ++h)
+                    t[i][c][h] = tag[i] >= 0 && j < a.rank
+                                     ? *(gptr<const f32x4>)((gptr<const float>)a.t + int64_t(row[i]) * (KINDS * a.rank) + c * a.rank + j + h * 4)
+                                     : f32x4{0.f, 0.f, 0.f, 0.f};
+        uint32_t left[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) left[i] = uint32_t(__ballot(tag[i] >= 0)) & 0xFFFFu;
+        struct Pick {
+            int ad;              // -1: none
+            uint32_t hit[MB];    // its rows
+        };
+        int skip = sub;
+        auto pick = [&]() {
+            Pick p;
+            for (;;) {
+                p.ad = -1;
+#pragma unroll
+                for (int i = MB - 1; i >= 0; --i)
+                    if (left[i]) p.ad = __builtin_amdgcn_readlane(tag[i], __builtin_ctz(left[i]));
+                if (p.ad < 0) break;
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    p.hit[i] = uint32_t(__ballot(tag[i] == p.ad)) & 0xFFFFu;
+                    left[i] &= ~p.hit[i];
+                }
+                if (skip == 0) {
+                    skip = nsub - 1;
+                    break;
+                }
+                --skip;
             }
-            if (skip == 0) {
-                skip = nsub - 1;
-                break;
-            }
-            --skip;
-        }
-        return p;
-    };
-    auto load_b = [&](u32x4 (&bf)[KINDS * NQ], int ad, int j) {
-        const gptr<const uint8_t> base = (gptr<const uint8_t>)a.b + (int64_t(ad) * a.E + e) * (int64_t(a.m) * a.rank * 2);
+            return p;
+        };
+        auto load_b = [&](u32x4 (&bf)[KINDS * NQ], int ad) {
+            const gptr<const uint8_t> base = (gptr<const uint8_t>)a.b + (int64_t(ad) * a.E + e) * (int64_t(a.m) * a.rank * 2);
 #pragma unroll
-        for (int q = 0; q < KINDS * NQ; ++q)
-            bf[q] = j < a.rank ? *(gptr<const u32x4>)(base + (int64_t(wrow[q]) * a.rank + j) * 2) : u32x4{0u, 0u, 0u, 0u};
-    };
-    Pick p = pick();
-    u32x4 bf[KINDS * NQ];
-    if (p.ad >= 0) load_b(bf, p.ad, g * 8);
-    while (p.ad >= 0) {
-        const Pick next = pick();
-        u32x4 bn[KINDS * NQ];
-        if (next.ad >= 0) load_b(bn, next.ad, g * 8);
-        for (int j0 = 0; j0 < a.rank; j0 += 32) {
-            const int j = j0 + g * 8;
-            if (j0 > 0) load_b(bf, p.ad, j);
+            for (int q = 0; q < KINDS * NQ; ++q)
+                bf[q] = j < a.rank ? *(gptr<const u32x4>)(base + (int64_t(wrow[q]) * a.rank + j) * 2) : u32x4{0u, 0u, 0u, 0u};
+        };
+        Pick p = pick();
+        u32x4 bf[KINDS * NQ];
+        if (p.ad >= 0) load_b(bf, p.ad);
+        u32x4 hi[MB][KINDS], lo[MB][KINDS];
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int c = 0; c < KINDS; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float p0 = t[i][c][k / 2][k % 2 * 2], p1 = t[i][c][k / 2][k % 2 * 2 + 1];
+                    const uint32_t h0 = to_bf16(p0), h1 = to_bf16(p1);
+                    float r0 = p0 - __uint_as_float(h0 << 16), r1 = p1 - __uint_as_float(h1 << 16);
+                    if (!(fabsf(r0) < INFINITY)) r0 = 0.f;   // an infinite t has no remainder
+                    if (!(fabsf(r1) < INFINITY)) r1 = 0.f;
+                    hi[i][c][k] = h0 | (h1 << 16);
+                    lo[i][c][k] = pack_bf16(r0, r1);
+                }
+        while (p.ad >= 0) {
+            const Pick next = pick();
+            u32x4 bn[KINDS * NQ];
+            if (next.ad >= 0) load_b(bn, next.ad);
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
                 if (!p.hit[i]) continue;
                 const bool mine = tag[i] == p.ad;
-                const gptr<const float> trow = (gptr<const float>)a.t + int64_t(row[i]) * (KINDS * a.rank);
 #pragma unroll
-                for (int c = 0; c < KINDS; ++c) {
-                    u32x4 hi = {0u, 0u, 0u, 0u}, lo = hi;
-                    if (mine && j < a.rank) {
-                        const f32x4 t0 = *(gptr<const f32x4>)(trow + c * a.rank + j);
-                        const f32x4 t1 = *(gptr<const f32x4>)(trow + c * a.rank + j + 4);
+                for (int q = 0; q < KINDS * NQ; ++q) {
+                    const f32x4 d = mfma_bf16(bf[q], hi[i][q / NQ], mfma_bf16(bf[q], lo[i][q / NQ], f32x4{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float p0 = k < 2 ? t0[2 * k] : t1[2 * k - 4], p1 = k < 2 ? t0[2 * k + 1] : t1[2 * k - 3];
-                            const uint32_t h0 = to_bf16(p0), h1 = to_bf16(p1);
-                            float r0 = p0 - __uint_as_float(h0 << 16), r1 = p1 - __uint_as_float(h1 << 16);
-                            if (!(fabsf(r0) < INFINITY)) r0 = 0.f;   // an infinite t has no remainder
-                            if (!(fabsf(r1) < INFINITY)) r1 = 0.f;
-                            hi[k] = h0 | (h1 << 16);
-                            lo[k] = pack_bf16(r0, r1);
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        const f32x4 d = mfma_bf16(bf[c * NQ + q], hi, mfma_bf16(bf[c * NQ + q], lo, f32x4{0.f, 0.f, 0.f, 0.f}));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[i][c * NQ + q][k] = mine ? v[i][c * NQ + q][k] + d[k] : v[i][c * NQ + q][k];
-                    }
+                    for (int k = 0; k < 4; ++k) v[i][q][k] = mine ? v[i][q][k] + d[k] : v[i][q][k];
                 }
             }
-        }
-        p = next;
+            p = next;
 #pragma unroll
-        for (int q = 0; q < KINDS * NQ; ++q) bf[q] = bn[q];
+            for (int q = 0; q < KINDS * NQ; ++q) bf[q] = bn[q];
+        }
     }
 }
 

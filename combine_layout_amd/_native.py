@@ -30,6 +30,7 @@ MAX_SOURCES, MAX_PARTITIONS, MAX_EXPERTS, MAX_TOPK = 16, 16, 512, 32
 STATIC_SCRATCH_BYTES = 64 << 20
 AFD_ACT_NONE, AFD_ACT_SWIGLU = 0, 1
 ACTIVATIONS = {None: AFD_ACT_NONE, "swiglu": AFD_ACT_SWIGLU}
+WEIGHTS_ROWS, WEIGHTS_PACKED = 0, 1
 MAX_ADAPTERS, MAX_RANK = 65536, 128
 
 STATUS_NAMES = {0: "AFD_OK", -1: "AFD_E_ARG", -2: "AFD_E_SHAPE", -3: "AFD_E_ORDER",
@@ -61,7 +62,8 @@ class RoundInfo(ctypes.Structure):
 class ProductConfig(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("alignment", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
-                ("activation", ctypes.c_int32), ("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
+                ("activation", ctypes.c_int32), ("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("weight_layout", ctypes.c_int32)]
 
 
 class ProductWeights(ctypes.Structure):
@@ -72,7 +74,7 @@ class ProductWeights(ctypes.Structure):
 class FfnConfig(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("alignment", ctypes.c_int32), ("hidden", ctypes.c_int32),
                 ("inner", ctypes.c_int32), ("dtype", ctypes.c_int32), ("num_adapters", ctypes.c_int32),
-                ("rank", ctypes.c_int32)]
+                ("rank", ctypes.c_int32), ("weight_layout", ctypes.c_int32)]
 
 
 DISPATCH_PATHS = {0: "none", 1: "one_kernel", 2: "tiled", 3: "cached", 4: "empty", 5: "one_launch"}
@@ -107,6 +109,7 @@ SIGNATURES = {
     "afd_product_query": ([ctypes.POINTER(ProductConfig), _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
     "afd_expert_product": ([ctypes.POINTER(ProductConfig), _I64, _P, _P, _P, _P, ctypes.POINTER(ProductWeights), _P, _P,
                             _P, ctypes.c_size_t, _P], _I32),
+    "afd_pack_weights": ([ctypes.POINTER(ProductConfig), _P, _P, _P], _I32),
     "afd_ffn_query": ([ctypes.POINTER(FfnConfig), _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
     "afd_expert_ffn": ([ctypes.POINTER(FfnConfig), _I64, _P, _P, _P, _P, ctypes.POINTER(ProductWeights),
                         ctypes.POINTER(ProductWeights), _P, _P, ctypes.c_size_t, _P], _I32),

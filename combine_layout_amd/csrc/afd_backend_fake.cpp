@@ -141,9 +141,16 @@ int be_read_stall(uint32_t *, void *, int clear, int *stalled)
 
 int be_launch_product(const ProductPlan &p, void *)
 {
-    logf("product E=%d alpha=%d k=%d n=%d fp8=%d out8=%d gated=%d nad=%d rank=%d rows=%lld x=%p out=%p outs=%p t=%p", p.E,
-         p.alpha, p.k, p.n, p.fp8, p.out8, p.gated, p.nad, p.rank, static_cast<long long>(p.rows), p.x, p.out,
+    logf("product E=%d alpha=%d k=%d n=%d fp8=%d out8=%d gated=%d nad=%d rank=%d packed=%d rows=%lld x=%p out=%p outs=%p t=%p", p.E,
+         p.alpha, p.k, p.n, p.fp8, p.out8, p.gated, p.nad, p.rank, p.packed,
+         static_cast<long long>(p.rows), p.x, p.out,
          static_cast<void *>(p.outs), static_cast<void *>(p.t));
+    return g_fail;
+}
+
+int be_launch_pack(const void *w, void *out, int64_t rows, int64_t row_bytes, void *)
+{
+    logf("pack %p->%p rows=%lld row_bytes=%lld", w, out, static_cast<long long>(rows), static_cast<long long>(row_bytes));
     return g_fail;
 }
 

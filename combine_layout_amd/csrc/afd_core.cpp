@@ -272,6 +272,7 @@ afd_status check_product(const afd_product_config *c, int64_t rows)
     if (c->out_dtype != AFD_BF16 && !(c->out_dtype == AFD_FP8_E4M3 && fp8 && gated)) return AFD_E_SHAPE;
     if (c->k < 1 || c->k > (1 << 21) || c->k % (fp8 ? 128 : 64) != 0) return AFD_E_SHAPE;
     if (c->n < 1 || c->n % (fp8 && gated ? 128 : 16) != 0) return AFD_E_SHAPE;
+    if (c->weight_layout != AFD_WEIGHTS_ROWS && c->weight_layout != AFD_WEIGHTS_PACKED) return AFD_E_SHAPE;
     // byte offsets inside one expert's weights, and inside 256 rows of x, are
     // 32-bit in the kernels
     if (int64_t(c->n) * (gated ? 2 : 1) * c->k * (fp8 ? 1 : 2) >= (int64_t(1) << 31)) return AFD_E_SHAPE;
@@ -308,6 +309,7 @@ ProductPlan plan_product(const afd_product_config &c, int64_t rows, const void *
     p.fp8 = c.dtype == AFD_FP8_E4M3;
     p.out8 = c.out_dtype == AFD_FP8_E4M3;
     p.gated = c.activation == AFD_ACT_SWIGLU;
+    p.packed = c.weight_layout == AFD_WEIGHTS_PACKED;
     p.nad = c.num_adapters;
     p.rank = c.rank;
     p.rows = rows;
@@ -333,9 +335,9 @@ afd_status plan_ffn(const afd_ffn_config *c, int64_t rows, FfnPlan *f)
     if (!c || !f) return AFD_E_ARG;
     const int fp8 = c->dtype == AFD_FP8_E4M3;
     f->up = {c->num_experts, c->alignment,  c->hidden,      c->inner,       c->dtype,
-             c->dtype,       AFD_ACT_SWIGLU, c->num_adapters, c->rank};
+             c->dtype,       AFD_ACT_SWIGLU, c->num_adapters, c->rank,        c->weight_layout};
     f->down = {c->num_experts, c->alignment,  c->inner,       c->hidden,      c->dtype,
-               AFD_BF16,       AFD_ACT_NONE, c->num_adapters, c->rank};
+               AFD_BF16,       AFD_ACT_NONE, c->num_adapters, c->rank,        c->weight_layout};
     afd_status st = check_product(&f->up, rows);
     if (st == AFD_OK) st = check_product(&f->down, rows);
     if (st != AFD_OK) return st;
@@ -700,6 +702,16 @@ afd_status afd_expert_product(const afd_product_config *cfg, int64_t rows, const
     const ProductPlan p =
         plan_product(*cfg, rows, x, x_scales, ends, row_adapters, *weights, out, out_scales, workspace);
     return be_launch_product(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_pack_weights(const afd_product_config *cfg, const void *w, void *out, void *stream)
+{
+    const afd_status st = check_product(cfg, 0);
+    if (st != AFD_OK) return st;
+    if (!w || !out || w == out || !aligned(w, 16) || !aligned(out, 16)) return AFD_E_ARG;
+    const int64_t rows = int64_t(cfg->num_experts) * cfg->n * (cfg->activation == AFD_ACT_SWIGLU ? 2 : 1);
+    const int64_t row_bytes = int64_t(cfg->k) * (cfg->dtype == AFD_FP8_E4M3 ? 1 : 2);
+    return be_launch_pack(w, out, rows, row_bytes, stream) == 0 ? AFD_OK : AFD_E_HIP;
 }
 
 afd_status afd_ffn_query(const afd_ffn_config *cfg, int64_t rows, size_t *workspace_bytes)

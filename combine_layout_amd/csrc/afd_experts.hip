@@ -42,7 +42,7 @@ using lptr = __attribute__((address_space(3))) T *;
 // One lane's operand of a 128-byte step of k: two 16-byte pieces (two bf16
 // products of 32 columns, or one E4M3 product of 128).  Both operands hold the
 // same columns in the same places, so the order of the columns inside a step
-// is free; lane group g (16 lanes) takes bytes 32g .. 32g + 31 of the step.
+// is free; lane group g (16 lanes) takes pieces g and 4 + g of the step's eight.
 struct Frag {
     u32x4 p[2];
 };
@@ -179,19 +179,11 @@ struct ProductArgs {
     int n;         // columns of out
     int m;         // weight rows of an expert: n, or 2n gated
     int kb;        // bytes of a row of x and of W
+    int packed;    // W's layout
+    int wstep;     // bytes from a step of 128 bytes of a weight row to the next: 128, or 2048 packed
     int nad, rank;
     int ntiles;    // column tiles
 };
-
-// Column of A-operand row r of a wavefront's block q.  D gives lane group r / 4 the
-// rows 4(r / 4) .. + 3, so this order makes a lane's results of two blocks eight
-// consecutive columns and the four lane groups' thirty-two: one store of 16 bytes
-// per lane then writes whole 64-byte pieces of a row.  (G: blocks of one kind.)
-template <int G>
-__device__ __forceinline__ int col_of(int q, int r)
-{
-    return G == 1 ? r : (q >> 1) * 32 + (r >> 2) * 8 + (q & 1) * 4 + (r & 3);
-}
 
 // Adds B t of the adapters of MB row blocks to v: per block, NQ column blocks per
 // kind of 4 consecutive columns of one row per lane.  wrow[] are the weight rows of
@@ -339,11 +331,12 @@ struct Few {
         uint32_t wo[NB], xo[MB];
 #pragma unroll
         for (int q = 0; q < NB; ++q) {
-            const int c = min(c0 + cw * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
-            wo[q] = uint32_t(q < G ? c : a.n + c) * uint32_t(a.kb) + g * 32;
+            const int c = min(c0 + cw * (16 * G) + q % G * 16, a.n - 16) + (q < G ? 0 : a.n);   // the block's first row
+            wo[q] = uint32_t(c) * uint32_t(a.kb) + (a.packed ? lane * 16 : uint32_t(r16) * uint32_t(a.kb) + g * 16);
         }
 #pragma unroll
-        for (int i = 0; i < MB; ++i) xo[i] = uint32_t(min(i * 16 + r16, t.nrows - 1)) * uint32_t(a.kb) + g * 32;
+        for (int i = 0; i < MB; ++i) xo[i] = uint32_t(min(i * 16 + r16, t.nrows - 1)) * uint32_t(a.kb) + g * 16;
+        const uint32_t piece = a.packed ? 1024 : 64;   // from a lane's first piece of a step to its second
         f32x4 acc[MB][NB];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
@@ -356,11 +349,11 @@ struct Few {
             for (int q = 0; q < NB; ++q)
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    st.w[q].p[p] = *(gptr<const u32x4>)(wb + wo[q] + u * 128 + p * 16);
+                    st.w[q].p[p] = *(gptr<const u32x4>)(wb + (wo[q] + uint32_t(u) * uint32_t(a.wstep) + p * piece));
 #pragma unroll
             for (int i = 0; i < MB; ++i)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) st.x[i].p[p] = *(gptr<const u32x4>)(xb + xo[i] + u * 128 + p * 16);
+                for (int p = 0; p < 2; ++p) st.x[i].p[p] = *(gptr<const u32x4>)(xb + xo[i] + u * 128 + p * 64);
             if constexpr (FP8) {
                 st.s0 = wsp[u];
                 st.s1 = GATED ? wsp[(a.n / 128) * nu + u] : 0.f;
@@ -418,7 +411,7 @@ struct Few {
             }
 #pragma unroll
             for (int q = 0; q < NB; ++q) {
-                const int c = min(c0 + cw * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
+                const int c = min(c0 + cw * (16 * G) + q % G * 16 + r16, a.n - 1);
                 wrow[q] = q < G ? c : a.n + c;
             }
             add_adapters<GATED ? 2 : 1, G, MB>(a, t.e, row, tag, wrow, acc, kw, KS);
@@ -460,7 +453,7 @@ struct Few {
                 if constexpr (GATED)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[1][j];
-                const int c = c0 + s * (16 * G) + col_of<G>(q, g * 4);
+                const int c = c0 + s * (16 * G) + q * 16 + g * 4;
                 if constexpr (!OUT8) {
                     if (in && c < a.n)
                         *(gptr<u32x2>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + c) =
@@ -492,7 +485,7 @@ struct Few {
                 for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? res[o][j] / sc : 0.f;
                 int code = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
                 code = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], code, true);
-                if (in) *(gptr<int>)((gptr<uint8_t>)a.out + int64_t(row) * a.n + c0 + s * (16 * G) + col_of<G>(q, g * 4)) = code;
+                if (in) *(gptr<int>)((gptr<uint8_t>)a.out + int64_t(row) * a.n + c0 + s * (16 * G) + q * 16 + g * 4) = code;
             }
         }
         __syncthreads();   // red and amax are written again
@@ -526,7 +519,8 @@ __global__ __launch_bounds__(KS * CS * kWave) void k_product_few(ProductArgs a)
 //
 // In LDS a row's step is eight pieces of 16 bytes, piece p of row r at p ^ (r % 8):
 // the rows that one cycle of a 16-byte read touches then lie in different banks,
-// while the writes, whose order the hardware fixes, stay whole rows.
+// while the writes, whose order the hardware fixes, stay whole rows.  Packed
+// weights lie as they come, sixteen rows in the order in which the lanes read them.
 struct ManyItem {
     Tile t;
     int c0;
@@ -547,6 +541,19 @@ __device__ __forceinline__ u32x4 uniform(u32x4 v)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = uint32_t(__builtin_amdgcn_readfirstlane(int(v[i])));
     return v;
+}
+
+// A lane's four columns of blocks q and q + 1 (columns 4g .. of each) to eight of one
+// block: odd lane groups take theirs of block q + 1, even ones of block q, from
+// each other.  Afterwards a holds the first four and b the last; the result is
+// the first one's column from block q's first (n columns: half a block).
+__device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b, int n)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+    const int g = (threadIdx.x & 63) >> 4;
+    return (g & 1) * 2 * n + (g >> 1) * n;
 }
 
 // 64 lanes x 16 (or 4) bytes of buffer `r`, lane by lane at voff + soff, to LDS
@@ -589,7 +596,8 @@ struct Many {
     lptr<unsigned char> stages;
     uint32_t lds;                  // LDS address of the first stage
     int lane, g, r16, wave, wm, wn;
-    uint32_t xo[S::nx], wo[S::nw], so;     // this lane's offsets of a step's pieces
+    uint32_t xo[S::nx], wo[S::nw], so;     // this lane's offsets of a step's pieces in memory
+    int xp[2], wp[2];                      // and of its own two of a block in LDS
     int nu;
 
     // the steps' loads run ahead of the products
@@ -617,10 +625,17 @@ struct Many {
         }
 #pragma unroll
         for (int i = 0; i < S::nw; ++i) {
-            const int row = ((i * S::waves + wave) * 64 + lane) / np;
+            const int at = ((i * S::waves + wave) * 64 + lane) * 16, row = at / 128;   // in the stage's weights
             // wavefront wn's rows of the stage are its four blocks in order
-            const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + col_of<G>(q % G, row & 15);
-            wo[i] = uint32_t(q < G ? c : a.n + c) * uint32_t(a.kb) + uint32_t(((lane % np) ^ key(row)) * 16);
+            const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + q % G * 16 + (q < G ? 0 : a.n);
+            wo[i] = uint32_t(c) * uint32_t(a.kb) +
+                    (a.packed ? uint32_t(at % 2048)
+                              : uint32_t(row & 15) * uint32_t(a.kb) + uint32_t(((lane % np) ^ key(row)) * 16));
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            xp[p] = r16 * 128 + ((4 * p + g) ^ key(r16)) * 16;
+            wp[p] = a.packed ? p * 1024 + lane * 16 : xp[p];
         }
         // the first half of the wavefronts bring 64 row scales each, the others the weights' two
         if (FP8) so = wave < S::waves / 2 ? uint32_t(wave * 64 + lane) * uint32_t(nu) * 4u
@@ -658,7 +673,7 @@ struct Many {
     {
         const uint32_t at = lds + uint32_t(ahead_stage) * stage_bytes, so_u = uint32_t(ahead_u) * uint32_t(S::SB);
 #pragma unroll
-        for (int i = 0; i < S::nw; ++i) to_lds16(ahead.wr, wo[i], so_u, at + S::xbytes + uint32_t(i * S::waves + wave) * 1024u);
+        for (int i = 0; i < S::nw; ++i) to_lds16(ahead.wr, wo[i], uint32_t(ahead_u) * uint32_t(a.wstep), at + S::xbytes + uint32_t(i * S::waves + wave) * 1024u);
 #pragma unroll
         for (int i = 0; i < S::nx; ++i) to_lds16(ahead.xr, xo[i], so_u, at + uint32_t(i * S::waves + wave) * 1024u);
         if (FP8) to_lds4(ahead.sr, so, uint32_t(ahead_u) * 4u, at + S::scales + uint32_t(wave) * 256u);
@@ -679,11 +694,12 @@ struct Many {
         for (int i = 0; i < S::ST - 1; ++i) issue(it);
     }
 
-    __device__ __forceinline__ Frag read(lptr<const unsigned char> base, int row) const
+    // A block of sixteen rows, this lane's pieces of it at `at`.
+    __device__ __forceinline__ Frag read(lptr<const unsigned char> block, const int (&at)[2]) const
     {
         Frag o;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) o.p[p] = *(lptr<const u32x4>)(base + row * S::SB + (((2 * g + p) ^ key(row)) * 16));
+        for (int p = 0; p < 2; ++p) o.p[p] = *(lptr<const u32x4>)(block + at[p]);
         return o;
     }
 
@@ -701,22 +717,23 @@ struct Many {
             // it has, and every read of the stage that is loaded next is over
             asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 2) * loads) : "memory");
             issue(it);
-            const lptr<const unsigned char> xb = stages + stage * stage_bytes, wb = xb + S::xbytes + wn * 64 * S::SB;
+            const lptr<const unsigned char> st = stages + stage * stage_bytes, xb = st + wm * MB * 2048,
+                                            wb = st + S::xbytes + wn * 4 * 2048;
             Frag wf[4], xf[MB];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) wf[q] = read(wb, q * 16 + r16);
+            for (int q = 0; q < 4; ++q) wf[q] = read(wb + q * 2048, wp);
             float s0 = 0.f, s1 = 0.f, sx[MB];
-            const lptr<const float> sc = (lptr<const float>)(xb + S::scales);
+            const lptr<const float> sc = (lptr<const float>)(st + S::scales);
             if (FP8) {
                 s0 = sc[S::waves * 32 + (GATED ? 0 : wn >> 1)];
                 s1 = sc[S::waves * 32 + 1];
 #pragma unroll
                 for (int i = 0; i < MB; ++i) sx[i] = sc[row + i * 16];
             }
-            xf[0] = read(xb, row);
+            xf[0] = read(xb, xp);
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
-                if (i + 1 < MB) xf[i + 1] = read(xb, row + (i + 1) * 16);
+                if (i + 1 < MB) xf[i + 1] = read(xb + (i + 1) * 2048, xp);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -740,7 +757,6 @@ struct Many {
     template <int MB>
     __device__ __forceinline__ void finish(const Tile &t, int c0, f32x4 (&acc)[MB][4]) const
     {
-        const int cw = c0 + wn * (16 * G) + g * 8;   // this lane's first column
         if constexpr (LOW) {
             int row[MB], tag[MB], wrow[4];
 #pragma unroll
@@ -752,7 +768,7 @@ struct Many {
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int c = min(c0 + wn * (16 * G) + col_of<G>(q % G, r16), a.n - 1);
+                const int c = min(c0 + wn * (16 * G) + q % G * 16 + r16, a.n - 1);
                 wrow[q] = q < G ? c : a.n + c;
             }
             add_adapters<GATED ? 2 : 1, G, MB>(a, t.e, row, tag, wrow, acc, 0, 1);
@@ -769,12 +785,18 @@ struct Many {
                     for (int j = 0; j < 4; ++j) acc[i][q][j] = silu(acc[i][q][j]) * acc[i][q + G][j];
             if constexpr (!OUT8) {
 #pragma unroll
-                for (int h = 0; h < G / 2; ++h)
-                    if (in && cw + h * 32 < a.n)
-                        *(gptr<u32x4>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + cw + h * 32) =
-                            u32x4{pack_bf16(acc[i][2 * h][0], acc[i][2 * h][1]), pack_bf16(acc[i][2 * h][2], acc[i][2 * h][3]),
-                                  pack_bf16(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
-                                  pack_bf16(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
+                for (int h = 0; h < G / 2; ++h) {
+                    uint32_t v[2][2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        v[q][0] = pack_bf16(acc[i][2 * h + q][0], acc[i][2 * h + q][1]);
+                        v[q][1] = pack_bf16(acc[i][2 * h + q][2], acc[i][2 * h + q][3]);
+                    }
+                    const int c = c0 + wn * (16 * G) + h * 32 + pair_up(v[0][0], v[1][0], 8);
+                    pair_up(v[0][1], v[1][1], 8);
+                    if (in && c < a.n)
+                        *(gptr<u32x4>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + c) = u32x4{v[0][0], v[0][1], v[1][0], v[1][1]};
+                }
             } else {
                 float v = 0.f;
 #pragma unroll
@@ -798,19 +820,20 @@ struct Many {
 #pragma unroll
                 for (int w = 1; w < S::WN; ++w) v = fmaxf(v, amax[w * S::rows + r]);
                 const float sc = v / 448.0f;
-                if (r < t.nrows) {
+                {
                     const int64_t row = t.row0 + r;
-                    if (wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
-                    u32x2 code;
+                    if (r < t.nrows && wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
+                    uint32_t code[2];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float d[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? acc[i][q][j] / sc : 0.f;
-                        int c = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
+                        const int c = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
                         code[q] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], c, true));
                     }
-                    *(gptr<u32x2>)((gptr<uint8_t>)a.out + row * a.n + cw) = code;
+                    const int c = c0 + wn * 32 + pair_up(code[0], code[1], 8);
+                    if (r < t.nrows) *(gptr<u32x2>)((gptr<uint8_t>)a.out + row * a.n + c) = u32x2{code[0], code[1]};
                 }
             }
             // (amax is written again behind the next item's step barriers)
@@ -1137,6 +1160,27 @@ __global__ __launch_bounds__(Shrink<FP8>::threads) void k_shrink(ShrinkArgs a)
     k.run(e, y, start, count);
 }
 
+// --------------------------------------------------------------- packing ----
+
+struct PackArgs {
+    const u32x4 *w;
+    u32x4 *out;
+    int64_t n;       // 16-byte pieces of all experts
+    int pieces;      // of a row
+};
+
+// One 16-byte piece per thread and turn, in the order of the packed weights
+// (m is a multiple of 16, so groups of sixteen rows do not cross experts).
+__global__ __launch_bounds__(256) void k_pack(PackArgs a)
+{
+    const int64_t group = int64_t(a.pieces) * 16;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < a.n; i += int64_t(gridDim.x) * 256) {
+        const int64_t gr = i / group;
+        const int in = int(i - gr * group), step = in >> 7, piece = in >> 4 & 7, row = in & 15;
+        a.out[i] = a.w[gr * group + int64_t(row) * a.pieces + step * 8 + piece];
+    }
+}
+
 // ------------------------------------------------------------------ tags ----
 
 struct TagArgs {
@@ -1274,11 +1318,21 @@ int be_launch_product(const ProductPlan &p, void *stream)
     a.n = p.n;
     a.m = p.n * (p.gated ? 2 : 1);
     a.kb = p.k * (p.fp8 ? 1 : 2);
+    a.packed = p.packed;
+    a.wstep = p.packed ? 2048 : 128;
     a.nad = p.nad;
     a.rank = p.rank;
     // the rows' bound without what alignment alone can add
     const bool many = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E >= kManyFrom;
     return p.nad > 0 ? launch_product<true>(p, a, many, st) : launch_product<false>(p, a, many, st);
+}
+
+int be_launch_pack(const void *w, void *out, int64_t rows, int64_t row_bytes, void *stream)
+{
+    PackArgs a{static_cast<const u32x4 *>(w), static_cast<u32x4 *>(out), rows * row_bytes / 16, int(row_bytes / 16)};
+    const int64_t blocks = std::min<int64_t>((a.n + 255) / 256, kComputeUnits * 32);
+    hipLaunchKernelGGL(k_pack, dim3(unsigned(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+    return launched();
 }
 
 int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *tags, int32_t *out, void *stream)

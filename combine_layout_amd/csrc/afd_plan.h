@@ -185,7 +185,7 @@ inline int layout_tiles(const RoundPlan &p, TileRec *out)
 // addresses recorded from the caller.
 struct ProductPlan {
     int E = 0, alpha = 1, k = 0, n = 0;
-    bool fp8 = false, out8 = false, gated = false;
+    bool fp8 = false, out8 = false, gated = false, packed = false;
     int nad = 0, rank = 0;           // adapters (0: none) and their rank
     int64_t rows = 0;
     const void *x = nullptr;
@@ -218,6 +218,8 @@ int be_read_error(uint64_t *dev_err, void *stream, int clear, uint64_t *word);
 int be_read_stall(uint32_t *dev_sync, void *stream, int clear, int *stalled);
 // A grouped product: with adapters a launch for A x, then the product.
 int be_launch_product(const ProductPlan &p, void *stream);
+// Row-major weight rows (of all experts) into the packed order.
+int be_launch_pack(const void *w, void *out, int64_t rows, int64_t row_bytes, void *stream);
 // tags[s][t] to the receive rows of partition f, from the round's slot map.
 int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *tags, int32_t *out, void *stream);
 int be_device_sync();

@@ -413,6 +413,15 @@ typedef enum {
     AFD_ACT_SWIGLU = 1  /* W holds n gate rows, then n up rows: y = g / (1 + exp(-g)) * u */
 } afd_activation;
 
+/*
+ * How W lies in memory: row by row, or packed (afd_pack_weights) in the order in
+ * which the products read it: of every sixteen rows, the first 16 bytes of each,
+ * then the next 16 of each, and so on; byte b of row r of an expert with rows of kb
+ * bytes at (r / 16) * 16 * kb + (b / 16) * 256 + (r % 16) * 16 + b % 16.  Same size, same
+ * results; every load reads one run of 1024 bytes.  The other arrays are row by row.
+ */
+typedef enum { AFD_WEIGHTS_ROWS = 0, AFD_WEIGHTS_PACKED = 1 } afd_weight_layout;
+
 #define AFD_MAX_ADAPTERS 65536
 #define AFD_MAX_RANK 128
 
@@ -435,6 +444,7 @@ typedef enum {
  *   num_adapters  0, or the number of adapters, at most AFD_MAX_ADAPTERS
  *   rank          of every adapter, a multiple of 8 up to AFD_MAX_RANK (smaller
  *                 ones are padded with zero rows of A); 0 without adapters
+ *   weight_layout afd_weight_layout
  * One expert's W may hold at most 2^31 - 1 bytes; rows is below 2^24.  Sums
  * are float32; a BF16 output is rounded once.
  */
@@ -448,6 +458,7 @@ typedef struct {
     int32_t activation; /* afd_activation */
     int32_t num_adapters;
     int32_t rank;
+    int32_t weight_layout; /* afd_weight_layout */
 } afd_product_config;
 
 /*
@@ -494,6 +505,14 @@ afd_status afd_expert_product(const afd_product_config *cfg, int64_t rows, const
                               void *out, float *out_scales, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * afd_pack_weights: W of a product (row by row) into its packed order, once, for
+ * calls with AFD_WEIGHTS_PACKED.  `out` is device memory of W's size that does
+ * not overlap it; cfg->weight_layout does not matter.  Enqueued on `stream`.
+ * Errors: AFD_E_ARG, AFD_E_SHAPE, AFD_E_HIP.
+ */
+afd_status afd_pack_weights(const afd_product_config *cfg, const void *w, void *out, void *stream);
+
+/*
  * The experts' network: h = swiglu(x Wup^T) [rows, inner], out = h Wdown^T
  * [rows, hidden] BF16, each product as above, both with the adapters' pairs
  * when num_adapters > 0.  h is kept in the workspace in the rows' format:
@@ -508,6 +527,7 @@ typedef struct {
     int32_t dtype; /* afd_dtype of x and the weights */
     int32_t num_adapters;
     int32_t rank;
+    int32_t weight_layout; /* afd_weight_layout, of both weights */
 } afd_ffn_config;
 
 /* afd_ffn_query: workspace bytes of afd_expert_ffn; errors as afd_product_query. */

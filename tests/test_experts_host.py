@@ -25,7 +25,7 @@ def log(lib):
 
 
 def pcfg(**kw):
-    c = dict(num_experts=4, alignment=16, k=256, n=128, dtype=0, out_dtype=0, activation=0, num_adapters=0, rank=0)
+    c = dict(num_experts=4, alignment=16, k=256, n=128, dtype=0, out_dtype=0, activation=0, num_adapters=0, rank=0, weight_layout=0)
     c.update(kw)
     return nat.ProductConfig(**c)
 
@@ -57,14 +57,15 @@ LOW = dict(num_adapters=3, rank=16)
 
 @pytest.mark.parametrize("kw", [dict(), dict(k=64, n=16), dict(activation=1, n=48), dict(dtype=1, n=16), FP8G,
                                 dict(FP8G, out_dtype=1), LOW, dict(FP8G, out_dtype=1, **LOW),
-                                dict(num_adapters=65536, rank=128), dict(num_experts=512), dict(alignment=2 ** 31 - 1)])
+                                dict(num_adapters=65536, rank=128), dict(num_experts=512), dict(alignment=2 ** 31 - 1),
+                                dict(weight_layout=1)])
 def test_accepted(lib, kw):
     log(lib)
     c = pcfg(**kw)
     assert call(lib, c) == 0
     lines = log(lib)
     assert len(lines) == 1 and lines[0].startswith(f"product E={c.num_experts} alpha={c.alignment} k={c.k} n={c.n} ")
-    assert f"nad={c.num_adapters} rank={c.rank} rows=100" in lines[0]
+    assert f"nad={c.num_adapters} rank={c.rank} packed={c.weight_layout} rows=100" in lines[0]
 
 
 @pytest.mark.parametrize("kw", [
@@ -73,7 +74,7 @@ def test_accepted(lib, kw):
     dict(dtype=1, out_dtype=1), dict(FP8G, out_dtype=2), dict(activation=1, out_dtype=1), dict(FP8G, n=64),
     dict(num_adapters=-1), dict(num_adapters=3), dict(rank=16), dict(LOW, rank=4), dict(LOW, rank=20), dict(LOW, rank=136),
     dict(num_adapters=65537, rank=16), dict(k=1 << 20, n=1 << 10), dict(k=1 << 19, n=1 << 10, activation=1),
-    dict(n=2 ** 31 - 16)])
+    dict(n=2 ** 31 - 16), dict(weight_layout=2), dict(weight_layout=-1)])
 def test_shapes_refused(lib, kw):
     log(lib)
     c = pcfg(**kw)
@@ -124,6 +125,19 @@ def test_workspace(lib):
         assert call(lib, c, rows=1000, wsb=need.value - 1) == nat.AFD_E_CAPACITY
         assert log(lib) == []
         assert call(lib, c, rows=1000, wsb=need.value) == 0
+
+
+def test_pack(lib):
+    log(lib)
+    c = pcfg(activation=1, n=48, k=320)
+    w, out = 9 << 20, 30 << 20
+    assert lib.afd_pack_weights(ctypes.byref(c), w, out, None) == 0
+    assert log(lib) == [f"pack {hex(w)}->{hex(out)} rows={4 * 96} row_bytes=640"]
+    for a, b in ((None, out), (w, None), (w, w), (w + 8, out), (w, out + 4)):
+        assert lib.afd_pack_weights(ctypes.byref(c), a, b, None) == nat.AFD_E_ARG
+    assert lib.afd_pack_weights(ctypes.byref(pcfg(k=100)), w, out, None) == nat.AFD_E_SHAPE
+    assert lib.afd_pack_weights(None, w, out, None) == nat.AFD_E_ARG
+    assert log(lib) == []
 
 
 def fcfg(**kw):

@@ -86,6 +86,28 @@ def test_product(shape, dtype, gated, k, n):
     _check(got, want, ref.rounded(want, tol), live, f"{shape} {dtype}")
 
 
+@pytest.mark.parametrize("shape", ["edges", "large"])
+@pytest.mark.parametrize("dtype,gated,k,n", [("bf16", False, 320, 144), ("bf16", True, 192, 80), ("fp8", False, 384, 272),
+                                             ("fp8", True, 256, 256)])
+def test_packed_weights_give_the_same_bits(shape, dtype, gated, k, n):
+    afd = _afd()
+    _print("packed", shape, dtype, gated, k, n)
+    counts, alpha = COUNTS[shape]
+    c = ref.make(11, len(counts), counts, alpha, k, n * (2 if gated else 1), dtype, gated=gated)
+    w = _dev(c["w"])
+    p = afd.pack_weights(w)
+    # byte b of row r at (r / 16) * 16 * kb + (b / 16) * 256 + (r % 16) * 16 + b % 16
+    E, m = w.shape[:2]
+    rows = w.view(torch.uint8).reshape(E, m // 16, 16, k * w.element_size() // 16, 16)
+    assert torch.equal(p.data, rows.permute(0, 1, 3, 2, 4).reshape(-1))
+    kw = dict(alignment=alpha, x_scales=_dev(c["xs"]), weight_scales=_dev(c["ws"]), activation="swiglu" if gated else None)
+    x, ends = _dev(c["x"]), torch.tensor(c["ends"], dtype=torch.int32).cuda()
+    a, b = (torch.full((c["rows"], n), FILL, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    afd.expert_product(x, ends, w, out=a, **kw)
+    afd.expert_product(x, ends, p, out=b, **kw)
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("shape", ["one_row", "edges", "aligned", "large", "many"])
 @pytest.mark.parametrize("k,n,S", [(256, 128, 0), (384, 384, 0), (256, 256, 3)])
 def test_product_fp8_out(shape, k, n, S):

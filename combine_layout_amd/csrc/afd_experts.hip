@@ -67,7 +67,8 @@ __device__ __forceinline__ uint32_t to_bf16(float v)
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return to_bf16(lo) | (to_bf16(hi) << 16); }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+// g / (1 + exp(-g)); the reciprocal is the hardware's, off by one float32 step.
+__device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // ------------------------------------------------------------- row tiles ----
 
@@ -127,22 +128,23 @@ __device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int
     if (lane == kWave - 1) s.first[E] = sum;
 }
 
-// Tile t (t below s.first[E]) and its expert: the last one whose first tile is
-// at or before t (experts without tiles share their successor's).
+// Item `at` of the tiles times `nt` column tiles: an expert's items are together,
+// and of these the row tiles of one column tile, so that the workgroups that read
+// the same weights run at the same time.  The expert is the last one whose first
+// item is at or before `at`, found by counting over the lanes of a wavefront.
 template <int MAX, int STEP>
-__device__ __forceinline__ Tile find_tile(const Tiles &s, int E, int t)
+__device__ __forceinline__ Tile find_tile(const Tiles &s, int E, int nt, int at, int &column)
 {
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (s.first[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    const int count = s.count[lo], h = tile_height<MAX, STEP>(count), done = (t - s.first[lo]) * h;
+    const int lane = threadIdx.x & 63, t = at / nt;
+    int e = -1;
+    for (int i = 0; i < E; i += kWave) e += __popcll(__ballot(i + lane < E && s.first[min(i + lane, E)] <= t));
+    const int first = s.first[e], row_tiles = s.first[e + 1] - first, in = at - first * nt, col = in / row_tiles;
+    const int count = s.count[e], h = tile_height<MAX, STEP>(count), done = (in - col * row_tiles) * h;
     Tile r;
-    r.e = __builtin_amdgcn_readfirstlane(lo);
-    r.row0 = __builtin_amdgcn_readfirstlane(s.start[lo] + done);
+    r.e = __builtin_amdgcn_readfirstlane(e);
+    r.row0 = __builtin_amdgcn_readfirstlane(s.start[e] + done);
     r.nrows = __builtin_amdgcn_readfirstlane(min(h, count - done));
+    column = __builtin_amdgcn_readfirstlane(col);
     return r;
 }
 
@@ -475,14 +477,14 @@ struct Few {
             float m = 0.f;
 #pragma unroll
             for (int w = 0; w < waves; ++w) m = fmaxf(m, sh.amax[w][r16]);
-            const float sc = m / 448.0f;
+            const float sc = m / 448.0f, inv = sc > 0.f ? 1.0f / sc : 0.f;
             if (in && wave == 0 && g == 0) ((gptr<float>)a.outs)[int64_t(row) * (a.n / 128) + c0 / 128] = sc;
 #pragma unroll
             for (int o = 0; o < own; ++o) {
                 const int idx = o * waves + wave, s = idx / G, q = idx - s * G;
                 float d[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? res[o][j] / sc : 0.f;
+                for (int j = 0; j < 4; ++j) d[j] = res[o][j] * inv;
                 int code = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
                 code = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], code, true);
                 if (in) *(gptr<int>)((gptr<uint8_t>)a.out + int64_t(row) * a.n + c0 + s * (16 * G) + q * 16 + g * 4) = code;
@@ -501,9 +503,9 @@ __global__ __launch_bounds__(KS * CS * kWave) void k_product_few(ProductArgs a)
     __syncthreads();
     F f(a, sh);
     for (Items it = my_items(sh.tiles.first[a.E] * a.ntiles); it.at < it.end; it.at += it.step) {
-        const int tile = it.at / a.ntiles;
-        const Tile t = find_tile<F::rows, 16>(sh.tiles, a.E, tile);
-        const int c0 = (it.at - tile * a.ntiles) * F::BN;
+        int c0;
+        const Tile t = find_tile<F::rows, 16>(sh.tiles, a.E, a.ntiles, it.at, c0);
+        c0 *= F::BN;
         if (t.nrows <= 16) f.template run<1>(t, c0);
         else f.template run<2>(t, c0);
     }
@@ -644,9 +646,9 @@ struct Many {
 
     __device__ __forceinline__ Tile tile_of(int at, int &c0) const
     {
-        const int tile = at / a.ntiles;
-        c0 = (at - tile * a.ntiles) * BN;
-        return find_tile<S::rows, 16 * S::WM>(tiles, a.E, tile);
+        const Tile t = find_tile<S::rows, 16 * S::WM>(tiles, a.E, a.ntiles, at, c0);
+        c0 *= BN;
+        return t;
     }
 
     __device__ __forceinline__ void load_item(int at, bool live)
@@ -819,7 +821,7 @@ struct Many {
                 float v = amax[r];
 #pragma unroll
                 for (int w = 1; w < S::WN; ++w) v = fmaxf(v, amax[w * S::rows + r]);
-                const float sc = v / 448.0f;
+                const float sc = v / 448.0f, inv = sc > 0.f ? 1.0f / sc : 0.f;
                 {
                     const int64_t row = t.row0 + r;
                     if (r < t.nrows && wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
@@ -828,7 +830,7 @@ struct Many {
                     for (int q = 0; q < 2; ++q) {
                         float d[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) d[j] = sc > 0.f ? acc[i][q][j] / sc : 0.f;
+                        for (int j = 0; j < 4; ++j) d[j] = acc[i][q][j] * inv;
                         const int c = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
                         code[q] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], c, true));
                     }
@@ -1147,7 +1149,7 @@ struct Shrink {
 
 // Workgroup b runs on XCD b % 8; an expert's share one L2 for its rows.
 template <bool FP8>
-__global__ __launch_bounds__(Shrink<FP8>::threads) void k_shrink(ShrinkArgs a)
+__global__ __launch_bounds__(Shrink<FP8>::threads, FP8 ? 2 : 4) void k_shrink(ShrinkArgs a)
 {
     __shared__ typename Shrink<FP8>::Shared sh;
     const int i = blockIdx.x >> 3, e = i / a.share * 8 + (blockIdx.x & 7), y = i % a.share;

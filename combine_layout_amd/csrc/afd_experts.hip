@@ -19,7 +19,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "afd_plan.h"
 
@@ -94,13 +93,12 @@ __device__ __forceinline__ int tile_height(int count)
     return n <= 1 ? MAX : ((count + n - 1) / n + STEP - 1) / STEP * STEP;
 }
 
-// Wavefront 0 of the workgroup; the caller places a barrier behind it.
-template <int MAX>
-__device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int rows)
+// The experts' rows, by wavefront 0; returns the rows and the experts that have
+// any, in every lane.
+__device__ int2 read_spans(Tiles &s, const int32_t *ends, int E, int alpha, int rows)
 {
-    const int lane = threadIdx.x;
-    const int per = (E + kWave - 1) / kWave, lo = lane * per;
-    int mine = 0;
+    const int lane = threadIdx.x, per = (E + kWave - 1) / kWave, lo = lane * per;
+    int2 n = {0, 0};
     for (int i = 0; i < per; ++i) {
         const int e = lo + i;
         if (e >= E) break;
@@ -111,19 +109,32 @@ __device__ void build_tiles(Tiles &s, const int32_t *ends, int E, int alpha, int
         const int count = max(end - start, 0);
         s.start[e] = start;
         s.count[e] = count;
-        mine += (count + MAX - 1) / MAX;
+        n.x += count;
+        n.y += count > 0;
     }
+    for (int d = 1; d < kWave; d *= 2) {
+        n.x += __shfl_xor(n.x, d);
+        n.y += __shfl_xor(n.y, d);
+    }
+    return n;
+}
+
+// The tiles of the spans, by wavefront 0; the caller places a barrier behind it.
+template <int MAX>
+__device__ void build_tiles(Tiles &s, int E)
+{
+    const int lane = threadIdx.x, per = (E + kWave - 1) / kWave, lo = lane * per;
+    int mine = 0;
+    for (int i = 0; i < per && lo + i < E; ++i) mine += (s.count[lo + i] + MAX - 1) / MAX;
     int sum = mine;
     for (int d = 1; d < kWave; d *= 2) {
         const int o = __shfl_up(sum, d);
         if (lane >= d) sum += o;
     }
     int run = sum - mine;
-    for (int i = 0; i < per; ++i) {
-        const int e = lo + i;
-        if (e >= E) break;
-        s.first[e] = run;
-        run += (s.count[e] + MAX - 1) / MAX;
+    for (int i = 0; i < per && lo + i < E; ++i) {
+        s.first[lo + i] = run;
+        run += (s.count[lo + i] + MAX - 1) / MAX;
     }
     if (lane == kWave - 1) s.first[E] = sum;
 }
@@ -499,7 +510,10 @@ __global__ __launch_bounds__(KS * CS * kWave) void k_product_few(ProductArgs a)
 {
     typedef Few<FP8, GATED, OUT8, LOW, NB, KS, CS> F;
     __shared__ typename F::Shared sh;
-    if (threadIdx.x < kWave) build_tiles<F::rows>(sh.tiles, a.ends, a.E, a.alpha, a.rows);
+    if (threadIdx.x < kWave) {
+        read_spans(sh.tiles, a.ends, a.E, a.alpha, a.rows);
+        build_tiles<F::rows>(sh.tiles, a.E);
+    }
     __syncthreads();
     F f(a, sh);
     for (Items it = my_items(sh.tiles.first[a.E] * a.ntiles); it.at < it.end; it.at += it.step) {
@@ -843,15 +857,11 @@ struct Many {
     }
 };
 
+// All items of a workgroup, in tiles of shape S.
 template <class S, bool FP8, bool GATED, bool OUT8, bool LOW>
-__global__ __launch_bounds__(S::threads, 2) void k_product_many(ProductArgs a)
+__device__ __forceinline__ void run_many(const ProductArgs &a, Tiles &tiles, float *amax, lptr<unsigned char> stages)
 {
-    extern __shared__ __align__(16) unsigned char stages[];
-    __shared__ Tiles tiles;
-    __shared__ float amax[OUT8 ? S::WN * S::rows : 1];
-    if (threadIdx.x < kWave) build_tiles<S::rows>(tiles, a.ends, a.E, a.alpha, a.rows);
-    __syncthreads();
-    Many<S, FP8, GATED, OUT8, LOW> k(a, tiles, amax, (lptr<unsigned char>)stages);
+    Many<S, FP8, GATED, OUT8, LOW> k(a, tiles, amax, stages);
     Items it = my_items(tiles.first[a.E] * a.ntiles);
     if (it.at >= it.end) return;
     const Items all = it;
@@ -884,11 +894,42 @@ __global__ __launch_bounds__(S::threads, 2) void k_product_many(ProductArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may come after the LDS is another workgroup's
 }
 
-// One workgroup per CU: 256 x 256 tiles and two stages, or 128 x 256 and three
-// where the registers of 256 rows are not there: FP8 holds the sums of one scale
-// block beside the scaled ones, the adapters theirs.
-typedef Shape<2, 4, 8, 2> ManyTall;
-typedef Shape<2, 4, 4, 3> ManyLow;
+// One workgroup per CU: 128 x 256 tiles with three stages, or 256 x 256 with two.
+// The taller ones read and move less per product, the others wait less for the
+// weights and leave fewer CUs idle at the end; FP8 (which holds the sums of one scale
+// block beside the scaled ones) and the adapters have no registers for 256 rows.
+typedef Shape<2, 4, 4, 3> Low;
+typedef Shape<2, 4, 8, 2> Tall;
+
+// Rows per expert (of those that have any) from which BF16 products take the tall tiles.
+// (64 experts, H 2048, inner 768: at 256 rows 259 us instead of 228, at 320 258 and
+// 262, at 384 275 and 326, at 512 378 and 406.)
+constexpr int kTallFrom = 320;
+
+template <bool FP8, bool GATED, bool OUT8, bool LOW>
+__global__ __launch_bounds__(Low::threads, 2) void k_product_many(ProductArgs a)
+{
+    extern __shared__ __align__(16) unsigned char stages[];
+    __shared__ Tiles tiles;
+    __shared__ float amax[OUT8 ? Low::WN * Low::rows : 1];
+    __shared__ int tall;
+    constexpr bool both = !FP8 && !LOW;
+    if (threadIdx.x < kWave) {
+        const int2 n = read_spans(tiles, a.ends, a.E, a.alpha, a.rows);
+        const bool t = both && int64_t(n.x) >= int64_t(kTallFrom) * n.y;
+        if (t) build_tiles<Tall::rows>(tiles, a.E);
+        else build_tiles<Low::rows>(tiles, a.E);
+        if (threadIdx.x == 0) tall = t;
+    }
+    __syncthreads();
+    if constexpr (both) {
+        if (__builtin_amdgcn_readfirstlane(tall)) {
+            run_many<Tall, FP8, GATED, OUT8, LOW>(a, tiles, amax, (lptr<unsigned char>)stages);
+            return;
+        }
+    }
+    run_many<Low, FP8, GATED, OUT8, LOW>(a, tiles, amax, (lptr<unsigned char>)stages);
+}
 
 // -------------------------------------------------------------- adapters ----
 
@@ -1240,21 +1281,24 @@ int launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
 template <bool FP8, bool GATED, bool OUT8, bool LOW>
 int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
 {
-    typedef std::conditional_t<FP8 || LOW, ManyLow, ManyTall> S;
-    typedef Many<S, FP8, GATED, OUT8, LOW> M;
-    constexpr int lds = S::ST * M::stage_bytes;
+    typedef Many<Low, FP8, GATED, OUT8, LOW> M;
+    constexpr int lds = std::max(Low::ST * M::stage_bytes, Tall::ST * Tall::scales);
+    static_assert(Low::threads == Tall::threads, "one launch");
     a.ntiles = (p.n + M::BN - 1) / M::BN;
-    static const hipError_t set =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(&k_product_many<S, FP8, GATED, OUT8, LOW>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_product_many<FP8, GATED, OUT8, LOW>),
+                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (set != hipSuccess) return 1;
-    const unsigned grid = persistent_grid(tile_bound(p, S::rows), a.ntiles, kComputeUnits);
-    hipLaunchKernelGGL((k_product_many<S, FP8, GATED, OUT8, LOW>), dim3(grid), dim3(S::threads), lds, st, a);
+    const unsigned grid = persistent_grid(tile_bound(p, Low::rows), a.ntiles, kComputeUnits);
+    hipLaunchKernelGGL((k_product_many<FP8, GATED, OUT8, LOW>), dim3(grid), dim3(Low::threads), lds, st, a);
     return launched();
 }
 
-// Rows per expert (by the host's bound) from which the tiled product runs.
-constexpr int64_t kManyFrom = 64;
+// Rows per expert (by the host's bound, which is up to twice what comes) from which
+// the tiled product runs.  64 experts, H 2048, inner 768, BF16 network: with one row
+// each 138 us few and 142 us tiled, with 8 113 and 110, with 16 122 and 112, with 32
+// 169 and 116; FP8 with 16 75 and 68.  With adapters (32 of rank 16) the few-row
+// kernel, whose wavefronts share a tile's adapters, is level at 16 (197 and 200).
+constexpr int64_t kManyFrom = 8, kManyFromLow = 64;
 
 template <bool LOW>
 int launch_product(const ProductPlan &p, const ProductArgs &a, bool many, hipStream_t st)
@@ -1325,7 +1369,7 @@ int be_launch_product(const ProductPlan &p, void *stream)
     a.nad = p.nad;
     a.rank = p.rank;
     // the rows' bound without what alignment alone can add
-    const bool many = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E >= kManyFrom;
+    const bool many = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E >= (p.nad > 0 ? kManyFromLow : kManyFrom);
     return p.nad > 0 ? launch_product<true>(p, a, many, st) : launch_product<false>(p, a, many, st);
 }
 

@@ -232,21 +232,22 @@ class Buffer:
         if len(tags) != self.N:
             raise ValueError("tags must hold one tensor per source")
         ptrs = (ctypes.c_void_p * self.N)()
+        dev = received.weights.device
         for s, t in enumerate(tags):
             T = self._T[s]
             if T == 0:
                 continue
             if t is None or t.dtype != torch.int32 or tuple(t.shape) != (T,) or not t.is_contiguous() or \
-                    t.device != self.device:
+                    t.device != dev:
                 raise ValueError("tags must be contiguous int32 [T] tensors on the buffer's device")
             ptrs[s] = t.data_ptr()
         n = received.receive_rows
         if out is None:
-            out = torch.full((n,), -1, dtype=torch.int32, device=self.device)
+            out = torch.full((n,), -1, dtype=torch.int32, device=dev)
         elif out.dtype != torch.int32 or tuple(out.shape) != (n,) or not out.is_contiguous() or \
-                out.device != self.device:
+                out.device != dev:
             raise ValueError("out must be contiguous int32 [receive_rows] on the buffer's device")
-        with _experts.on_device(self.device):
+        with _experts.on_device(dev):
             st = self.lib.afd_worker_tags(self.ctx, f, ptrs, _ptr(out), n, ctypes.byref(received.receipt),
                                           _stream(self.device))
         nat.check(st, "worker_tags")

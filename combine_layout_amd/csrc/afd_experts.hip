@@ -19,6 +19,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "afd_plan.h"
 
@@ -68,6 +70,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return to_bf
 
 // g / (1 + exp(-g)); the reciprocal is the hardware's, off by one float32 step.
 __device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// Scale of a block of E4M3 codes with the largest value m, and the factor to the
+// codes.  A scale below float32's smallest normal number counts as zero: its
+// reciprocal would be infinite.
+__device__ __forceinline__ float scale_of(float m, float &inv)
+{
+    const float s = m / 448.0f;
+    if (s < 0x1p-126f) {
+        inv = 0.f;
+        return 0.f;
+    }
+    inv = 1.0f / s;
+    return s;
+}
+
+// Four values times inv as E4M3 codes, nearest even.
+__device__ __forceinline__ uint32_t codes_of(const f32x4 &v, float inv)
+{
+    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, c, true));
+}
 
 // ------------------------------------------------------------- row tiles ----
 
@@ -488,17 +511,14 @@ struct Few {
             float m = 0.f;
 #pragma unroll
             for (int w = 0; w < waves; ++w) m = fmaxf(m, sh.amax[w][r16]);
-            const float sc = m / 448.0f, inv = sc > 0.f ? 1.0f / sc : 0.f;
+            float inv;
+            const float sc = scale_of(m, inv);
             if (in && wave == 0 && g == 0) ((gptr<float>)a.outs)[int64_t(row) * (a.n / 128) + c0 / 128] = sc;
 #pragma unroll
             for (int o = 0; o < own; ++o) {
                 const int idx = o * waves + wave, s = idx / G, q = idx - s * G;
-                float d[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] = res[o][j] * inv;
-                int code = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
-                code = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], code, true);
-                if (in) *(gptr<int>)((gptr<uint8_t>)a.out + int64_t(row) * a.n + c0 + s * (16 * G) + q * 16 + g * 4) = code;
+                const uint32_t code = codes_of(res[o], inv);
+                if (in) *(gptr<uint32_t>)((gptr<uint8_t>)a.out + int64_t(row) * a.n + c0 + s * (16 * G) + q * 16 + g * 4) = code;
             }
         }
         __syncthreads();   // red and amax are written again
@@ -543,33 +563,28 @@ struct ManyItem {
     u32x4 xr, wr, sr;   // buffer descriptors of the tile's rows, weight rows and (by wavefront) scales
 };
 
+// The same in every lane, told to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return uint32_t(__builtin_amdgcn_readfirstlane(int(v))); }
+__device__ __forceinline__ u32x4 uniform(u32x4 v) { return u32x4{uniform(v[0]), uniform(v[1]), uniform(v[2]), uniform(v[3])}; }
+
+// The descriptor of `bytes` bytes from p on; reads behind them give zero.
 __device__ __forceinline__ u32x4 buffer_of(const void *p, uint32_t bytes)
 {
     const uint64_t v = reinterpret_cast<uint64_t>(p);
-    return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(v)))),
-                 uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(v >> 32) & 0xFFFFu))),
-                 uint32_t(__builtin_amdgcn_readfirstlane(int(bytes))), 0x00020000u};
-}
-
-// The same in every lane, told to the compiler.
-__device__ __forceinline__ u32x4 uniform(u32x4 v)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = uint32_t(__builtin_amdgcn_readfirstlane(int(v[i])));
-    return v;
+    return uniform(u32x4{uint32_t(v), uint32_t(v >> 32) & 0xFFFFu, bytes, 0x00020000u});
 }
 
 // A lane's four columns of blocks q and q + 1 (columns 4g .. of each) to eight of one
-// block: odd lane groups take theirs of block q + 1, even ones of block q, from
-// each other.  Afterwards a holds the first four and b the last; the result is
-// the first one's column from block q's first (n columns: half a block).
-__device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b, int n)
+// block: odd lane groups take theirs of block q + 1, even ones of block q, from each
+// other, so that a row's stores are whole 64-byte pieces.  Afterwards a holds the
+// first four columns and b the last; returns the first one, from block q's first on.
+__device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b)
 {
     const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
     a = r[0];
     b = r[1];
     const int g = (threadIdx.x & 63) >> 4;
-    return (g & 1) * 2 * n + (g >> 1) * n;
+    return (g & 1) * 16 + (g >> 1) * 8;
 }
 
 // 64 lanes x 16 (or 4) bytes of buffer `r`, lane by lane at voff + soff, to LDS
@@ -579,23 +594,23 @@ __device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b, int n)
 // written out where a stage is first read.  (These kernels use M0 nowhere else.)
 __device__ __forceinline__ void to_lds16(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(uniform(r)),
-                 "s"(__builtin_amdgcn_readfirstlane(int(soff))));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(uniform(lds)),
+                 "v"(voff), "s"(uniform(r)), "s"(uniform(soff)));
 }
 __device__ __forceinline__ void to_lds4(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(voff), "s"(uniform(r)),
-                 "s"(__builtin_amdgcn_readfirstlane(int(soff))));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(uniform(lds)),
+                 "v"(voff), "s"(uniform(r)), "s"(uniform(soff)));
 }
 
 template <int WM_, int WN_, int MX_, int ST_>
 struct Shape {
-    static constexpr int WM = WM_, WN = WN_, MX = MX_, ST = ST_, SB = 128;
+    static constexpr int WM = WM_, WN = WN_, MX = MX_, ST = ST_;
     static constexpr int waves = WM * WN, threads = waves * kWave;
     static constexpr int rows = WM * MX * 16, wrows = WN * 64;
-    static constexpr int nx = rows * SB / 1024 / waves, nw = wrows * SB / 1024 / waves;   // loads of a wavefront and step
-    static constexpr uint32_t xbytes = rows * SB, scales = (rows + wrows) * SB;
-    static_assert(nx * waves * 1024 == rows * SB && nw * waves * 1024 == wrows * SB, "whole loads");
+    static constexpr int nx = rows / 8 / waves, nw = wrows / 8 / waves;   // loads (1 KiB) of a wavefront and step
+    static constexpr uint32_t xbytes = rows * 128, scales = (rows + wrows) * 128;
+    static_assert(nx * waves * 8 == rows && nw * waves * 8 == wrows, "whole loads");
 };
 
 template <class S, bool FP8, bool GATED, bool OUT8, bool LOW>
@@ -604,7 +619,7 @@ struct Many {
     static constexpr int BN = S::wrows / (GATED ? 2 : 1); // columns of out per tile
     static constexpr uint32_t stage_bytes = S::scales + (FP8 ? S::waves * 256 : 0);
     static constexpr int loads = S::nx + S::nw + (FP8 ? 1 : 0);
-    static_assert(!FP8 || (S::SB == 128 && S::rows <= 128 * S::waves / 2), "FP8 steps are scale blocks");
+    static_assert(!FP8 || S::rows <= 64 * S::waves / 2, "half the wavefronts bring the rows' scales");
 
     const ProductArgs &a;
     Tiles &tiles;
@@ -616,7 +631,7 @@ struct Many {
     int xp[2], wp[2];                      // and of its own two of a block in LDS
     int nu;
 
-    // the steps' loads run ahead of the products
+    // the next load: its item, step and stage
     ManyItem ahead;
     int ahead_u, ahead_at, ahead_stage;
 
@@ -632,12 +647,11 @@ struct Many {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         wm = wave / S::WN;
         wn = wave % S::WN;
-        nu = a.kb / S::SB;
-        constexpr int np = S::SB / 16;   // pieces of a row
+        nu = a.kb / 128;
 #pragma unroll
         for (int i = 0; i < S::nx; ++i) {
-            const int row = ((i * S::waves + wave) * 64 + lane) / np;
-            xo[i] = uint32_t(row) * uint32_t(a.kb) + uint32_t(((lane % np) ^ key(row)) * 16);
+            const int row = ((i * S::waves + wave) * 64 + lane) / 8;
+            xo[i] = uint32_t(row) * uint32_t(a.kb) + uint32_t(((lane & 7) ^ key(row)) * 16);
         }
 #pragma unroll
         for (int i = 0; i < S::nw; ++i) {
@@ -646,7 +660,7 @@ struct Many {
             const int q = row >> 4 & 3, c = (row >> 6) * (16 * G) + q % G * 16 + (q < G ? 0 : a.n);
             wo[i] = uint32_t(c) * uint32_t(a.kb) +
                     (a.packed ? uint32_t(at % 2048)
-                              : uint32_t(row & 15) * uint32_t(a.kb) + uint32_t(((lane % np) ^ key(row)) * 16));
+                              : uint32_t(row & 15) * uint32_t(a.kb) + uint32_t(((lane & 7) ^ key(row)) * 16));
         }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -687,11 +701,11 @@ struct Many {
     // The next step's loads on their way.
     __device__ __forceinline__ void issue(const Items &it)
     {
-        const uint32_t at = lds + uint32_t(ahead_stage) * stage_bytes, so_u = uint32_t(ahead_u) * uint32_t(S::SB);
+        const uint32_t at = lds + uint32_t(ahead_stage) * stage_bytes, xu = uint32_t(ahead_u) * 128u, wu = uint32_t(ahead_u) * uint32_t(a.wstep);
 #pragma unroll
-        for (int i = 0; i < S::nw; ++i) to_lds16(ahead.wr, wo[i], uint32_t(ahead_u) * uint32_t(a.wstep), at + S::xbytes + uint32_t(i * S::waves + wave) * 1024u);
+        for (int i = 0; i < S::nw; ++i) to_lds16(ahead.wr, wo[i], wu, at + S::xbytes + uint32_t(i * S::waves + wave) * 1024u);
 #pragma unroll
-        for (int i = 0; i < S::nx; ++i) to_lds16(ahead.xr, xo[i], so_u, at + uint32_t(i * S::waves + wave) * 1024u);
+        for (int i = 0; i < S::nx; ++i) to_lds16(ahead.xr, xo[i], xu, at + uint32_t(i * S::waves + wave) * 1024u);
         if (FP8) to_lds4(ahead.sr, so, uint32_t(ahead_u) * 4u, at + S::scales + uint32_t(wave) * 256u);
         ahead_stage = ahead_stage + 1 == S::ST ? 0 : ahead_stage + 1;
         if (++ahead_u == nu) {
@@ -808,8 +822,8 @@ struct Many {
                         v[q][0] = pack_bf16(acc[i][2 * h + q][0], acc[i][2 * h + q][1]);
                         v[q][1] = pack_bf16(acc[i][2 * h + q][2], acc[i][2 * h + q][3]);
                     }
-                    const int c = c0 + wn * (16 * G) + h * 32 + pair_up(v[0][0], v[1][0], 8);
-                    pair_up(v[0][1], v[1][1], 8);
+                    const int c = c0 + wn * (16 * G) + h * 32 + pair_up(v[0][0], v[1][0]);
+                    pair_up(v[0][1], v[1][1]);
                     if (in && c < a.n)
                         *(gptr<u32x4>)((gptr<uint16_t>)a.out + int64_t(row) * a.n + c) = u32x4{v[0][0], v[0][1], v[1][0], v[1][1]};
                 }
@@ -835,22 +849,13 @@ struct Many {
                 float v = amax[r];
 #pragma unroll
                 for (int w = 1; w < S::WN; ++w) v = fmaxf(v, amax[w * S::rows + r]);
-                const float sc = v / 448.0f, inv = sc > 0.f ? 1.0f / sc : 0.f;
-                {
-                    const int64_t row = t.row0 + r;
-                    if (r < t.nrows && wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
-                    uint32_t code[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float d[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) d[j] = acc[i][q][j] * inv;
-                        const int c = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
-                        code[q] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], c, true));
-                    }
-                    const int c = c0 + wn * 32 + pair_up(code[0], code[1], 8);
-                    if (r < t.nrows) *(gptr<u32x2>)((gptr<uint8_t>)a.out + row * a.n + c) = u32x2{code[0], code[1]};
-                }
+                float inv;
+                const float sc = scale_of(v, inv);
+                const int64_t row = t.row0 + r;
+                if (r < t.nrows && wn == 0 && g == 0) ((gptr<float>)a.outs)[row * (a.n / 128) + c0 / 128] = sc;
+                uint32_t code[2] = {codes_of(acc[i][0], inv), codes_of(acc[i][1], inv)};
+                const int c = c0 + wn * 32 + pair_up(code[0], code[1]);
+                if (r < t.nrows) *(gptr<u32x2>)((gptr<uint8_t>)a.out + row * a.n + c) = u32x2{code[0], code[1]};
             }
             // (amax is written again behind the next item's step barriers)
         }
@@ -963,29 +968,33 @@ __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t q0, uint32_t q1)
 }
 
 // t[r, :] = scaling[i] A[i, j] x[r] for every row r of expert j with an adapter i.
-// Bound by reading the A of every (adapter, expert) pair once.  An expert's
-// workgroups find its distinct adapters from a bit map of the rows' tags; the
-// pairs of an adapter and 32 rows of its A go round them.  For each, the adapter's
-// rows are gathered, 32 at a time, and multiplied as in k_product_few: the
-// A operand holds rows of A, the wavefronts split k.
+// Meant to be bound by reading the A of every (adapter, expert) pair once.  An
+// expert's workgroups find its distinct adapters from a bit map of the rows' tags;
+// the pairs of an adapter and 32 rows of its A go round them.  For each, the
+// adapter's rows are gathered, 32 (FP8 64) at a time, and multiplied as in
+// k_product_few: the A operand holds rows of A, the wavefronts split k.
+// Measured: 32 adapters of rank 16, 1024 rows over 64 experts (813 pairs, 106 MB of
+// A) 41 us for the first product; FP8, 8 of rank 32, 16384 rows (134 MB) 68 us, of
+// which the gathered reads of x take 26.
 template <bool FP8>
 struct Shrink {
     static constexpr int KS = 4, threads = KS * kWave, NB = 2, CH = 16 * NB;
     static constexpr int step = FP8 ? 128 : 64;         // columns of k
     static constexpr int NP = FP8 ? 4 : 2;              // products of 32 columns per step
+    static constexpr int MAXB = FP8 ? 4 : 2, GROUP = 16 * MAXB;   // row blocks and rows at a time
     static constexpr int words = AFD_MAX_ADAPTERS / 32;
 
     struct Shared {
         uint32_t bits[words];
         int sums[threads];
-        int list[threads + 32];   // gathered rows
+        int list[threads + GROUP];   // gathered rows
         int waves[KS], found;
-        f32x4 red[KS][2 * NB][kWave];
+        f32x4 red[KS][MAXB * NB][kWave];
     };
     template <int MB>
     struct Step {
         u32x4 a[NB][NP];
-        Frag x[MB];
+        std::conditional_t<FP8, u32x2, u32x4> x[MB][NP];   // eight columns each: lane group g's of every 32
         float s[MB];
     };
 
@@ -1011,13 +1020,13 @@ struct Shrink {
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             row[i] = sh.list[first + min(i * 16 + r16, n - 1)];
-            xp[i] = (gptr<const uint8_t>)a.x + int64_t(row[i]) * a.k * (FP8 ? 1 : 2) + g * 32;
+            xp[i] = (gptr<const uint8_t>)a.x + int64_t(row[i]) * a.k * (FP8 ? 1 : 2) + g * (FP8 ? 8 : 16);
         }
         gptr<const uint8_t> ap[NB];
 #pragma unroll
         for (int q = 0; q < NB; ++q)
             ap[q] = (gptr<const uint8_t>)a.a +
-                    ((int64_t(ad) * a.E + e) * a.c + min(c0 + q * 16 + r16, a.c - 1)) * int64_t(a.k) * 2 + g * (FP8 ? 64 : 32);
+                    ((int64_t(ad) * a.E + e) * a.c + min(c0 + q * 16 + r16, a.c - 1)) * int64_t(a.k) * 2 + g * 16;
         f32x4 acc[MB][NB];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
@@ -1027,11 +1036,14 @@ struct Shrink {
 #pragma unroll
             for (int q = 0; q < NB; ++q)
 #pragma unroll
-                for (int p = 0; p < NP; ++p) st.a[q][p] = *(gptr<const u32x4>)(ap[q] + u * (step * 2) + p * 16);
+                for (int p = 0; p < NP; ++p) st.a[q][p] = *(gptr<const u32x4>)(ap[q] + u * (step * 2) + p * 64);
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
 #pragma unroll
-                for (int p = 0; p < 2; ++p) st.x[i].p[p] = *(gptr<const u32x4>)(xp[i] + u * 128 + p * 16);
+                for (int p = 0; p < NP; ++p) {
+                    if constexpr (FP8) st.x[i][p] = *(gptr<const u32x2>)(xp[i] + u * 128 + p * 32);
+                    else st.x[i][p] = *(gptr<const u32x4>)(xp[i] + u * 128 + p * 64);
+                }
                 if (FP8) st.s[i] = ((gptr<const float>)a.xs)[int64_t(row[i]) * nu + u];
             }
         };
@@ -1044,8 +1056,7 @@ struct Shrink {
                     for (int q = 0; q < NB; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        const u32x4 h = st.x[i].p[p / 2];
-                        const u32x4 xv = p % 2 ? fp8_to_bf16(h[2], h[3]) : fp8_to_bf16(h[0], h[1]);
+                        const u32x4 xv = fp8_to_bf16(st.x[i][p][0], st.x[i][p][1]);
 #pragma unroll
                         for (int q = 0; q < NB; ++q) d[q] = mfma_bf16(st.a[q][p], xv, d[q]);
                     }
@@ -1057,11 +1068,18 @@ struct Shrink {
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
 #pragma unroll
-                        for (int q = 0; q < NB; ++q) acc[i][q] = mfma_bf16(st.a[q][p], st.x[i].p[p], acc[i][q]);
+                        for (int q = 0; q < NB; ++q) acc[i][q] = mfma_bf16(st.a[q][p], st.x[i][p], acc[i][q]);
                 }
             }
         };
-        if (wave < nu) {
+        if constexpr (FP8) {   // 64 rows' steps leave no registers for two
+            for (int u = wave; u < nu; u += KS) {
+                Step<MB> s0;
+                load(s0, u);
+                __builtin_amdgcn_sched_barrier(0);
+                use(s0);
+            }
+        } else if (wave < nu) {
             Step<MB> s0, s1;
             int u = wave;
             load(s0, u);
@@ -1087,13 +1105,13 @@ struct Shrink {
 #pragma unroll
             for (int q = 0; q < NB; ++q) sh.red[wave][i * NB + q][lane] = acc[i][q];
         __syncthreads();
-        if (wave < MB * NB) {
-            const int i = wave / NB, q = wave % NB, c = c0 + q * 16 + g * 4;
-            f32x4 v = sh.red[0][wave][lane];
+        for (int b = wave; b < MB * NB; b += KS) {
+            const int i = b / NB, q = b % NB, c = c0 + q * 16 + g * 4;
+            f32x4 v = sh.red[0][b][lane];
 #pragma unroll
             for (int w = 1; w < KS; ++w)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] += sh.red[w][wave][lane][j];
+                for (int j = 0; j < 4; ++j) v[j] += sh.red[w][b][lane][j];
             const float f = ((gptr<const float>)a.scaling)[ad];
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] *= f;
@@ -1169,13 +1187,14 @@ struct Shrink {
                 __syncthreads();
                 const bool last = base + threads >= count;
                 int first = 0;
-                while (have - first >= 32 || (last && have > first)) {
-                    const int n32 = min(have - first, 32);
-                    if (n32 <= 16) multiply<1>(e, ad, c0, first, n32);
-                    else multiply<2>(e, ad, c0, first, n32);
-                    first += n32;
+                while (have - first >= GROUP || (last && have > first)) {
+                    const int n = min(have - first, GROUP);
+                    if (n <= 16) multiply<1>(e, ad, c0, first, n);
+                    else if (n <= 32 || MAXB == 2) multiply<2>(e, ad, c0, first, n);
+                    else multiply<MAXB>(e, ad, c0, first, n);
+                    first += n;
                 }
-                // fewer than 32 rows left: to the front, for the next tags
+                // fewer rows left than a group: to the front, for the next tags
                 const int rest = have - first;
                 int keep = 0;
                 if (tid < rest) keep = sh.list[first + tid];
@@ -1190,7 +1209,7 @@ struct Shrink {
 
 // Workgroup b runs on XCD b % 8; an expert's share one L2 for its rows.
 template <bool FP8>
-__global__ __launch_bounds__(Shrink<FP8>::threads, FP8 ? 2 : 4) void k_shrink(ShrinkArgs a)
+__global__ __launch_bounds__(Shrink<FP8>::threads, FP8 ? 3 : 4) void k_shrink(ShrinkArgs a)
 {
     __shared__ typename Shrink<FP8>::Shared sh;
     const int i = blockIdx.x >> 3, e = i / a.share * 8 + (blockIdx.x & 7), y = i % a.share;
@@ -1277,7 +1296,7 @@ int launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
     return launched();
 }
 
-// A launch whose dynamic LDS exceeds 64 KiB; the kernel is told once.
+// A launch whose dynamic LDS exceeds 64 KiB; the kernel is told once per device.
 template <bool FP8, bool GATED, bool OUT8, bool LOW>
 int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
 {
@@ -1285,9 +1304,15 @@ int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
     constexpr int lds = std::max(Low::ST * M::stage_bytes, Tall::ST * Tall::scales);
     static_assert(Low::threads == Tall::threads, "one launch");
     a.ntiles = (p.n + M::BN - 1) / M::BN;
-    static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_product_many<FP8, GATED, OUT8, LOW>),
-                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (set != hipSuccess) return 1;
+    static std::atomic<uint64_t> told{0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+    if (!(told.load() >> dev & 1)) {
+        if (hipFuncSetAttribute(reinterpret_cast<const void *>(&k_product_many<FP8, GATED, OUT8, LOW>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
+            return 1;
+        told.fetch_or(uint64_t(1) << dev);
+    }
     const unsigned grid = persistent_grid(tile_bound(p, Low::rows), a.ntiles, kComputeUnits);
     hipLaunchKernelGGL((k_product_many<FP8, GATED, OUT8, LOW>), dim3(grid), dim3(Low::threads), lds, st, a);
     return launched();

@@ -438,8 +438,8 @@ typedef enum { AFD_WEIGHTS_ROWS = 0, AFD_WEIGHTS_PACKED = 1 } afd_weight_layout;
  *                 columns, W per 128 x 128 block
  *   out_dtype     AFD_BF16; AFD_FP8_E4M3 only for an FP8 product with
  *                 AFD_ACT_SWIGLU: per row and 128 columns scale = amax / 448
- *                 and code = e4m3(v / scale) to nearest even; an all-zero
- *                 block has scale 0 and codes 0
+ *                 and code = e4m3(v * (1 / scale)) to nearest even; a scale
+ *                 below 2^-126 counts as 0 and gives codes 0
  *   activation    afd_activation
  *   num_adapters  0, or the number of adapters, at most AFD_MAX_ADAPTERS
  *   rank          of every adapter, a multiple of 8 up to AFD_MAX_RANK (smaller

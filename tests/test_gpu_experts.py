@@ -64,6 +64,8 @@ COUNTS = {
     "large": ([300, 3, 513], 128),
     "many": ([(7 * i) % 11 for i in range(130)], 4),
     "tall": ([1100], 1),
+    "taller": ([321, 0, 700, 256, 385], 32),       # 256-row tiles (BF16)
+    "skewed": ([70, 33, 0, 17] + [0] * 60, 1),     # few rows on the average, some experts with more than a tile
 }
 
 
@@ -71,7 +73,7 @@ def _print(*a):
     print("[experts]", *a, flush=True)
 
 
-@pytest.mark.parametrize("shape", ["one_row", "empty_and_one", "edges", "aligned", "large", "many", "tall"])
+@pytest.mark.parametrize("shape", list(COUNTS))
 @pytest.mark.parametrize("dtype,gated,k,n", [
     ("bf16", False, 256, 256), ("bf16", False, 64, 16), ("bf16", False, 704, 272), ("bf16", True, 320, 96),
     ("bf16", True, 512, 336), ("fp8", False, 128, 16), ("fp8", False, 768, 400), ("fp8", True, 384, 128),
@@ -86,7 +88,7 @@ def test_product(shape, dtype, gated, k, n):
     _check(got, want, ref.rounded(want, tol), live, f"{shape} {dtype}")
 
 
-@pytest.mark.parametrize("shape", ["edges", "large"])
+@pytest.mark.parametrize("shape", ["edges", "large", "taller", "skewed"])
 @pytest.mark.parametrize("dtype,gated,k,n", [("bf16", False, 320, 144), ("bf16", True, 192, 80), ("fp8", False, 384, 272),
                                              ("fp8", True, 256, 256)])
 def test_packed_weights_give_the_same_bits(shape, dtype, gated, k, n):
@@ -108,7 +110,7 @@ def test_packed_weights_give_the_same_bits(shape, dtype, gated, k, n):
     assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("shape", ["one_row", "edges", "aligned", "large", "many"])
+@pytest.mark.parametrize("shape", ["one_row", "edges", "aligned", "large", "many", "skewed"])
 @pytest.mark.parametrize("k,n,S", [(256, 128, 0), (384, 384, 0), (256, 256, 3)])
 def test_product_fp8_out(shape, k, n, S):
     afd = _afd()
@@ -137,7 +139,27 @@ def test_product_fp8_out(shape, k, n, S):
     assert (top == 448)[live & (torch.arange(c["rows"]) >= c["ends"][0])].all()
 
 
-@pytest.mark.parametrize("shape", ["one_row", "empty_and_one", "edges", "aligned", "large"])
+@pytest.mark.parametrize("rows", [3, 200])
+def test_fp8_out_of_tiny_and_infinite_rows(rows):
+    """A block whose scale would be subnormal has scale 0 and codes 0; an
+    infinite value makes only its own row's block infinite."""
+    afd = _afd()
+    _print("tiny", rows)
+    c = ref.make(12, 1, [rows], 1, 128, 256, "fp8", gated=True)
+    c["xs"][0] = 2.0 ** -75          # gate and up of about 2^-75: products of about 2^-151
+    c["xs"][1] = float("inf")
+    out, outs = _run_product(afd, c, out8=True)
+    s, codes = outs.double().cpu()[:rows], out.float().double().cpu()[:rows]
+    assert s[0].item() == 0 and not codes[0].any()
+    assert not torch.isfinite(s[1]).all() or torch.isnan(codes[1]).any()
+    want, tol, live = ref.run_product(c, c["x"], torch.where(torch.isfinite(c["xs"]), c["xs"], torch.ones(())), c["w"],
+                                      c["ws"], None, None, c["ends"], 1, c["rows"])
+    got, bound = codes * s.repeat_interleave(128, 1), tol + (2.0 ** -4 + 4 * ref.F32) * (want.abs() + tol)
+    bound[:rows] += (s * 2.0 ** -10).repeat_interleave(128, 1)
+    assert ((got - want[:rows]).abs() <= bound[:rows])[2:].all()
+
+
+@pytest.mark.parametrize("shape", ["one_row", "empty_and_one", "edges", "aligned", "large", "skewed"])
 @pytest.mark.parametrize("dtype,gated,k,n,S,rank", [
     ("bf16", False, 320, 144, 1, 8), ("bf16", True, 256, 96, 5, 16), ("bf16", True, 192, 64, 40, 24),
     ("bf16", False, 256, 272, 3, 128), ("fp8", False, 256, 144, 7, 40), ("fp8", True, 384, 128, 2, 64)])
@@ -220,7 +242,7 @@ def test_no_rows_and_ends_behind_the_rows():
                            torch.zeros(3, dtype=torch.int32, device="cuda"), w)
     assert z.shape == (0, 32)
     # all experts empty; ends past the rows are cut, descending ends give empty experts
-    for ends in ([0, 0, 0], [50, 500, 501], [30, 10, 45], [-5, 20, 2 ** 31 - 1]):
+    for ends in ([0, 0, 0], [50, 500, 501], [30, 10, 10], [-5, 20, 2 ** 31 - 1]):
         c = ref.make(8, 3, [20, 10, 10], 1, 64, 32, "bf16")
         c["x"] = torch.randn(c["rows"], 64).bfloat16()
         c["ends"] = ends

@@ -231,25 +231,23 @@ class Buffer:
         keep what `out` held; without `out` they are -1."""
         if len(tags) != self.N:
             raise ValueError("tags must hold one tensor per source")
-        ptrs = (ctypes.c_void_p * self.N)()
         dev = received.weights.device
+        ptrs = (ctypes.c_void_p * self.N)()
         for s, t in enumerate(tags):
             T = self._T[s]
-            if T == 0:
-                continue
-            if t is None or t.dtype != torch.int32 or tuple(t.shape) != (T,) or not t.is_contiguous() or \
-                    t.device != dev:
-                raise ValueError("tags must be contiguous int32 [T] tensors on the buffer's device")
-            ptrs[s] = t.data_ptr()
+            if T:
+                if t is None or t.dtype is not torch.int32 or t.shape != (T,) or t.device != dev or \
+                        not t.is_contiguous():
+                    raise ValueError("tags must be contiguous int32 [T] tensors on the buffer's device")
+                ptrs[s] = t.data_ptr()
         n = received.receive_rows
         if out is None:
             out = torch.full((n,), -1, dtype=torch.int32, device=dev)
-        elif out.dtype != torch.int32 or tuple(out.shape) != (n,) or not out.is_contiguous() or \
-                out.device != dev:
+        elif out.dtype is not torch.int32 or out.shape != (n,) or out.device != dev or not out.is_contiguous():
             raise ValueError("out must be contiguous int32 [receive_rows] on the buffer's device")
         with _experts.on_device(dev):
-            st = self.lib.afd_worker_tags(self.ctx, f, ptrs, _ptr(out), n, ctypes.byref(received.receipt),
-                                          _stream(self.device))
+            st = self.lib.afd_worker_tags(self.ctx, f, ptrs, out.data_ptr(), n, received.receipt,
+                                          _experts.raw_stream(dev))
         nat.check(st, "worker_tags")
         self._round_refs[("tags", f)] = (tags, out)
         return out

@@ -750,6 +750,7 @@ struct Many {
             const lptr<const unsigned char> st = stages + stage * stage_bytes, xb = st + wm * MB * 2048,
                                             wb = st + S::xbytes + wn * 4 * 2048;
             Frag wf[4], xf[MB];
+            f32x4 d[2][4];   // FP8: a row block's sums are scaled under the next one's products
 #pragma unroll
             for (int q = 0; q < 4; ++q) wf[q] = read(wb + q * 2048, wp);
             float s0 = 0.f, s1 = 0.f, sx[MB];
@@ -768,17 +769,26 @@ struct Many {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if constexpr (FP8) {
-                        const f32x4 d = mfma_fp8(wf[q], xf[i], f32x4{0.f, 0.f, 0.f, 0.f});
-                        const float s = sx[i] * (q < G ? s0 : s1);
+                        d[i & 1][q] = mfma_fp8(wf[q], xf[i], f32x4{0.f, 0.f, 0.f, 0.f});
+                        if (i > 0) {
+                            const float s = sx[i - 1] * (q < G ? s0 : s1);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[i][q][j] = fmaf(d[j], s, acc[i][q][j]);
+                            for (int j = 0; j < 4; ++j) acc[i - 1][q][j] = fmaf(d[(i - 1) & 1][q][j], s, acc[i - 1][q][j]);
+                        }
                     } else {
 #pragma unroll
                         for (int p = 0; p < 2; ++p) acc[i][q] = mfma_bf16(wf[q].p[p], xf[i].p[p], acc[i][q]);
                     }
                 }
-                if (!FP8) __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            if constexpr (FP8)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float s = sx[MB - 1] * (q < G ? s0 : s1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[MB - 1][q][j] = fmaf(d[(MB - 1) & 1][q][j], s, acc[MB - 1][q][j]);
+                }
             stage = stage + 1 == S::ST ? 0 : stage + 1;
         }
         finish<MB>(t, c0, acc);

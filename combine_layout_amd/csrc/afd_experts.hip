@@ -20,7 +20,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "afd_plan.h"
 
@@ -997,8 +996,8 @@ __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t q0, uint32_t q1)
 // adapter's rows are gathered, 32 (FP8 64) at a time, and multiplied as in
 // k_product_few: the A operand holds rows of A, the wavefronts split k.
 // Measured: 32 adapters of rank 16, 1024 rows over 64 experts (813 pairs, 106 MB of
-// A) 41 us for the first product; FP8, 8 of rank 32, 16384 rows (134 MB) 68 us, of
-// which the gathered reads of x take 26.
+// A) 41 us for the first product; FP8, 8 of rank 32, 16384 rows (134 MB) 56 us
+// (68 with x read 8 bytes at a time).
 template <bool FP8>
 struct Shrink {
     static constexpr int KS = 4, threads = KS * kWave, NB = 2, CH = 16 * NB;
@@ -1017,7 +1016,7 @@ struct Shrink {
     template <int MB>
     struct Step {
         u32x4 a[NB][NP];
-        std::conditional_t<FP8, u32x2, u32x4> x[MB][NP];   // eight columns each: lane group g's of every 32
+        u32x4 x[MB][2];   // FP8: 16 codes, of two products
         float s[MB];
     };
 
@@ -1043,13 +1042,13 @@ struct Shrink {
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             row[i] = sh.list[first + min(i * 16 + r16, n - 1)];
-            xp[i] = (gptr<const uint8_t>)a.x + int64_t(row[i]) * a.k * (FP8 ? 1 : 2) + g * (FP8 ? 8 : 16);
+            xp[i] = (gptr<const uint8_t>)a.x + int64_t(row[i]) * a.k * (FP8 ? 1 : 2) + g * 16;
         }
         gptr<const uint8_t> ap[NB];
 #pragma unroll
         for (int q = 0; q < NB; ++q)
             ap[q] = (gptr<const uint8_t>)a.a +
-                    ((int64_t(ad) * a.E + e) * a.c + min(c0 + q * 16 + r16, a.c - 1)) * int64_t(a.k) * 2 + g * 16;
+                    ((int64_t(ad) * a.E + e) * a.c + min(c0 + q * 16 + r16, a.c - 1)) * int64_t(a.k) * 2 + g * (FP8 ? 32 : 16);
         f32x4 acc[MB][NB];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
@@ -1059,14 +1058,11 @@ struct Shrink {
 #pragma unroll
             for (int q = 0; q < NB; ++q)
 #pragma unroll
-                for (int p = 0; p < NP; ++p) st.a[q][p] = *(gptr<const u32x4>)(ap[q] + u * (step * 2) + p * 64);
+                for (int p = 0; p < NP; ++p) st.a[q][p] = *(gptr<const u32x4>)(ap[q] + u * (step * 2) + (FP8 ? p / 2 * 128 + p % 2 * 16 : p * 64));
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    if constexpr (FP8) st.x[i][p] = *(gptr<const u32x2>)(xp[i] + u * 128 + p * 32);
-                    else st.x[i][p] = *(gptr<const u32x4>)(xp[i] + u * 128 + p * 64);
-                }
+                for (int p = 0; p < 2; ++p) st.x[i][p] = *(gptr<const u32x4>)(xp[i] + u * 128 + p * 64);
                 if (FP8) st.s[i] = ((gptr<const float>)a.xs)[int64_t(row[i]) * nu + u];
             }
         };
@@ -1079,7 +1075,7 @@ struct Shrink {
                     for (int q = 0; q < NB; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        const u32x4 xv = fp8_to_bf16(st.x[i][p][0], st.x[i][p][1]);
+                        const u32x4 xv = fp8_to_bf16(st.x[i][p / 2][p % 2 * 2], st.x[i][p / 2][p % 2 * 2 + 1]);
 #pragma unroll
                         for (int q = 0; q < NB; ++q) d[q] = mfma_bf16(st.a[q][p], xv, d[q]);
                     }

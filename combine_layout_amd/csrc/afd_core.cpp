@@ -285,7 +285,7 @@ afd_status check_product(const afd_product_config *c, int64_t rows)
 size_t product_workspace(const afd_product_config &c, int64_t rows)
 {
     if (c.num_adapters == 0) return 0;
-    return align256(size_t(rows) * size_t(c.rank) * (c.activation == AFD_ACT_SWIGLU ? 2 : 1) * 4);
+    return align256(size_t(rows) * size_t(c.rank) * (c.activation == AFD_ACT_SWIGLU ? 2 : 1) * 2 * 2);
 }
 
 // Pointers of a product's weights; `fp8` and `adapters` say which there are.
@@ -320,7 +320,7 @@ ProductPlan plan_product(const afd_product_config &c, int64_t rows, const void *
     p.w = w;
     p.out = out;
     p.outs = outs;
-    p.t = c.num_adapters ? static_cast<float *>(t) : nullptr;
+    p.t = c.num_adapters ? static_cast<uint16_t *>(t) : nullptr;
     return p;
 }
 

@@ -7,7 +7,7 @@
 //   FP8       x = q * xs[r, k/128] and W = p * ws[j, n/128, k/128]: the codes of
 //             one 128-column block are multiplied and summed by the matrix unit,
 //             and each block's sum enters the float32 sum times xs * ws
-//   adapters  t[r, :] = scaling[a] * A[a, j] x[r] (k_shrink, float32), then
+//   adapters  t[r, :] = scaling[a] * A[a, j] x[r] (k_shrink, summed in float32), then
 //             B[a, j] t[r] is added to row r's sums before the activation
 //
 // Orientation.  The matrix unit's A operand holds weight rows and its B operand
@@ -206,7 +206,7 @@ struct ProductArgs {
     const uint8_t *w;
     const float *xs, *ws;
     const int32_t *ends, *tags;
-    const float *t;
+    const uint16_t *t;   // [rows][2][c * rank]: the two bf16 parts of every row's t
     const uint8_t *b;
     void *out;
     float *outs;
@@ -220,13 +220,21 @@ struct ProductArgs {
     int ntiles;    // column tiles
 };
 
+// t enters the matrix unit as two bf16 parts, t - hi - lo below 2^-16 of t: hi in the
+// low half, lo in the high half.
+__device__ __forceinline__ uint32_t split_t(float t)
+{
+    const uint32_t hi = to_bf16(t);
+    const float rest = t - __uint_as_float(hi << 16);
+    return hi | (fabsf(rest) < INFINITY ? to_bf16(rest) << 16 : 0u);   // an infinite t has no rest
+}
+
 // Adds B t of the adapters of MB row blocks to v (37 and 30 us on top of the 103 and
 // 65 us FP8 products of 256 rows per expert with about five adapters of rank 32 in
 // 64 rows: a chain of one load of t and one of B per adapter): per block, NQ column blocks per
 // kind of 4 consecutive columns of one row per lane.  wrow[] are the weight rows of
 // this lane's A-operand rows.  Per 32 ranks, every row's t is loaded once (each row
-// has one adapter) and enters the matrix unit as two bf16 parts, t - hi - lo below
-// 2^-16 of t; the distinct adapters number sub, sub + nsub, .. are taken one after
+// has one adapter), in its two bf16 parts (split_t); the distinct adapters number sub, sub + nsub, .. are taken one after
 // the other, the next one's B on its way meanwhile, and each lane adds only its own
 // row's, by selection, so an adapter's infinities reach no other request.
 template <int KINDS, int NQ, int MB>
@@ -236,16 +244,16 @@ __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, const 
     const int lane = threadIdx.x & 63, g = lane >> 4;
     for (int j0 = 0; j0 < a.rank; j0 += 32) {
         const int j = j0 + g * 8;
-        f32x4 t[MB][KINDS][2];
+        u32x4 hi[MB][KINDS], lo[MB][KINDS];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int c = 0; c < KINDS; ++c)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    t[i][c][h] = tag[i] >= 0 && j < a.rank
-                                     ? *(gptr<const f32x4>)((gptr<const float>)a.t + int64_t(row[i]) * (KINDS * a.rank) + c * a.rank + j + h * 4)
-                                     : f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int c = 0; c < KINDS; ++c) {
+                const bool have = tag[i] >= 0 && j < a.rank;
+                const gptr<const uint16_t> t = (gptr<const uint16_t>)a.t + int64_t(row[i]) * (2 * KINDS * a.rank) + c * a.rank + j;
+                hi[i][c] = have ? *(gptr<const u32x4>)t : u32x4{0u, 0u, 0u, 0u};
+                lo[i][c] = have ? *(gptr<const u32x4>)(t + KINDS * a.rank) : u32x4{0u, 0u, 0u, 0u};
+            }
         uint32_t left[MB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) left[i] = uint32_t(__ballot(tag[i] >= 0)) & 0xFFFFu;
@@ -284,21 +292,6 @@ __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, const 
         Pick p = pick();
         u32x4 bf[KINDS * NQ];
         if (p.ad >= 0) load_b(bf, p.ad);
-        u32x4 hi[MB][KINDS], lo[MB][KINDS];
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int c = 0; c < KINDS; ++c)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float p0 = t[i][c][k / 2][k % 2 * 2], p1 = t[i][c][k / 2][k % 2 * 2 + 1];
-                    const uint32_t h0 = to_bf16(p0), h1 = to_bf16(p1);
-                    float r0 = p0 - __uint_as_float(h0 << 16), r1 = p1 - __uint_as_float(h1 << 16);
-                    if (!(fabsf(r0) < INFINITY)) r0 = 0.f;   // an infinite t has no remainder
-                    if (!(fabsf(r1) < INFINITY)) r1 = 0.f;
-                    hi[i][c][k] = h0 | (h1 << 16);
-                    lo[i][c][k] = pack_bf16(r0, r1);
-                }
         while (p.ad >= 0) {
             const Pick next = pick();
             u32x4 bn[KINDS * NQ];
@@ -966,7 +959,7 @@ struct ShrinkArgs {
     const int32_t *ends, *tags;
     const uint8_t *a;
     const float *scaling;
-    float *t;
+    uint16_t *t;   // [rows][2][c]
     int rows, E, alpha;
     int k;
     int c;       // rows of one adapter's A: rank, or 2 rank gated
@@ -1132,10 +1125,14 @@ struct Shrink {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] += sh.red[w][b][lane][j];
             const float f = ((gptr<const float>)a.scaling)[ad];
+            uint32_t h[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] *= f;
-            if (i * 16 + r16 < n && c < a.c)
-                *(gptr<f32x4>)((gptr<float>)a.t + int64_t(sh.list[first + i * 16 + r16]) * a.c + c) = v;
+            for (int j = 0; j < 4; ++j) h[j] = split_t(v[j] * f);
+            if (i * 16 + r16 < n && c < a.c) {
+                const gptr<uint16_t> t = (gptr<uint16_t>)a.t + int64_t(sh.list[first + i * 16 + r16]) * (2 * a.c) + c;
+                *(gptr<u32x2>)t = u32x2{(h[0] & 0xFFFFu) | h[1] << 16, (h[2] & 0xFFFFu) | h[3] << 16};
+                *(gptr<u32x2>)(t + a.c) = u32x2{h[0] >> 16 | (h[1] & 0xFFFF0000u), h[2] >> 16 | (h[3] & 0xFFFF0000u)};
+            }
         }
         __syncthreads();   // red is written again, and the list may be
     }

@@ -195,7 +195,7 @@ struct ProductPlan {
     afd_product_weights w{};
     void *out = nullptr;
     float *outs = nullptr;
-    float *t = nullptr;              // [rows][(gated ? 2 : 1) * rank] scaling * A x of every row
+    uint16_t *t = nullptr;           // [rows][2][(gated ? 2 : 1) * rank] two bf16 parts of every row's scaling * A x
 };
 
 // Contexts made by afd_create_static use a static scratch array of this many

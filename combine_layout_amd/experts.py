@@ -116,6 +116,20 @@ def _act_dtype(x):
     raise TypeError("x must be bfloat16 or float8_e4m3fn")
 
 
+def _number_and_rank(low):
+    if low.scaling.dim() != 1 or low.b.dim() != 4:
+        raise ValueError("adapters hold a [S, E, rank or 2*rank, k], b [S, E, m, rank] and scaling [S]")
+    return low.scaling.shape[0], low.b.shape[3]
+
+
+def _no_gradients(*tensors):
+    """These are forward calls: what asks for a gradient would silently get none."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if getattr(t, "requires_grad", False):
+                raise ValueError("the experts' calls have no gradients: detach their inputs or call under no_grad()")
+
+
 def _weights(what, w, scales, low, E, m, k, code, dtype, gated, device):
     """The checked pointers of one product's weights."""
     p = nat.ProductWeights()
@@ -132,7 +146,7 @@ def _weights(what, w, scales, low, E, m, k, code, dtype, gated, device):
     elif scales is not None:
         raise ValueError("weight scales belong to float8_e4m3fn weights")
     if low is not None:
-        S, rank = low.scaling.shape[0], low.b.shape[-1]
+        S, rank = _number_and_rank(low)
         p.a = _want(low.a, f"{what} adapters' A", torch.bfloat16, (S, E, rank * (2 if gated else 1), k), device)
         p.b = _want(low.b, f"{what} adapters' B", torch.bfloat16, (S, E, m, rank), device)
         p.scaling = _want(low.scaling, f"{what} adapters' scaling", torch.float32, (S,), device)
@@ -174,8 +188,11 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
     A float8 swiglu product writes float8 rows when `out` is a float8_e4m3fn
     tensor, with their scales in out_scales float32 [rows, n/128].
     Without `out` the result is new memory, its padding rows undefined.
+    Runs on x's device and its current stream; forward only (inputs that ask
+    for a gradient are refused unless gradients are off).
     """
     dev = _x(x)
+    _no_gradients(x, weight, *(adapters or ()))
     R, k = x.shape
     code, dtype = _act_dtype(x)
     if activation not in nat.ACTIVATIONS:
@@ -190,7 +207,7 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
     pe, ps, pa = _rows(x, ends, x_scales, code, adapters, row_adapters, dev)
     w = _weights("the", weight, weight_scales, adapters, E, m, k, code, dtype, gated, dev)
     out8 = out is not None and out.dtype is torch.float8_e4m3fn
-    S, rank = (adapters.scaling.shape[0], adapters.b.shape[-1]) if adapters is not None else (0, 0)
+    S, rank = _number_and_rank(adapters) if adapters is not None else (0, 0)
     cfg, need = _product_plan(R, E, alignment, k, n, code, nat.AFD_FP8_E4M3 if out8 else nat.AFD_BF16,
                               nat.ACTIVATIONS[activation], S, rank,
                               nat.WEIGHTS_PACKED if isinstance(weight, PackedWeights) else nat.WEIGHTS_ROWS)
@@ -219,6 +236,7 @@ def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapter
     columns).  adapters: pairs beside both projections, of one rank and number.
     """
     dev = _x(x)
+    _no_gradients(x, *(adapters.up + adapters.down if adapters is not None else ()))
     R, hidden = x.shape
     code, dtype = _act_dtype(x)
     if experts.up.shape[1] % 2:
@@ -229,8 +247,8 @@ def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapter
     pe, ps, pa = _rows(x, ends, x_scales, code, adapters, row_adapters, dev)
     S = rank = 0
     if adapters is not None:
-        S, rank = adapters.up.scaling.shape[0], adapters.up.b.shape[-1]
-        if adapters.down.scaling.shape[0] != S or adapters.down.b.shape[-1] != rank:
+        S, rank = _number_and_rank(adapters.up)
+        if _number_and_rank(adapters.down) != (S, rank):
             raise ValueError("both projections' adapters must have one number and rank")
     lu, ld = (adapters.up, adapters.down) if adapters is not None else (None, None)
     wu = _weights("up", experts.up, experts.up_scales, lu, E, 2 * inner, hidden, code, dtype, True, dev)

@@ -243,3 +243,16 @@ def test_worker_tags_order_and_arguments(lib):
     assert tag(1, rec1) == nat.AFD_E_ORDER
     x.destroy()
     log(lib)
+
+
+def test_python_calls_refuse_host_tensors():
+    import torch
+
+    import combine_layout_amd as afd
+    x, ends, w = torch.zeros((4, 64)).bfloat16(), torch.tensor([4], dtype=torch.int32), torch.zeros((1, 16, 64)).bfloat16()
+    with pytest.raises(ValueError):
+        afd.expert_product(x, ends, w)
+    with pytest.raises(ValueError):
+        afd.expert_ffn(x, ends, None)
+    with pytest.raises(ValueError):
+        afd.pack_weights(w)

@@ -461,3 +461,103 @@ def test_tags_keep_rows_of_no_choice_and_refusals():
         buf.worker_reply(f, torch.zeros((recs[f].receive_rows, 256), dtype=torch.bfloat16, device="cuda"), recs[f].receipt)
     with pytest.raises(afd.AfdError):
         buf.worker_tags(0, [tags], recs[0])      # after the reply
+
+
+def test_tags_of_a_cached_round():
+    """A round that reuses the last layout has its slot map: tags follow it."""
+    afd = _afd()
+    _print("tags cached")
+    rng = np.random.default_rng(3)
+    T, E, K, F, alpha = 50, 8, 3, 2, 4
+    ids = _ids(rng, T, E, K)
+    buf = afd.Buffer(1, F, E, K, 256, alpha, T)
+    first = []
+    for rnd in range(2):
+        x = torch.randn(T, 256, device="cuda").bfloat16()
+        buf.source_dispatch(0, x, torch.from_numpy(ids).cuda() if rnd == 0 else None, torch.rand(T, K, device="cuda"), bucket=T,
+                            cached=rnd > 0)
+        recs = [buf.worker_receive(f, bucket=T) for f in range(F)]
+        tags = torch.arange(T, dtype=torch.int32, device="cuda") * (rnd + 1)
+        got = [buf.worker_tags(f, [tags], recs[f]) for f in range(F)]
+        if rnd == 0:
+            first = [g.clone() for g in got]
+        else:
+            for f in range(F):
+                assert torch.equal(got[f], torch.where(first[f] >= 0, first[f] * 2, first[f]))
+        for f in range(F):
+            live = got[f] >= 0      # the token's row stands where its tag does
+            tok = (got[f][live] // (rnd + 1)).long()
+            assert torch.equal(recs[f].rows[live], x[tok])
+            buf.worker_reply(f, torch.zeros((recs[f].receive_rows, 256), dtype=torch.bfloat16, device="cuda"), recs[f].receipt)
+        buf.source_collect(0)
+
+
+def test_python_refusals():
+    afd = _afd()
+    _print("refusals")
+    x = torch.zeros((8, 128), dtype=torch.bfloat16, device="cuda")
+    ends = torch.tensor([4, 8], dtype=torch.int32, device="cuda")
+    w = torch.zeros((2, 32, 128), dtype=torch.bfloat16, device="cuda")
+    xq, xs = x.to(torch.float8_e4m3fn), torch.ones((8, 1), device="cuda")
+    wq, ws = w.to(torch.float8_e4m3fn), torch.ones((2, 1, 1), device="cuda")
+    low = afd.LowRank(torch.zeros((3, 2, 8, 128), dtype=torch.bfloat16, device="cuda"),
+                      torch.zeros((3, 2, 32, 8), dtype=torch.bfloat16, device="cuda"), torch.ones(3, device="cuda"))
+    tags = torch.zeros(8, dtype=torch.int32, device="cuda")
+    afd.expert_product(x, ends, w)
+    afd.expert_product(xq, ends, wq, x_scales=xs, weight_scales=ws)
+    afd.expert_product(x, ends, w, adapters=low, row_adapters=tags)
+    bad = [
+        (TypeError, (x.float(), ends, w), {}), (ValueError, (x.cpu(), ends, w), {}), (ValueError, (x.t(), ends, w), {}),
+        (ValueError, (x[0], ends, w), {}), (ValueError, (x, ends.long(), w), {}), (ValueError, (x, ends[:1], w), {}),
+        (ValueError, (x, ends.cpu(), w), {}), (ValueError, (x, ends, w.float()), {}), (ValueError, (x, ends, w[:, :, :64]), {}),
+        (ValueError, (x, ends, w[0]), {}), (ValueError, (x, ends, w.cpu()), {}), (ValueError, (x, ends, w), dict(activation="gelu")),
+        (ValueError, (x, ends, w[:, :31].contiguous()), dict(activation="swiglu")),
+        (ValueError, (x, ends, w), dict(x_scales=xs)), (ValueError, (x, ends, w), dict(weight_scales=ws)),
+        (ValueError, (xq, ends, wq), {}), (ValueError, (xq, ends, wq), dict(x_scales=xs)),
+        (ValueError, (xq, ends, wq), dict(x_scales=xs[:4], weight_scales=ws)),
+        (ValueError, (x, ends, w), dict(row_adapters=tags)), (ValueError, (x, ends, w), dict(adapters=low)),
+        (ValueError, (x, ends, w), dict(adapters=low, row_adapters=tags[:4])),
+        (ValueError, (x, ends, w), dict(adapters=low._replace(a=low.a[:2]), row_adapters=tags)),
+        (ValueError, (x, ends, w), dict(adapters=low._replace(scaling=low.scaling[0]), row_adapters=tags)),
+        (ValueError, (x, ends, w), dict(out=torch.zeros((8, 16), dtype=torch.bfloat16, device="cuda"))),
+        (ValueError, (x, ends, w), dict(out=torch.zeros((8, 32), device="cuda"))),
+        (ValueError, (x, ends, w), dict(out_scales=xs)),
+        (ValueError, (x.clone().requires_grad_(), ends, w), {}), (ValueError, (x, ends, w.clone().requires_grad_()), {}),
+        (afd.AfdError, (x, ends, w), dict(alignment=0)), (afd.AfdError, (x[:, :32].contiguous(), ends, w[:, :, :32].contiguous()), {}),
+        (afd.AfdError, (x, ends, w[:, :24].contiguous()), {}),
+        (afd.AfdError, (x, ends, w), dict(out=torch.zeros((8, 32), device="cuda").to(torch.float8_e4m3fn), out_scales=xs)),
+    ]
+    for err, args, kw in bad:
+        with pytest.raises((err, ValueError) if err is afd.AfdError else err):
+            afd.expert_product(*args, **kw)
+    with torch.no_grad():
+        afd.expert_product(x.clone().requires_grad_(), ends, w)
+    up, down = torch.zeros((2, 128, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 128, 64), dtype=torch.bfloat16, device="cuda")
+    ex = afd.Experts(up, down)
+    assert afd.expert_ffn(x, ends, ex).shape == (8, 128)
+    with pytest.raises(ValueError):
+        afd.expert_ffn(x, ends[:1], ex)
+    with pytest.raises(ValueError):
+        afd.expert_ffn(xq, ends, ex, x_scales=xs)
+    with pytest.raises(ValueError):
+        afd.expert_ffn(x, ends, afd.Experts(up, up))
+    with pytest.raises(ValueError):
+        afd.pack_weights(up.cpu())
+    with pytest.raises(ValueError):
+        afd.pack_weights(up.transpose(1, 2))
+    with pytest.raises(afd.AfdError):
+        afd.pack_weights(torch.zeros((1, 20, 64), dtype=torch.bfloat16, device="cuda"))
+
+
+def test_a_stream_that_is_not_the_default():
+    """Inputs made on one stream and used, in order, on another."""
+    afd = _afd()
+    _print("side stream")
+    c = ref.make(13, 3, [40, 0, 90], 1, 256, 64, "bf16", S=2, rank=16)
+    want = _run_product(afd, c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _run_product(afd, c)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)

@@ -4,7 +4,7 @@ A step is one round of the whole hot path for every role: N source
 dispatches, F worker receives (layout + scatter), F worker replies (the last
 one runs the combine) and N source collects, over one seeded synthetic batch
 resident in HBM.  Replies come from identity experts computed once before
-timing (expert compute is outside the library and outside the round, as in
+timing (expert compute is outside the round, as in
 the afdEP-comm measurements, which time communication only).
 
 Every workload (the six seeded shapes) is measured by default; the top-level

@@ -229,14 +229,15 @@ __device__ __forceinline__ uint32_t split_t(float t)
     return hi | (fabsf(rest) < INFINITY ? to_bf16(rest) << 16 : 0u);   // an infinite t has no rest
 }
 
-// Adds B t of the adapters of MB row blocks to v (37 and 30 us on top of the 103 and
-// 65 us FP8 products of 256 rows per expert with about five adapters of rank 32 in
-// 64 rows: a chain of one load of t and one of B per adapter): per block, NQ column blocks per
-// kind of 4 consecutive columns of one row per lane.  wrow[] are the weight rows of
-// this lane's A-operand rows.  Per 32 ranks, every row's t is loaded once (each row
-// has one adapter), in its two bf16 parts (split_t); the distinct adapters number sub, sub + nsub, .. are taken one after
-// the other, the next one's B on its way meanwhile, and each lane adds only its own
-// row's, by selection, so an adapter's infinities reach no other request.
+// Adds B t of the adapters of MB row blocks to v (33 and 29 us on top of the 102 and
+// 64 us FP8 products of 256 rows per expert with about five adapters of rank 32 in
+// 64 rows: a chain of one load of t and one of B per adapter): per block, NQ column
+// blocks per kind of 4 consecutive columns of one row per lane.  wrow[] are the weight
+// rows of this lane's A-operand rows.  Per 32 ranks, every row's t is loaded once
+// (each row has one adapter), in its two bf16 parts (split_t); the distinct adapters
+// number sub, sub + nsub, .. are taken one after the other, the next one's B on its
+// way meanwhile, and each lane adds only its own row's, by selection, so an adapter's
+// infinities reach no other request.
 template <int KINDS, int NQ, int MB>
 __device__ __forceinline__ void add_adapters(const ProductArgs &a, int e, const int (&row)[MB], const int (&tag)[MB],
                                              const int (&wrow)[KINDS * NQ], f32x4 (&v)[MB][KINDS * NQ], int sub, int nsub)

@@ -2,8 +2,8 @@
 uploads a generated instance, runs one round through the library's Python
 binding (the C ABI), and plays the FFN with identity experts written in
 torch (expert e scales its rows by s_e = 1 + e/E and rounds to bfloat16) --
-the stand-in for the caller's expert computation, which is not part of the
-library.  It holds none of the exchange's arithmetic and never touches the
+the stand-in for a trained model's experts, cheap and exactly computed on the
+CPU too.  It holds none of the exchange's arithmetic and never touches the
 CPU oracle."""
 from __future__ import annotations
 

@@ -966,6 +966,7 @@ struct ShrinkArgs {
     int c;       // rows of one adapter's A: rank, or 2 rank gated
     int nad;
     int share;   // workgroups per expert
+    int spread;  // experts side by side: 8, or all of fewer
 };
 
 // Eight E4M3 codes to bf16 (exact: four significant bits).
@@ -1224,12 +1225,13 @@ struct Shrink {
     }
 };
 
-// Workgroup b runs on XCD b % 8; an expert's share one L2 for its rows.
+// Workgroup b runs on XCD b % 8: from eight experts on, an expert's share one L2 for
+// its rows; of fewer, each has workgroups on every XCD.
 template <bool FP8>
 __global__ __launch_bounds__(Shrink<FP8>::threads, FP8 ? 3 : 4) void k_shrink(ShrinkArgs a)
 {
     __shared__ typename Shrink<FP8>::Shared sh;
-    const int i = blockIdx.x >> 3, e = i / a.share * 8 + (blockIdx.x & 7), y = i % a.share;
+    const int i = blockIdx.x / a.spread, e = i / a.share * a.spread + blockIdx.x % a.spread, y = i % a.share;
     if (e >= a.E) return;
     const int prev = e == 0 ? 0 : min(max(a.ends[e - 1], 0), a.rows);
     const uint32_t st = (uint32_t(prev) + uint32_t(a.alpha) - 1u) / uint32_t(a.alpha) * uint32_t(a.alpha);
@@ -1335,29 +1337,49 @@ int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
     return launched();
 }
 
-// Rows per expert (by the host's bound, which is up to twice what comes) from which
-// the tiled product runs.  64 experts, H 2048, inner 768, BF16 network: with one row
-// each 138 us few and 142 us tiled, with 8 113 and 110, with 16 122 and 112, with 32
-// 169 and 116; FP8 with 16 75 and 68.  With adapters (32 of rank 16) the few-row
-// kernel, whose wavefronts share a tile's adapters, is level at 16 (197 and 200).
+// The tiled product runs from this many rows per expert on (by the host's bound, which
+// is up to twice what comes), unless the few-row kernel's items fit side by side.
+// 64 experts, H 2048, inner 768, BF16 network: with one row each 138 us few and 142 us
+// tiled, with 8 113 and 110, with 16 122 and 112, with 32 169 and 116; FP8 with 16 75
+// and 68.  With adapters (32 of rank 16) the few-row kernel, whose wavefronts share a
+// tile's adapters, is level at 16 (197 and 200).
 constexpr int64_t kManyFrom = 8, kManyFromLow = 64;
 
-template <bool LOW>
-int launch_product(const ProductPlan &p, const ProductArgs &a, bool many, hipStream_t st)
+// Items of the few-row kernel, per CU, that run side by side.  Up to there the tiled
+// product, whose larger tiles occupy few CUs, waits longer for each tile's chain of
+// steps than the few-row kernel for reading rows and weights again.
+// K 2048, N 768 gated, BF16 (items: few, tiled, us): 432: 13.2, 30.0; 1584: 32.3,
+// 46.8; 2304: 31.2, 23.9.  K 768, N 2048: 1280: 11.4, 16.0; 2304: 19.8, 16.6; FP8 640:
+// 7.9, 12.8; 1152: 13.0, 13.3; 1536: 13.2, 10.7; FP8 output (eight wavefronts for 256
+// weight rows) 240: 35.3, 41.7; 408: 38.0, 24.9.
+template <bool FP8, bool OUT8>
+constexpr int kSideBySide = OUT8 ? 1 : FP8 ? 4 : 8;
+
+template <bool FP8, bool GATED, bool OUT8, bool LOW, int NB, int KS, int CS>
+int launch_either(const ProductPlan &p, const ProductArgs &a, hipStream_t st)
 {
-    if (many) {
-        if (!p.fp8) return p.gated ? launch_many<false, true, false, LOW>(p, a, st) : launch_many<false, false, false, LOW>(p, a, st);
-        if (p.out8) return launch_many<true, true, true, LOW>(p, a, st);
-        return p.gated ? launch_many<true, true, false, LOW>(p, a, st) : launch_many<true, false, false, LOW>(p, a, st);
-    }
-    // Workgroups of four wavefronts leave the most loads in flight per CU: 32
+    typedef Few<FP8, GATED, OUT8, LOW, NB, KS, CS> F;
+    // the rows' bound without what alignment alone can add
+    const int64_t each = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E;
+    const int64_t items = tile_bound(p, F::rows) * ((p.n + F::BN - 1) / F::BN);
+    if (each >= (LOW ? kManyFromLow : kManyFrom) && items > kComputeUnits * kSideBySide<FP8, OUT8>)
+        return launch_many<FP8, GATED, OUT8, LOW>(p, a, st);
+    return launch_few<FP8, GATED, OUT8, LOW, NB, KS, CS>(p, a, st);
+}
+
+template <bool LOW>
+int launch_product(const ProductPlan &p, const ProductArgs &a, hipStream_t st)
+{
+    // Few rows: workgroups of four wavefronts leave the most loads in flight per CU: 32
     // weight rows (BF16; 64 take 133 us instead of 129 for 1024 rows over 64
     // experts, H 2048, inner 768) or 64 (FP8: 32 take 35 us instead of 32 for the
     // second product).  An FP8 output needs 256 weight rows, one scale block.
     if (!p.fp8)
-        return p.gated ? launch_few<false, true, false, LOW, 2, 4, 1>(p, a, st) : launch_few<false, false, false, LOW, 2, 4, 1>(p, a, st);
-    if (p.out8) return launch_few<true, true, true, LOW, 4, 2, 4>(p, a, st);
-    return p.gated ? launch_few<true, true, false, LOW, 4, 4, 1>(p, a, st) : launch_few<true, false, false, LOW, 4, 4, 1>(p, a, st);
+        return p.gated ? launch_either<false, true, false, LOW, 2, 4, 1>(p, a, st)
+                       : launch_either<false, false, false, LOW, 2, 4, 1>(p, a, st);
+    if (p.out8) return launch_either<true, true, true, LOW, 4, 2, 4>(p, a, st);
+    return p.gated ? launch_either<true, true, false, LOW, 4, 4, 1>(p, a, st)
+                   : launch_either<true, false, false, LOW, 4, 4, 1>(p, a, st);
 }
 
 }  // namespace
@@ -1384,7 +1406,8 @@ int be_launch_product(const ProductPlan &p, void *stream)
         // than it can have pairs of an adapter and 32 rows of A
         const int pairs = std::min(p.nad, int(std::min<int64_t>(p.rows, AFD_MAX_ADAPTERS))) * ((s.c + 31) / 32);
         s.share = std::max(1, std::min(kComputeUnits * 8 / p.E, pairs));
-        const unsigned grid = unsigned((p.E + 7) / 8 * 8 * s.share);
+        s.spread = std::min(p.E, 8);
+        const unsigned grid = unsigned((p.E + s.spread - 1) / s.spread * s.spread * s.share);
         if (p.fp8) hipLaunchKernelGGL(k_shrink<true>, dim3(grid), dim3(Shrink<true>::threads), 0, st, s);
         else hipLaunchKernelGGL(k_shrink<false>, dim3(grid), dim3(Shrink<false>::threads), 0, st, s);
         if (launched() != 0) return 1;
@@ -1410,9 +1433,7 @@ int be_launch_product(const ProductPlan &p, void *stream)
     a.wstep = p.packed ? 2048 : 128;
     a.nad = p.nad;
     a.rank = p.rank;
-    // the rows' bound without what alignment alone can add
-    const bool many = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E >= (p.nad > 0 ? kManyFromLow : kManyFrom);
-    return p.nad > 0 ? launch_product<true>(p, a, many, st) : launch_product<false>(p, a, many, st);
+    return p.nad > 0 ? launch_product<true>(p, a, st) : launch_product<false>(p, a, st);
 }
 
 int be_launch_pack(const void *w, void *out, int64_t rows, int64_t row_bytes, void *stream)

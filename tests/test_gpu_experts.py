@@ -11,6 +11,7 @@ from tests import experts_ref as ref
 pytestmark = pytest.mark.gpu
 
 FILL = -7.25
+ARENA = 0        # rows of the arrays where more than the case's: the host's bound picks the kernels
 
 
 def _afd():
@@ -41,19 +42,40 @@ def _check(got, want, tol, live, what):
                            f"worst {float((err / tol[live]).nan_to_num(float('inf')).max())} of the bound")
 
 
+def _widen(t, rows):
+    """t on the GPU, with the arena's further rows behind it: NaN, or tag 0."""
+    if t is None or ARENA <= rows:
+        return _dev(t)
+    if t.dtype is torch.float8_e4m3fn:
+        w = torch.full((ARENA, t.shape[1]), 0x7F, dtype=torch.uint8, device="cuda")
+        w[:rows] = t.view(torch.uint8).cuda()
+        return w.view(torch.float8_e4m3fn)
+    w = torch.full((ARENA, *t.shape[1:]), 0 if t.dtype is torch.int32 else float("nan"), dtype=t.dtype, device="cuda")
+    w[:rows] = t.cuda()
+    return w
+
+
+def _cut(t, rows, fill):
+    """The case's rows; those behind them still hold `fill`."""
+    rest = t[rows:].float()
+    assert torch.equal(rest, torch.full_like(rest, fill)), "a row behind the last expert was written"
+    return t[:rows]
+
+
 def _run_product(afd, c, out8=False):
     n = c["w"].shape[1] // (2 if c["gated"] else 1)
     ends = torch.tensor(c["ends"], dtype=torch.int32).cuda()
-    kw = dict(alignment=c["alpha"], x_scales=_dev(c["xs"]), weight_scales=_dev(c["ws"]),
-              activation="swiglu" if c["gated"] else None, adapters=_low(afd, c["low"]), row_adapters=_dev(c["tags"]))
+    R = c["rows"]
+    kw = dict(alignment=c["alpha"], x_scales=_widen(c["xs"], R), weight_scales=_dev(c["ws"]),
+              activation="swiglu" if c["gated"] else None, adapters=_low(afd, c["low"]), row_adapters=_widen(c["tags"], R))
     if out8:
-        out = torch.full((c["rows"], n), FILL, device="cuda").to(torch.float8_e4m3fn)
-        outs = torch.full((c["rows"], n // 128), 1.0, device="cuda")
-        afd.expert_product(_dev(c["x"]), ends, _dev(c["w"]), out=out, out_scales=outs, **kw)
-        return out, outs
-    out = torch.full((c["rows"], n), FILL, dtype=torch.bfloat16, device="cuda")
-    afd.expert_product(_dev(c["x"]), ends, _dev(c["w"]), out=out, **kw)
-    return out
+        out = torch.full((max(R, ARENA), n), FILL, device="cuda").to(torch.float8_e4m3fn)
+        outs = torch.full((max(R, ARENA), n // 128), 1.0, device="cuda")
+        afd.expert_product(_widen(c["x"], R), ends, _dev(c["w"]), out=out, out_scales=outs, **kw)
+        return _cut(out, R, float(torch.tensor(FILL).to(torch.float8_e4m3fn).float())), _cut(outs, R, 1.0)
+    out = torch.full((max(R, ARENA), n), FILL, dtype=torch.bfloat16, device="cuda")
+    afd.expert_product(_widen(c["x"], R), ends, _dev(c["w"]), out=out, **kw)
+    return _cut(out, R, FILL)
 
 
 COUNTS = {
@@ -102,9 +124,10 @@ def test_packed_weights_give_the_same_bits(shape, dtype, gated, k, n):
     E, m = w.shape[:2]
     rows = w.view(torch.uint8).reshape(E, m // 16, 16, k * w.element_size() // 16, 16)
     assert torch.equal(p.data, rows.permute(0, 1, 3, 2, 4).reshape(-1))
-    kw = dict(alignment=alpha, x_scales=_dev(c["xs"]), weight_scales=_dev(c["ws"]), activation="swiglu" if gated else None)
-    x, ends = _dev(c["x"]), torch.tensor(c["ends"], dtype=torch.int32).cuda()
-    a, b = (torch.full((c["rows"], n), FILL, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kw = dict(alignment=alpha, x_scales=_widen(c["xs"], c["rows"]), weight_scales=_dev(c["ws"]),
+              activation="swiglu" if gated else None)
+    x, ends = _widen(c["x"], c["rows"]), torch.tensor(c["ends"], dtype=torch.int32).cuda()
+    a, b = (torch.full((x.shape[0], n), FILL, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     afd.expert_product(x, ends, w, out=a, **kw)
     afd.expert_product(x, ends, p, out=b, **kw)
     assert torch.equal(a, b)
@@ -223,12 +246,14 @@ def test_ffn(shape, dtype, hidden, inner, S, rank):
     E = len(counts)
     u = ref.make(6, E, counts, alpha, hidden, 2 * inner, dtype, S=S, rank=rank, gated=True)
     d = ref.make(7, E, counts, alpha, inner, hidden, dtype, S=S, rank=rank)
-    out = torch.full((u["rows"], hidden), FILL, dtype=torch.bfloat16, device="cuda")
-    afd.expert_ffn(_dev(u["x"]), torch.tensor(u["ends"], dtype=torch.int32).cuda(),
+    R = u["rows"]
+    out = torch.full((max(R, ARENA), hidden), FILL, dtype=torch.bfloat16, device="cuda")
+    afd.expert_ffn(_widen(u["x"], R), torch.tensor(u["ends"], dtype=torch.int32).cuda(),
                    afd.Experts(_dev(u["w"]), _dev(d["w"]), _dev(u["ws"]), _dev(d["ws"])), alignment=alpha,
-                   x_scales=_dev(u["xs"]),
+                   x_scales=_widen(u["xs"], R),
                    adapters=afd.ExpertAdapters(_low(afd, u["low"]), _low(afd, d["low"])) if S else None,
-                   row_adapters=_dev(u["tags"]), out=out)
+                   row_adapters=_widen(u["tags"], R), out=out)
+    out = _cut(out, R, FILL)
     want, tol, live = ref.run_ffn(u["x"], u["xs"], u["w"], u["ws"], d["w"], d["ws"], u["low"], d["low"], u["tags"],
                                   u["ends"], alpha, u["rows"])
     _check(out, want, ref.rounded(want, tol), live, f"{shape} {dtype}")
@@ -561,3 +586,78 @@ def test_a_stream_that_is_not_the_default():
         got = _run_product(afd, c)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, want)
+
+
+# The products choose between two kernels by the host's bound of the rows.  The cases
+# above leave most of these small sizes to the few-row kernel; in an arena of many rows
+# (its first ones used) the tiled kernel computes them.
+
+@pytest.fixture
+def arena(monkeypatch):
+    monkeypatch.setitem(globals(), "ARENA", 32 * 2100)
+
+
+TILED = ["one_row", "edges", "aligned", "large", "many", "tall", "taller", "skewed"]
+
+
+@pytest.mark.parametrize("shape", TILED)
+@pytest.mark.parametrize("dtype,gated,k,n", [
+    ("bf16", False, 64, 16), ("bf16", False, 704, 272), ("bf16", True, 320, 96), ("bf16", True, 512, 336),
+    ("fp8", False, 128, 16), ("fp8", False, 768, 400), ("fp8", True, 384, 128), ("fp8", True, 256, 384)])
+def test_product_in_an_arena(arena, shape, dtype, gated, k, n):
+    test_product(shape, dtype, gated, k, n)
+
+
+@pytest.mark.parametrize("shape", ["edges", "large", "taller"])
+@pytest.mark.parametrize("dtype,gated,k,n", [("bf16", False, 320, 144), ("bf16", True, 192, 80), ("fp8", False, 384, 272),
+                                             ("fp8", True, 256, 256)])
+def test_packed_weights_in_an_arena(arena, shape, dtype, gated, k, n):
+    test_packed_weights_give_the_same_bits(shape, dtype, gated, k, n)
+
+
+@pytest.mark.parametrize("shape", ["one_row", "edges", "aligned", "large", "many", "skewed"])
+@pytest.mark.parametrize("k,n,S", [(256, 128, 0), (384, 384, 0), (256, 256, 3)])
+def test_product_fp8_out_in_an_arena(arena, shape, k, n, S):
+    test_product_fp8_out(shape, k, n, S)
+
+
+@pytest.mark.parametrize("shape", ["one_row", "empty_and_one", "edges", "aligned", "large", "skewed"])
+@pytest.mark.parametrize("dtype,gated,k,n,S,rank", [
+    ("bf16", False, 320, 144, 1, 8), ("bf16", True, 256, 96, 5, 16), ("bf16", True, 192, 64, 40, 24),
+    ("bf16", False, 256, 272, 3, 128), ("fp8", False, 256, 144, 7, 40), ("fp8", True, 384, 128, 2, 64)])
+def test_adapters_in_an_arena(arena, shape, dtype, gated, k, n, S, rank):
+    test_adapters(shape, dtype, gated, k, n, S, rank)
+
+
+@pytest.mark.parametrize("shape", ["one_row", "edges", "aligned", "large", "tall"])
+@pytest.mark.parametrize("dtype,hidden,inner,S,rank", [
+    ("bf16", 256, 192, 0, 0), ("fp8", 256, 384, 0, 0), ("bf16", 512, 64, 4, 16), ("fp8", 256, 128, 6, 8)])
+def test_ffn_in_an_arena(arena, shape, dtype, hidden, inner, S, rank):
+    test_ffn(shape, dtype, hidden, inner, S, rank)
+
+
+def test_infinities_in_an_arena(arena):
+    for gated in (False, True):
+        test_adapter_infinities_stay_with_their_rows(gated, 300)
+    test_row_infinities_stay_in_their_rows()
+    test_fp8_out_of_tiny_and_infinite_rows(200)
+
+
+def test_tiled_rows_behind_four_gib():
+    """The tiled kernel across 4 GiB of x: rows of zeros but for the first and last."""
+    afd = _afd()
+    _print("tiled rows behind 4 GiB")
+    k, n, many = 2048, 2304, (1 << 20) + 5
+    x = torch.zeros((many, k), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(9)
+    v = torch.randn(8, k, generator=g).bfloat16()
+    x[:3], x[-5:] = v[:3].cuda(), v[3:].cuda()
+    w = (torch.randn(2, n, k, generator=g) * k ** -0.5).bfloat16()
+    out = torch.full((many, n), FILL, dtype=torch.bfloat16, device="cuda")
+    afd.expert_product(x, torch.tensor([3, many], dtype=torch.int32).cuda(), w.cuda(), out=out)
+    got = torch.cat([out[:3], out[-5:]]).double().cpu()
+    for j, sl in enumerate((slice(0, 3), slice(3, 8))):
+        vd = v[sl].double()
+        want, tol = ref.product(vd, torch.zeros_like(vd), w[j].double(), False, None, None, j)
+        assert ((got[sl] - want).abs() <= ref.rounded(want, tol)).all()
+    assert not out[3:-5].any()

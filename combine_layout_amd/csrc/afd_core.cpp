@@ -297,6 +297,13 @@ bool weights_ok(const afd_product_weights *w, bool fp8, bool adapters)
     return w->a && w->b && w->scaling && aligned(w->a, 16) && aligned(w->b, 16) && aligned(w->scaling, 4);
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 ProductPlan plan_product(const afd_product_config &c, int64_t rows, const void *x, const float *xs,
                          const int32_t *ends, const int32_t *tags, const afd_product_weights &w, void *out, float *outs,
                          void *t)
@@ -696,6 +703,8 @@ afd_status afd_expert_product(const afd_product_config *cfg, int64_t rows, const
     if (out8 ? !out_scales || !aligned(out_scales, 4) : out_scales != nullptr) return AFD_E_ARG;
     if (low ? !row_adapters || !aligned(row_adapters, 4) : row_adapters != nullptr) return AFD_E_ARG;
     if (!weights_ok(weights, fp8, low)) return AFD_E_ARG;
+    // a tile's rows of x are read while another tile's rows of out are written
+    if (overlap(x, size_t(rows) * cfg->k * (fp8 ? 1 : 2), out, size_t(rows) * cfg->n * (out8 ? 1 : 2))) return AFD_E_ARG;
     const size_t need = product_workspace(*cfg, rows);
     if (need > 0 && (!workspace || !aligned(workspace, 256))) return AFD_E_ARG;
     if (workspace_bytes < need) return AFD_E_CAPACITY;

@@ -1226,7 +1226,8 @@ struct Shrink {
 };
 
 // Workgroup b runs on XCD b % 8: from eight experts on, an expert's share one L2 for
-// its rows; of fewer, each has workgroups on every XCD.
+// its rows; of fewer, each has workgroups on every XCD (the network of 60 rows, one
+// expert, 64 adapters of rank 64: 60 us instead of 91).
 template <bool FP8>
 __global__ __launch_bounds__(Shrink<FP8>::threads, FP8 ? 3 : 4) void k_shrink(ShrinkArgs a)
 {

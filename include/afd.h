@@ -472,7 +472,8 @@ typedef struct {
  * A row r of expert j with adapter i = row_adapters[r] in [0, num_adapters)
  * adds scaling[i] * B_ij (A_ij x[r]) to its sums before the activation (with
  * SwiGLU the gate rows of B take the gate's A, the up rows the up's); a row
- * with any other value has no adapter.  An adapter reaches no row but its own.
+ * with any other value has no adapter.  An adapter reaches no row but its own;
+ * where its B holds an infinity, its rows' values may be NaN.
  */
 typedef struct {
     const void *w;
@@ -493,7 +494,7 @@ afd_status afd_product_query(const afd_product_config *cfg, int64_t rows, size_t
  *   x, x_scales   device [rows, k]; [rows, k/128] FP32 (FP8, else NULL)
  *   ends          device [num_experts]
  *   row_adapters  device [rows] (with adapters, else NULL; see afd_worker_tags)
- *   out           device [rows, n], not overlapping the inputs
+ *   out           device [rows, n], not overlapping the inputs (over x: AFD_E_ARG)
  *   out_scales    device [rows, n/128] FP32 (FP8 output, else NULL)
  *   workspace     device, at least afd_product_query bytes, 256-byte aligned;
  *                 in use until the call's work has run
@@ -534,7 +535,8 @@ typedef struct {
 afd_status afd_ffn_query(const afd_ffn_config *cfg, int64_t rows, size_t *workspace_bytes);
 
 /* afd_expert_ffn: arguments and errors as afd_expert_product; out is a whole
- * reply for afd_worker_reply. */
+ * reply for afd_worker_reply, and may be x's own memory (x is read only by the
+ * first product). */
 afd_status afd_expert_ffn(const afd_ffn_config *cfg, int64_t rows, const void *x, const float *x_scales,
                           const int32_t *ends, const int32_t *row_adapters, const afd_product_weights *up,
                           const afd_product_weights *down, void *out, void *workspace, size_t workspace_bytes,

@@ -256,3 +256,14 @@ def test_python_calls_refuse_host_tensors():
         afd.expert_ffn(x, ends, None)
     with pytest.raises(ValueError):
         afd.pack_weights(w)
+
+
+def test_out_over_x_refused(lib):
+    """x [100, 256] bf16 holds 51200 bytes, out [100, 128] 25600."""
+    log(lib)
+    for out in (X, X + 51200 - 16, X - 25600 + 16):
+        assert call(lib, pcfg(), out=out) == nat.AFD_E_ARG
+    assert not log(lib)
+    for out in (X + 51200, X - 25600):
+        assert call(lib, pcfg(), out=out) == 0
+    assert len(log(lib)) == 2

@@ -661,3 +661,26 @@ def test_tiled_rows_behind_four_gib():
         want, tol = ref.product(vd, torch.zeros_like(vd), w[j].double(), False, None, None, j)
         assert ((got[sl] - want).abs() <= ref.rounded(want, tol)).all()
     assert not out[3:-5].any()
+
+
+@pytest.mark.parametrize("S", [0, 3])
+def test_network_into_its_own_rows(S):
+    """The network's rows may take the place of x; a single product refuses that."""
+    afd = _afd()
+    _print("in place", S)
+    counts, alpha = COUNTS["aligned"]
+    E, H, inner = len(counts), 256, 128
+    u = ref.make(14, E, counts, alpha, H, 2 * inner, "bf16", S=S, rank=8 if S else 0, gated=True)
+    d = ref.make(15, E, counts, alpha, inner, H, "bf16", S=S, rank=8 if S else 0)
+    x, ends = u["x"].cuda(), torch.tensor(u["ends"], dtype=torch.int32).cuda()
+    kw = dict(alignment=alpha, row_adapters=_dev(u["tags"]),
+              adapters=afd.ExpertAdapters(_low(afd, u["low"]), _low(afd, d["low"])) if S else None)
+    ex = afd.Experts(u["w"].cuda(), d["w"].cuda())
+    want = afd.expert_ffn(x, ends, ex, **kw)
+    got = afd.expert_ffn(x, ends, ex, out=x, **kw)
+    live = u["live"].cuda()
+    assert got.data_ptr() == x.data_ptr() and torch.equal(got[live], want[live])
+    assert torch.isnan(x[~live]).all()
+    square = torch.zeros((E, H, H), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(afd.AfdError):
+        afd.expert_product(x, ends, square, alignment=alpha, out=x)

@@ -86,8 +86,14 @@ def raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _alignment(alpha):
+    if not 0 < alpha < 2 ** 31:
+        raise ValueError("alignment must be in [1, 2^31)")
+
+
 @functools.lru_cache(maxsize=256)
 def _product_plan(rows, *cfg):
+    _alignment(cfg[1])
     c, ws = nat.ProductConfig(*cfg), ctypes.c_size_t(0)
     nat.check(nat.load().afd_product_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_product")
     return c, ws.value
@@ -95,6 +101,7 @@ def _product_plan(rows, *cfg):
 
 @functools.lru_cache(maxsize=256)
 def _ffn_plan(rows, *cfg):
+    _alignment(cfg[1])
     c, ws = nat.FfnConfig(*cfg), ctypes.c_size_t(0)
     nat.check(nat.load().afd_ffn_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_ffn")
     return c, ws.value

@@ -548,7 +548,8 @@ def test_python_refusals():
         (ValueError, (x, ends, w), dict(out=torch.zeros((8, 32), device="cuda"))),
         (ValueError, (x, ends, w), dict(out_scales=xs)),
         (ValueError, (x.clone().requires_grad_(), ends, w), {}), (ValueError, (x, ends, w.clone().requires_grad_()), {}),
-        (afd.AfdError, (x, ends, w), dict(alignment=0)), (afd.AfdError, (x[:, :32].contiguous(), ends, w[:, :, :32].contiguous()), {}),
+        (ValueError, (x, ends, w), dict(alignment=0)), (ValueError, (x, ends, w), dict(alignment=2 ** 32 + 1)),
+        (afd.AfdError, (x[:, :32].contiguous(), ends, w[:, :, :32].contiguous()), {}),
         (afd.AfdError, (x, ends, w[:, :24].contiguous()), {}),
         (afd.AfdError, (x, ends, w), dict(out=torch.zeros((8, 32), device="cuda").to(torch.float8_e4m3fn), out_scales=xs)),
     ]
@@ -562,6 +563,8 @@ def test_python_refusals():
     assert afd.expert_ffn(x, ends, ex).shape == (8, 128)
     with pytest.raises(ValueError):
         afd.expert_ffn(x, ends[:1], ex)
+    with pytest.raises(ValueError):
+        afd.expert_ffn(x, ends, ex, alignment=2 ** 32)
     with pytest.raises(ValueError):
         afd.expert_ffn(xq, ends, ex, x_scales=xs)
     with pytest.raises(ValueError):

@@ -593,20 +593,40 @@ __device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b)
     return (g & 1) * 16 + (g >> 1) * 8;
 }
 
-// 64 lanes x 16 (or 4) bytes of buffer `r`, lane by lane at voff + soff, to LDS
-// from `lds` on.  In assembly, because the compiler waits for every such load it
-// knows of before any LDS read that it cannot tell apart, which would end the
-// overlap of one step's arithmetic with the next one's loads; the waits are
-// written out where a stage is first read.  (These kernels use M0 nowhere else.)
-__device__ __forceinline__ void to_lds16(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(uniform(lds)),
-                 "v"(voff), "s"(uniform(r)), "s"(uniform(soff)));
-}
+// N loads of 64 lanes x 16 bytes (or one of 64 x 4) of buffer `r`, lane by lane at
+// voff[i] + soff, to LDS from `lds` + i STEP on.  In assembly, because the compiler
+// waits for every such load it knows of before any LDS read that it cannot tell apart,
+// which would end the overlap of one step's arithmetic with the next one's loads; the
+// waits are written out where a stage is first read.
+//
+// The compiler places no wait states inside assembly, nor does the hardware: a vector
+// memory instruction may read a scalar register five wait states after a vector
+// instruction (the v_readfirstlane of uniform(), a register spilled to lanes) wrote it,
+// and use M0 one after.  All of a block's registers are written before it, so the wait
+// stands once per block, ahead of its first load: s_mov and s_nop 3.
 __device__ __forceinline__ void to_lds4(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(uniform(lds)),
-                 "v"(voff), "s"(uniform(r)), "s"(uniform(soff)));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(uniform(lds)), "v"(voff),
+                 "s"(uniform(r)), "s"(uniform(soff))
+                 : "m0");
+}
+template <uint32_t STEP>
+__device__ __forceinline__ void to_lds16(u32x4 r, const uint32_t (&voff)[2], uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %3, %4 offen lds\n\t"
+                 "s_add_u32 m0, m0, %5\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds" ::"s"(uniform(lds)),
+                 "v"(voff[0]), "v"(voff[1]), "s"(uniform(r)), "s"(uniform(soff)), "n"(STEP)
+                 : "m0", "scc");
+}
+template <uint32_t STEP>
+__device__ __forceinline__ void to_lds16(u32x4 r, const uint32_t (&voff)[4], uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %5, %6 offen lds\n\t"
+                 "s_add_u32 m0, m0, %7\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %5, %6 offen lds\n\t"
+                 "s_add_u32 m0, m0, %7\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %5, %6 offen lds\n\t"
+                 "s_add_u32 m0, m0, %7\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %5, %6 offen lds" ::"s"(uniform(lds)),
+                 "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(uniform(r)), "s"(uniform(soff)), "n"(STEP)
+                 : "m0", "scc");
 }
 
 template <int WM_, int WN_, int MX_, int ST_>
@@ -708,10 +728,8 @@ struct Many {
     __device__ __forceinline__ void issue(const Items &it)
     {
         const uint32_t at = lds + uint32_t(ahead_stage) * stage_bytes, xu = uint32_t(ahead_u) * 128u, wu = uint32_t(ahead_u) * uint32_t(a.wstep);
-#pragma unroll
-        for (int i = 0; i < S::nw; ++i) to_lds16(ahead.wr, wo[i], wu, at + S::xbytes + uint32_t(i * S::waves + wave) * 1024u);
-#pragma unroll
-        for (int i = 0; i < S::nx; ++i) to_lds16(ahead.xr, xo[i], xu, at + uint32_t(i * S::waves + wave) * 1024u);
+        to_lds16<S::waves * 1024>(ahead.wr, wo, wu, at + S::xbytes + uint32_t(wave) * 1024u);
+        to_lds16<S::waves * 1024>(ahead.xr, xo, xu, at + uint32_t(wave) * 1024u);
         if (FP8) to_lds4(ahead.sr, so, uint32_t(ahead_u) * 4u, at + S::scales + uint32_t(wave) * 256u);
         ahead_stage = ahead_stage + 1 == S::ST ? 0 : ahead_stage + 1;
         if (++ahead_u == nu) {

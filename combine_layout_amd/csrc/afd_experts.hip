@@ -604,6 +604,8 @@ __device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b)
 // instruction (the v_readfirstlane of uniform(), a register spilled to lanes) wrote it,
 // and use M0 one after.  All of a block's registers are written before it, so the wait
 // stands once per block, ahead of its first load: s_mov and s_nop 3.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // that M0, which the compiler sets where it needs it, is named as written
 __device__ __forceinline__ void to_lds4(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(uniform(lds)), "v"(voff),
@@ -628,6 +630,7 @@ __device__ __forceinline__ void to_lds16(u32x4 r, const uint32_t (&voff)[4], uin
                  "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(uniform(r)), "s"(uniform(soff)), "n"(STEP)
                  : "m0", "scc");
 }
+#pragma clang diagnostic pop
 
 template <int WM_, int WN_, int MX_, int ST_>
 struct Shape {

@@ -660,9 +660,10 @@ struct Many {
     int xp[2], wp[2];                      // and of its own two of a block in LDS
     int nu;
 
-    // the next load: its item, step and stage
+    // the next load: its place among the items, its item and stage
+    LoadCursor next;
     ManyItem ahead;
-    int ahead_u, ahead_at, ahead_stage;
+    int ahead_stage;
 
     static __device__ __forceinline__ int key(int row) { return row & 7; }
 
@@ -708,9 +709,10 @@ struct Many {
         return t;
     }
 
-    __device__ __forceinline__ void load_item(int at, bool live)
+    __device__ __forceinline__ void load_item()
     {
-        ahead.t = tile_of(at, ahead.c0);
+        const bool live = next.live;
+        ahead.t = tile_of(next.at, ahead.c0);
         const Tile &t = ahead.t;
         const int c0 = ahead.c0;
         // behind the last item the loads go on without a byte, so that their number stays the same
@@ -724,29 +726,24 @@ struct Many {
                 ahead.sr = buffer_of(a.ws + (int64_t(t.e) * mb + c0 / 128) * nu,
                                      live ? uint32_t(mb - c0 / 128) * uint32_t(nu) * 4u : 0u);
         }
-        ahead_u = 0;
     }
 
     // The next step's loads on their way.
     __device__ __forceinline__ void issue(const Items &it)
     {
-        const uint32_t at = lds + uint32_t(ahead_stage) * stage_bytes, xu = uint32_t(ahead_u) * 128u, wu = uint32_t(ahead_u) * uint32_t(a.wstep);
+        const uint32_t at = lds + uint32_t(ahead_stage) * stage_bytes, xu = uint32_t(next.u) * 128u, wu = uint32_t(next.u) * uint32_t(a.wstep);
         to_lds16<S::waves * 1024>(ahead.wr, wo, wu, at + S::xbytes + uint32_t(wave) * 1024u);
         to_lds16<S::waves * 1024>(ahead.xr, xo, xu, at + uint32_t(wave) * 1024u);
-        if (FP8) to_lds4(ahead.sr, so, uint32_t(ahead_u) * 4u, at + S::scales + uint32_t(wave) * 256u);
+        if (FP8) to_lds4(ahead.sr, so, uint32_t(next.u) * 4u, at + S::scales + uint32_t(wave) * 256u);
         ahead_stage = ahead_stage + 1 == S::ST ? 0 : ahead_stage + 1;
-        if (++ahead_u == nu) {
-            const bool live = ahead_at + it.step < it.end;
-            if (live) ahead_at += it.step;
-            load_item(ahead_at, live);
-        }
+        if (next.advance(nu, it.end, it.step)) load_item();
     }
 
     __device__ __forceinline__ void begin(const Items &it)
     {
-        ahead_at = it.at;
+        next = LoadCursor{it.at, 0, true};
         ahead_stage = 0;
-        load_item(it.at, true);
+        load_item();
 #pragma unroll
         for (int i = 0; i < S::ST - 1; ++i) issue(it);
     }

@@ -198,6 +198,25 @@ struct ProductPlan {
     uint16_t *t = nullptr;           // [rows][2][(gated ? 2 : 1) * rank] two bf16 parts of every row's scaling * A x
 };
 
+// Where the tiled product's next load stands: step u of its item `at` (the workgroup's
+// are at, at + step, .. below end), of nu steps each.  Loads run ahead of the arithmetic,
+// and their number is the same for every step; behind the last item they go on without
+// a byte (an empty buffer) and at step 0: a step's scalar offset may be no larger than its
+// buffer, because the hardware's range check is given as offset >= size - scalar offset.
+struct LoadCursor {
+    int at, u;
+    bool live;   // false: behind the last item
+    // To the next step; true if another item begins, or the last one has ended.
+    constexpr bool advance(int nu, int end, int step)
+    {
+        if (!live || ++u < nu) return false;
+        u = 0;
+        live = at + step < end;
+        if (live) at += step;
+        return true;
+    }
+};
+
 // Contexts made by afd_create_static use a static scratch array of this many
 // bytes per GPU as their workspace (one such context per device at a time).
 constexpr size_t kStaticScratchBytes = size_t(AFD_STATIC_SCRATCH_BYTES);

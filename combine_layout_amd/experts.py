@@ -14,6 +14,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as nat
 
@@ -39,9 +40,11 @@ class PackedWeights:
 def pack_weights(w) -> PackedWeights:
     """A packed copy of row-major weights [E, m, k], bf16 or float8_e4m3fn, m a
     multiple of 16 and k of 64 (float8: 128).  The products read runs of
-    1024 bytes of it, faster than rows; the results are the same."""
+    1024 bytes of it, faster than rows; the results are the same.  The copy has no
+    gradient: weights that ask for one are refused unless gradients are off."""
     if isinstance(w, PackedWeights):
         return w
+    _no_gradients(w)
     if w.dim() != 3 or w.device.type != "cuda" or not w.is_contiguous():
         raise ValueError("weights must be a contiguous [E, m, k] tensor on a GPU")
     E, m, k = w.shape
@@ -57,14 +60,16 @@ def pack_weights(w) -> PackedWeights:
 class Experts:
     """Weights of a partition's experts, bf16, or float8_e4m3fn with float32
     scales per 128 x 128 block, laid out once: up and down are kept as packed
-    copies (pack_weights), and the tensors passed here can go.
+    copies (pack_weights), and the tensors passed here can go.  Like the copies,
+    the scales are kept without a gradient, and refused where they ask for one.
 
     up [E, 2*inner, hidden] (gate rows, then up rows), down [E, hidden, inner],
     up_scales [E, 2*inner/128, hidden/128], down_scales [E, hidden/128, inner/128]."""
 
     def __init__(self, up, down, up_scales=None, down_scales=None):
+        _no_gradients(up_scales, down_scales)
         self.up, self.down = pack_weights(up), pack_weights(down)
-        self.up_scales, self.down_scales = up_scales, down_scales
+        self.up_scales, self.down_scales = (None if s is None else s.detach() for s in (up_scales, down_scales))
 
 
 class ExpertAdapters(NamedTuple):
@@ -130,11 +135,16 @@ def _number_and_rank(low):
 
 
 def _no_gradients(*tensors):
-    """These are forward calls: what asks for a gradient would silently get none."""
+    """These are forward calls: what asks for a gradient, or carries a forward
+    one, would silently lose it."""
     if torch.is_grad_enabled():
         for t in tensors:
             if getattr(t, "requires_grad", False):
                 raise ValueError("the experts' calls have no gradients: detach their inputs or call under no_grad()")
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("the experts' calls have no gradients: pass the primal of a dual tensor")
 
 
 def _weights(what, w, scales, low, E, m, k, code, dtype, gated, device):
@@ -195,11 +205,11 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
     A float8 swiglu product writes float8 rows when `out` is a float8_e4m3fn
     tensor, with their scales in out_scales float32 [rows, n/128].
     Without `out` the result is new memory, its padding rows undefined.
-    Runs on x's device and its current stream; forward only (inputs that ask
-    for a gradient are refused unless gradients are off).
+    Runs on x's device and its current stream; forward only (tensors that ask
+    for a gradient are refused unless gradients are off, dual tensors always).
     """
+    _no_gradients(x, weight, x_scales, weight_scales, out, out_scales, *(adapters or ()))
     dev = _x(x)
-    _no_gradients(x, weight, *(adapters or ()))
     R, k = x.shape
     code, dtype = _act_dtype(x)
     if activation not in nat.ACTIVATIONS:
@@ -242,8 +252,8 @@ def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapter
     rows' own format (bf16, or float8_e4m3fn with a scale per row and 128
     columns).  adapters: pairs beside both projections, of one rank and number.
     """
+    _no_gradients(x, x_scales, out, *(adapters.up + adapters.down if adapters is not None else ()))
     dev = _x(x)
-    _no_gradients(x, *(adapters.up + adapters.down if adapters is not None else ()))
     R, hidden = x.shape
     code, dtype = _act_dtype(x)
     if experts.up.shape[1] % 2:

@@ -256,9 +256,14 @@ class Buffer:
         """The reply of partition f: its experts' network over the received
         rows (expert_ffn with the buffer's layout), [receive_rows, H] BF16,
         ready for worker_reply.  row_adapters: worker_tags of the tokens'
-        adapters."""
+        adapters.  A receive of an earlier round is refused (AFD_E_ORDER): its
+        arena and its ends hold the last enqueued round's."""
         if received.receipt.partition != f:
             raise ValueError("received belongs to another partition")
+        info = nat.RoundInfo()
+        nat.check(self.lib.afd_get_round_info(self.ctx, ctypes.byref(info)), "worker_experts")
+        if received.receipt.round != info.round:
+            raise nat.AfdError(nat.AFD_E_ORDER, "worker_experts: a receive of an earlier round")
         return _experts.expert_ffn(received.rows, received.ends, experts, alignment=self.alpha,
                                    x_scales=received.scales, adapters=adapters, row_adapters=row_adapters, out=out)
 

@@ -47,8 +47,8 @@ def test_product(lib, kw, kinds, rows):
     # the first width whose expert holds 2^31 bytes
     step, row = 128 if c.out_dtype else 16, kinds * c.k * (1 if c.dtype else 2)
     over = -(-(1 << 31) // row // step) * step
-    assert call(lib, pcfg(num_experts=512, **dict(kw, n=over))) == nat.AFD_E_SHAPE
-    assert call(lib, pcfg(num_experts=512, **dict(kw, n=over - step))) == 0
+    assert call(lib, pcfg(num_experts=512, **dict(kw, n=over)), **fake) == nat.AFD_E_SHAPE
+    assert call(lib, pcfg(num_experts=512, **dict(kw, n=over - step)), **fake) == 0
     log(lib)
 
 

@@ -63,7 +63,7 @@ class ProductConfig(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("alignment", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("activation", ctypes.c_int32), ("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
-                ("weight_layout", ctypes.c_int32)]
+                ("weight_layout", ctypes.c_int32), ("rows_per_expert", ctypes.c_int32)]
 
 
 class ProductWeights(ctypes.Structure):
@@ -74,7 +74,7 @@ class ProductWeights(ctypes.Structure):
 class FfnConfig(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("alignment", ctypes.c_int32), ("hidden", ctypes.c_int32),
                 ("inner", ctypes.c_int32), ("dtype", ctypes.c_int32), ("num_adapters", ctypes.c_int32),
-                ("rank", ctypes.c_int32), ("weight_layout", ctypes.c_int32)]
+                ("rank", ctypes.c_int32), ("weight_layout", ctypes.c_int32), ("rows_per_expert", ctypes.c_int32)]
 
 
 DISPATCH_PATHS = {0: "none", 1: "one_kernel", 2: "tiled", 3: "cached", 4: "empty", 5: "one_launch"}

@@ -265,7 +265,8 @@ class Buffer:
         if received.receipt.round != info.round:
             raise nat.AfdError(nat.AFD_E_ORDER, "worker_experts: a receive of an earlier round")
         return _experts.expert_ffn(received.rows, received.ends, experts, alignment=self.alpha,
-                                   x_scales=received.scales, adapters=adapters, row_adapters=row_adapters, out=out)
+                                   x_scales=received.scales, adapters=adapters, row_adapters=row_adapters, out=out,
+                                   rows_per_expert=-(-sum(self._T) * self.K // self.E))   # of evenly spread choices
 
     def source_collect(self, s, *, view=False) -> torch.Tensor:
         res = ctypes.c_void_p(0)

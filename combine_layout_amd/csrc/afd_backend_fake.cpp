@@ -141,9 +141,9 @@ int be_read_stall(uint32_t *, void *, int clear, int *stalled)
 
 int be_launch_product(const ProductPlan &p, void *)
 {
-    logf("product E=%d alpha=%d k=%d n=%d fp8=%d out8=%d gated=%d nad=%d rank=%d packed=%d rows=%lld x=%p out=%p outs=%p t=%p", p.E,
+    logf("product E=%d alpha=%d k=%d n=%d fp8=%d out8=%d gated=%d nad=%d rank=%d packed=%d rows=%lld each=%d live=%lld x=%p out=%p outs=%p t=%p", p.E,
          p.alpha, p.k, p.n, p.fp8, p.out8, p.gated, p.nad, p.rank, p.packed,
-         static_cast<long long>(p.rows), p.x, p.out,
+         static_cast<long long>(p.rows), p.each, static_cast<long long>(p.live), p.x, p.out,
          static_cast<void *>(p.outs), static_cast<void *>(p.t));
     return g_fail;
 }

@@ -273,6 +273,7 @@ afd_status check_product(const afd_product_config *c, int64_t rows)
     if (c->k < 1 || c->k > (1 << 21) || c->k % (fp8 ? 128 : 64) != 0) return AFD_E_SHAPE;
     if (c->n < 1 || c->n % (fp8 && gated ? 128 : 16) != 0) return AFD_E_SHAPE;
     if (c->weight_layout != AFD_WEIGHTS_ROWS && c->weight_layout != AFD_WEIGHTS_PACKED) return AFD_E_SHAPE;
+    if (c->rows_per_expert < 0) return AFD_E_SHAPE;
     // byte offsets inside one expert's weights, and inside 256 rows of x, are
     // 32-bit in the kernels
     if (int64_t(c->n) * (gated ? 2 : 1) * c->k * (fp8 ? 1 : 2) >= (int64_t(1) << 31)) return AFD_E_SHAPE;
@@ -320,6 +321,8 @@ ProductPlan plan_product(const afd_product_config &c, int64_t rows, const void *
     p.nad = c.num_adapters;
     p.rank = c.rank;
     p.rows = rows;
+    p.each = rows_of_expert(c, rows);
+    p.live = c.rows_per_expert > 0 ? std::min(rows, int64_t(p.E) * p.each) : rows;
     p.x = x;
     p.xs = xs;
     p.ends = ends;
@@ -342,9 +345,9 @@ afd_status plan_ffn(const afd_ffn_config *c, int64_t rows, FfnPlan *f)
     if (!c || !f) return AFD_E_ARG;
     const int fp8 = c->dtype == AFD_FP8_E4M3;
     f->up = {c->num_experts, c->alignment,  c->hidden,      c->inner,       c->dtype,
-             c->dtype,       AFD_ACT_SWIGLU, c->num_adapters, c->rank,        c->weight_layout};
+             c->dtype,       AFD_ACT_SWIGLU, c->num_adapters, c->rank,        c->weight_layout, c->rows_per_expert};
     f->down = {c->num_experts, c->alignment,  c->inner,       c->hidden,      c->dtype,
-               AFD_BF16,       AFD_ACT_NONE, c->num_adapters, c->rank,        c->weight_layout};
+               AFD_BF16,       AFD_ACT_NONE, c->num_adapters, c->rank,        c->weight_layout, c->rows_per_expert};
     afd_status st = check_product(&f->up, rows);
     if (st == AFD_OK) st = check_product(&f->down, rows);
     if (st != AFD_OK) return st;

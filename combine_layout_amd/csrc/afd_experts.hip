@@ -1321,11 +1321,7 @@ unsigned persistent_grid(int64_t tiles, int64_t per_tile, int most)
     const int64_t items = (tiles * per_tile + 7) / 8 * 8;
     return unsigned(items < most ? items : most);
 }
-int64_t tile_bound(const ProductPlan &p, int height)
-{
-    const int64_t t = p.E + p.rows / height;
-    return t < p.rows ? t : p.rows;
-}
+int64_t tile_bound(int E, int64_t rows, int height) { return std::min(E + rows / height, rows); }
 
 constexpr int kComputeUnits = 256;
 
@@ -1334,7 +1330,7 @@ int launch_few(const ProductPlan &p, ProductArgs a, hipStream_t st)
 {
     typedef Few<FP8, GATED, OUT8, LOW, NB, KS, CS> F;
     a.ntiles = (p.n + F::BN - 1) / F::BN;
-    const unsigned grid = persistent_grid(tile_bound(p, F::rows), a.ntiles, kComputeUnits * 8);
+    const unsigned grid = persistent_grid(tile_bound(p.E, p.rows, F::rows), a.ntiles, kComputeUnits * 8);
     hipLaunchKernelGGL((k_product_few<FP8, GATED, OUT8, LOW, NB, KS, CS>), dim3(grid), dim3(F::threads), 0, st, a);
     return launched();
 }
@@ -1356,18 +1352,20 @@ int launch_many(const ProductPlan &p, ProductArgs a, hipStream_t st)
             return 1;
         told.fetch_or(uint64_t(1) << dev);
     }
-    const unsigned grid = persistent_grid(tile_bound(p, Low::rows), a.ntiles, kComputeUnits);
+    const unsigned grid = persistent_grid(tile_bound(p.E, p.rows, Low::rows), a.ntiles, kComputeUnits);
     hipLaunchKernelGGL((k_product_many<FP8, GATED, OUT8, LOW>), dim3(grid), dim3(Low::threads), lds, st, a);
     return launched();
 }
 
-// The tiled product runs from this many rows per expert on (by the host's bound, which
-// is up to twice what comes), unless the few-row kernel's items fit side by side.
-// 64 experts, H 2048, inner 768, BF16 network: with one row each 138 us few and 142 us
-// tiled, with 8 113 and 110, with 16 122 and 112, with 32 169 and 116; FP8 with 16 75
-// and 68.  With adapters (32 of rank 16) the few-row kernel, whose wavefronts share a
-// tile's adapters, is level at 16 (197 and 200).
-constexpr int64_t kManyFrom = 8, kManyFromLow = 64;
+// The tiled product runs from this many expected rows per expert on (rows_of_expert),
+// unless the few-row kernel's items fit side by side.
+// 64 experts, H 2048, inner 768, network, us few and tiled: BF16 with 1 row each 79 and
+// 97, 2 96 and 102, 4 108 and 108, 8 113 and 109, 32 162 and 115, 64 221 and 124; FP8 59
+// and 61, 66 and 63, 69 and 66, 71 and 67, 100 and 74, 131 and 80.  With adapters (32 of
+// rank 16) the few-row kernel's wavefronts share a tile's adapters: BF16 with 16 rows 188
+// and 199, 24 235 and 228, 32 304 and 252, 64 413 and 296; FP8 161 and 166, 191 and 193,
+// 239 and 213, 323 and 264.
+constexpr int kManyFrom = 4, kManyFromLow = 24;
 
 // Items of the few-row kernel, per CU, that run side by side.  Up to there the tiled
 // product, whose larger tiles occupy few CUs, waits longer for each tile's chain of
@@ -1383,10 +1381,8 @@ template <bool FP8, bool GATED, bool OUT8, bool LOW, int NB, int KS, int CS>
 int launch_either(const ProductPlan &p, const ProductArgs &a, hipStream_t st)
 {
     typedef Few<FP8, GATED, OUT8, LOW, NB, KS, CS> F;
-    // the rows' bound without what alignment alone can add
-    const int64_t each = (p.rows - int64_t(p.E) * (p.alpha - 1)) / p.E;
-    const int64_t items = tile_bound(p, F::rows) * ((p.n + F::BN - 1) / F::BN);
-    if (each >= (LOW ? kManyFromLow : kManyFrom) && items > kComputeUnits * kSideBySide<FP8, OUT8>)
+    const int64_t items = tile_bound(p.E, p.live, F::rows) * ((p.n + F::BN - 1) / F::BN);
+    if (p.each >= (LOW ? kManyFromLow : kManyFrom) && items > kComputeUnits * kSideBySide<FP8, OUT8>)
         return launch_many<FP8, GATED, OUT8, LOW>(p, a, st);
     return launch_few<FP8, GATED, OUT8, LOW, NB, KS, CS>(p, a, st);
 }

@@ -3,6 +3,7 @@
 // Plain C++17; no HIP types.
 #pragma once
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 
@@ -181,6 +182,16 @@ inline int layout_tiles(const RoundPlan &p, TileRec *out)
     return p.nblk;
 }
 
+// Rows that an expert is expected to have, which the kernel is chosen by: what the caller
+// says, no more than rows has room for; or else half of the rows' bound without what
+// alignment alone can add (the bound counts every choice for this partition).
+inline int rows_of_expert(const afd_product_config &c, int64_t rows)
+{
+    const int64_t E = c.num_experts;
+    if (c.rows_per_expert > 0) return int(std::min<int64_t>(c.rows_per_expert, (rows + E - 1) / E));
+    return int(std::max<int64_t>((rows - E * (c.alignment - 1)) / E / 2, 0));
+}
+
 // One grouped product (and its adapters' first halves); pointers are device
 // addresses recorded from the caller.
 struct ProductPlan {
@@ -188,6 +199,8 @@ struct ProductPlan {
     bool fp8 = false, out8 = false, gated = false, packed = false;
     int nad = 0, rank = 0;           // adapters (0: none) and their rank
     int64_t rows = 0;
+    int each = 0;                    // rows that an expert is expected to have (rows_of_expert)
+    int64_t live = 0;                // and all experts together; rows where nobody says
     const void *x = nullptr;
     const float *xs = nullptr;
     const int32_t *ends = nullptr;

@@ -91,14 +91,16 @@ def raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _alignment(alpha):
+def _int32s(alpha, each):
     if not 0 < alpha < 2 ** 31:
         raise ValueError("alignment must be in [1, 2^31)")
+    if not 0 <= each < 2 ** 31:
+        raise ValueError("rows_per_expert must be in [0, 2^31)")
 
 
 @functools.lru_cache(maxsize=256)
 def _product_plan(rows, *cfg):
-    _alignment(cfg[1])
+    _int32s(cfg[1], cfg[-1])
     c, ws = nat.ProductConfig(*cfg), ctypes.c_size_t(0)
     nat.check(nat.load().afd_product_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_product")
     return c, ws.value
@@ -106,7 +108,7 @@ def _product_plan(rows, *cfg):
 
 @functools.lru_cache(maxsize=256)
 def _ffn_plan(rows, *cfg):
-    _alignment(cfg[1])
+    _int32s(cfg[1], cfg[-1])
     c, ws = nat.FfnConfig(*cfg), ctypes.c_size_t(0)
     nat.check(nat.load().afd_ffn_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_ffn")
     return c, ws.value
@@ -193,7 +195,7 @@ def _x(x):
 
 
 def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales=None, activation=None, adapters=None,
-                   row_adapters=None, out=None, out_scales=None):
+                   row_adapters=None, out=None, out_scales=None, rows_per_expert=0):
     """out[r] = act(x[r] W_j^T) for the rows r of expert j, [rows, n] bf16.
 
     x [rows, k] bf16, or float8_e4m3fn with x_scales float32 [rows, k/128];
@@ -205,6 +207,9 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
     A float8 swiglu product writes float8 rows when `out` is a float8_e4m3fn
     tensor, with their scales in out_scales float32 [rows, n/128].
     Without `out` the result is new memory, its padding rows undefined.
+    rows_per_expert: the rows that an expert is expected to have, by which a kernel
+    is chosen (0: taken from the number of rows as worker_receive sizes them
+    without host counts).
     Runs on x's device and its current stream; forward only (tensors that ask
     for a gradient are refused unless gradients are off, dual tensors always).
     """
@@ -227,7 +232,8 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
     S, rank = _number_and_rank(adapters) if adapters is not None else (0, 0)
     cfg, need = _product_plan(R, E, alignment, k, n, code, nat.AFD_FP8_E4M3 if out8 else nat.AFD_BF16,
                               nat.ACTIVATIONS[activation], S, rank,
-                              nat.WEIGHTS_PACKED if isinstance(weight, PackedWeights) else nat.WEIGHTS_ROWS)
+                              nat.WEIGHTS_PACKED if isinstance(weight, PackedWeights) else nat.WEIGHTS_ROWS,
+                              rows_per_expert)
     if out is None:
         out = torch.empty((R, n), dtype=torch.bfloat16, device=dev)
     po = _want(out, "out", torch.float8_e4m3fn if out8 else torch.bfloat16, (R, n), dev)
@@ -246,7 +252,7 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
 
 
 def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapters: Optional[ExpertAdapters] = None,
-               row_adapters=None, out=None):
+               row_adapters=None, out=None, rows_per_expert=0):
     """The experts' network, swiglu(x Wup^T) Wdown^T per expert, [rows, hidden]
     bf16.  Arguments as expert_product; the hidden layer is rounded to the
     rows' own format (bf16, or float8_e4m3fn with a scale per row and 128
@@ -270,7 +276,7 @@ def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapter
     lu, ld = (adapters.up, adapters.down) if adapters is not None else (None, None)
     wu = _weights("up", experts.up, experts.up_scales, lu, E, 2 * inner, hidden, code, dtype, True, dev)
     wd = _weights("down", experts.down, experts.down_scales, ld, E, hidden, inner, code, dtype, False, dev)
-    cfg, need = _ffn_plan(R, E, alignment, hidden, inner, code, S, rank, nat.WEIGHTS_PACKED)
+    cfg, need = _ffn_plan(R, E, alignment, hidden, inner, code, S, rank, nat.WEIGHTS_PACKED, rows_per_expert)
     if out is None:
         out = torch.empty((R, hidden), dtype=torch.bfloat16, device=dev)
     po = _want(out, "out", torch.bfloat16, (R, hidden), dev)

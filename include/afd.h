@@ -445,6 +445,12 @@ typedef enum { AFD_WEIGHTS_ROWS = 0, AFD_WEIGHTS_PACKED = 1 } afd_weight_layout;
  *   rank          of every adapter, a multiple of 8 up to AFD_MAX_RANK (smaller
  *                 ones are padded with zero rows of A); 0 without adapters
  *   weight_layout afd_weight_layout
+ *   rows_per_expert  live rows that an expert is expected to have, or 0: taken from
+ *                 rows, as half of what alignment alone cannot add.  That fits an
+ *                 arena of afd_worker_receive without host counts and with two
+ *                 partitions; of more, rows is further from what comes, and rows
+ *                 that the host counted hold their padding.  It chooses a kernel,
+ *                 and with it the order of the sums and the time.
  * One expert's W may hold at most 2^31 - 1 bytes; rows is below 2^24.
  *
  * A BF16 output is rounded once.  Sums are float32, with two exceptions.  Of an
@@ -466,6 +472,7 @@ typedef struct {
     int32_t num_adapters;
     int32_t rank;
     int32_t weight_layout; /* afd_weight_layout */
+    int32_t rows_per_expert;
 } afd_product_config;
 
 /*
@@ -536,6 +543,7 @@ typedef struct {
     int32_t num_adapters;
     int32_t rank;
     int32_t weight_layout; /* afd_weight_layout, of both weights */
+    int32_t rows_per_expert; /* as in afd_product_config */
 } afd_ffn_config;
 
 /* afd_ffn_query: workspace bytes of afd_expert_ffn; errors as afd_product_query. */

@@ -15,7 +15,7 @@ def round_trip():
     lib = nat.load_fake()
     ctx = Ctx(lib, nat.Config(2, 2, 8, 2, 256, 4, 16, 0, 0, 0))
     buf = afd.Buffer.__new__(afd.Buffer)
-    buf.lib, buf.ctx, buf.alpha = lib, ctx.ctx, 4
+    buf.lib, buf.ctx, buf.alpha, buf.K, buf.E, buf._T = lib, ctx.ctx, 4, 2, 8, [4, 4]
 
     def receive():
         for s in range(2):

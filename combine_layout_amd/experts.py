@@ -49,8 +49,8 @@ def pack_weights(w) -> PackedWeights:
         raise ValueError("weights must be a contiguous [E, m, k] tensor on a GPU")
     E, m, k = w.shape
     code, _ = _act_dtype(w)
+    c = _config(nat.ProductConfig, E, 1, k, m, code, nat.AFD_BF16, nat.AFD_ACT_NONE, 0, 0, nat.WEIGHTS_ROWS)
     data = torch.empty(w.numel() * w.element_size(), dtype=torch.uint8, device=w.device)
-    c = nat.ProductConfig(E, 1, k, m, code, nat.AFD_BF16, nat.AFD_ACT_NONE, 0, 0, nat.WEIGHTS_ROWS)
     with on_device(w.device):
         st = nat.load().afd_pack_weights(c, w.data_ptr(), data.data_ptr(), raw_stream(w.device))
     nat.check(st, "pack_weights")
@@ -91,25 +91,24 @@ def raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _int32s(alpha, each):
-    if not 0 < alpha < 2 ** 31:
-        raise ValueError("alignment must be in [1, 2^31)")
-    if not 0 <= each < 2 ** 31:
-        raise ValueError("rows_per_expert must be in [0, 2^31)")
+def _config(kind, *values):
+    """The configuration of int32 values; what no int32 holds is refused, not cut."""
+    for (name, _), v in zip(kind._fields_, values):
+        if not (name == "alignment") <= v < 2 ** 31:
+            raise ValueError(f"{name} must be in [{int(name == 'alignment')}, 2^31), got {v}")
+    return kind(*values)
 
 
 @functools.lru_cache(maxsize=256)
 def _product_plan(rows, *cfg):
-    _int32s(cfg[1], cfg[-1])
-    c, ws = nat.ProductConfig(*cfg), ctypes.c_size_t(0)
+    c, ws = _config(nat.ProductConfig, *cfg), ctypes.c_size_t(0)
     nat.check(nat.load().afd_product_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_product")
     return c, ws.value
 
 
 @functools.lru_cache(maxsize=256)
 def _ffn_plan(rows, *cfg):
-    _int32s(cfg[1], cfg[-1])
-    c, ws = nat.FfnConfig(*cfg), ctypes.c_size_t(0)
+    c, ws = _config(nat.FfnConfig, *cfg), ctypes.c_size_t(0)
     nat.check(nat.load().afd_ffn_query(ctypes.byref(c), rows, ctypes.byref(ws)), "expert_ffn")
     return c, ws.value
 

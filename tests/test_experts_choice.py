@@ -65,3 +65,24 @@ def test_worker_experts_expects_evenly_spread_choices(lib, monkeypatch, T, want)
     rec = afd.Received(torch.zeros(1, 1), None, None, None, nat.Receipt(7, 0, 0), 1, None)
     buf.worker_experts(0, rec, None)
     assert seen["rows_per_expert"] == want and seen["alignment"] == 64
+
+
+@pytest.mark.parametrize("at,what", [(0, "num_experts"), (1, "alignment"), (2, "k"), (3, "n"), (7, "num_adapters"), (8, "rank"),
+                                     (10, "rows_per_expert")])
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 64, -1])
+def test_what_no_int32_holds_is_refused(monkeypatch, lib, at, what, value):
+    """A width of 2^32 + 64 is not one of 64."""
+    from combine_layout_amd import experts
+    monkeypatch.setattr(nat, "load", nat.load_fake)
+    good = [4, 16, 64, 64, nat.AFD_BF16, nat.AFD_BF16, 0, 2, 8, 0, 0]
+    assert experts._product_plan(10, *good)[0].k == 64
+    good[at] = value
+    with pytest.raises(ValueError, match=what):
+        experts._product_plan(10, *good)
+    network = [4, 16, 64, 64, nat.AFD_BF16, 2, 8, 0, 0]
+    assert experts._ffn_plan(10, *network)[0].inner == 64
+    fields = [name for name, _ in nat.FfnConfig._fields_]
+    name = {"k": "hidden", "n": "inner"}.get(what, what)
+    network[fields.index(name)] = value
+    with pytest.raises(ValueError, match=name):
+        experts._ffn_plan(10, *network)

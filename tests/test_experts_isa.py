@@ -116,6 +116,37 @@ def faults(blocks):
     return sorted(found), loads
 
 
+def left_at_barriers(blocks):
+    """The most LDS operations (scalar loads counted with them, as the hardware
+    does) that a wavefront can still have under way at each barrier: line -> number."""
+    index = {label: i for i, (label, _) in enumerate(blocks)}
+    entry, todo, left = [None] * len(blocks), [0], {}
+    entry[0] = 0
+    while todo:
+        i = todo.pop()
+        n, targets, falls = entry[i], [], True
+        for op, operands, line in blocks[i][1]:
+            if op.startswith(("ds_", "s_load", "s_buffer_load")):
+                n = min(n + 1, 15)
+            elif op == "s_waitcnt":
+                m = re.search(r"lgkmcnt\((\d+)\)", " ".join(operands))
+                n = min(n, int(m[1])) if m else n
+            elif op == "s_barrier":
+                left[line] = max(left.get(line, 0), n)
+            if BRANCH.match(op):
+                targets.append(index[operands[0]])
+                falls = op != "s_branch"
+            elif op == "s_endpgm":
+                falls = False
+        if falls and i + 1 < len(blocks):
+            targets.append(i + 1)
+        for t in targets:
+            if entry[t] is None or n > entry[t]:
+                entry[t] = n
+                todo.append(t)
+    return left
+
+
 GOOD = """
 k_a:
 \ts_cbranch_scc1 .LBB0_2
@@ -146,6 +177,24 @@ def test_the_reader_finds_planted_faults():
     assert {(f[2], f[3]) for f in count(over)} == {("s6", 4), ("s7", 4)}
 
 
+WAITED = """
+k_b:
+.LBB1_1:
+\ts_barrier
+\tds_read_b128 v[0:3], v4
+\tds_read_b128 v[4:7], v8
+\ts_waitcnt vmcnt(3) lgkmcnt(0)
+\ts_cbranch_scc1 .LBB1_1
+\ts_endpgm
+"""
+
+
+def test_the_reader_counts_what_is_left_at_a_barrier():
+    assert left_at_barriers(parse(WAITED)["k_b"]) == {4: 0}
+    assert left_at_barriers(parse(WAITED.replace("lgkmcnt(0)", "lgkmcnt(1)"))["k_b"]) == {4: 1}
+    assert left_at_barriers(parse(WAITED.replace(" lgkmcnt(0)", ""))["k_b"]) == {4: 15}
+
+
 @pytest.fixture(scope="module")
 def kernels(tmp_path_factory):
     hipcc = shutil.which(build.HIPCC)
@@ -168,3 +217,14 @@ def test_loads_into_lds_wait_for_their_registers(kernels):
             assert loads, f"{name}: no loads found"
     assert seen > 100
     assert not bad, f"{len(bad)} of {seen} loads:\n" + "\n".join(bad[:20])
+
+
+def test_lds_reads_are_over_at_barriers(kernels):
+    """A stage is loaded anew behind the barrier after its last read; the barrier is
+    written in assembly, where the compiler adds no wait of its own."""
+    seen = 0
+    for name, blocks in kernels.items():
+        left = left_at_barriers(blocks)
+        seen += len(left)
+        assert not any(left.values()), f"{name}: {left}"
+    assert seen > 50

@@ -608,7 +608,8 @@ __device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b)
 // memory instruction may read a scalar register five wait states after a vector
 // instruction (the v_readfirstlane of uniform(), a register spilled to lanes) wrote it,
 // and use M0 one after.  All of a block's registers are written before it, so the wait
-// stands once per block, ahead of its first load: s_mov and s_nop 3.
+// stands once per block, ahead of its first load: s_mov and s_nop 3.  (All of a step.s
+// loads in one block: no difference.)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // that M0, which the compiler sets where it needs it, is named as written
 __device__ __forceinline__ void to_lds4(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds)
@@ -947,7 +948,9 @@ typedef Shape<2, 4, 8, 2> Tall;
 
 // Rows per expert (of those that have any) from which BF16 products take the tall tiles.
 // (64 experts, H 2048, inner 768: at 256 rows 259 us instead of 228, at 320 258 and
-// 262, at 384 275 and 326, at 512 378 and 406.)
+// 262, at 384 275 and 326, at 512 378 and 406.  Measured at this width and number of
+// experts only; at 256 rows the 384 tall items are 1.5 rounds of the CUs, the 768 low ones
+// three.)
 constexpr int kTallFrom = 320;
 
 template <bool FP8, bool GATED, bool OUT8, bool LOW>
@@ -1010,7 +1013,8 @@ __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t q0, uint32_t q1)
 // t[r, :] = scaling[i] A[i, j] x[r] for every row r of expert j with an adapter i.
 // Meant to be bound by reading the A of every (adapter, expert) pair once.  An
 // expert's workgroups find its distinct adapters from a bit map of the rows' tags;
-// the pairs of an adapter and 32 rows of its A go round them.  For each, the
+// the pairs of an adapter and 32 rows of its A go round them.  For each, the expert's
+// tags are read again (rows times distinct adapters in all) and the
 // adapter's rows are gathered, 32 (FP8 64) at a time, and multiplied as in
 // k_product_few: the A operand holds rows of A, the wavefronts split k.
 // Measured: 32 adapters of rank 16, 1024 rows over 64 experts (813 pairs, 106 MB of

@@ -487,7 +487,8 @@ typedef struct {
  * adds scaling[i] * B_ij (A_ij x[r]) to its sums before the activation (with
  * SwiGLU the gate rows of B take the gate's A, the up rows the up's); a row
  * with any other value has no adapter.  An adapter reaches no row but its own;
- * where its B holds an infinity, its rows' values may be NaN.
+ * where its B holds an infinity, its rows' values may be NaN.  The time grows with
+ * the rows of an expert times its distinct adapters.
  */
 typedef struct {
     const void *w;

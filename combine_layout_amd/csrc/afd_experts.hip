@@ -608,7 +608,7 @@ __device__ __forceinline__ int pair_up(uint32_t &a, uint32_t &b)
 // memory instruction may read a scalar register five wait states after a vector
 // instruction (the v_readfirstlane of uniform(), a register spilled to lanes) wrote it,
 // and use M0 one after.  All of a block's registers are written before it, so the wait
-// stands once per block, ahead of its first load: s_mov and s_nop 3.  (All of a step.s
+// stands once per block, ahead of its first load: s_mov and s_nop 3.  (All of a step's
 // loads in one block: no difference.)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // that M0, which the compiler sets where it needs it, is named as written

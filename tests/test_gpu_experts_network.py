@@ -90,3 +90,51 @@ def test_fp8_sums_of_cancelling_products(arena, rows, n, k):
     case = dict(tags=None, ends=[rows], alpha=1, rows=rows)
     want, tol, _ = bounds.product(case, xq, xs, None, wq[None], ws)
     assert ((got - want).abs() <= ref.rounded(want, tol)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,F,alpha", [((5, 3), 2, 1), ((0, 40), 1, 16), ((300, 400, 1), 4, 64)])
+def test_round_is_its_replies(dtype, T, F, alpha):
+    """A round's replies are expert_ffn of its received rows, bit for bit, and its
+    results are the replies' weighted sums within float32 and one BF16 rounding
+    (the tags name every row's source and token)."""
+    afd = _afd()
+    _print("round", dtype, T, F, alpha)
+    E, K, H, inner, S, rank = 8, 3, 256, 128, 4, 8
+    g = torch.Generator().manual_seed(24)
+    N, bucket, El = len(T), max(T), E // F
+    u = ref.make(25, E, [1] * E, 1, H, 2 * inner, dtype, S=S, rank=rank, gated=True)
+    d = ref.make(26, E, [1] * E, 1, inner, H, dtype, S=S, rank=rank)
+    buf = afd.Buffer(N, F, E, K, H, alpha, bucket, dtype)
+    first = [sum(T[:s]) for s in range(N)]
+    for s in range(N):
+        x = torch.randn(T[s], H, generator=g)
+        q, qs = (ref.quant(x, 1) if dtype == "fp8" else (x.bfloat16(), None)) if T[s] else (None, None)
+        ids = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T[s])]).int() if T[s] else torch.zeros(0, K).int()
+        ids[torch.rand(ids.shape, generator=g) < 0.1] = -1
+        buf.source_dispatch(s, _dev(q), ids.cuda(), torch.rand(T[s], K, generator=g).cuda(), _dev(qs), bucket=bucket)
+    token = [torch.arange(first[s], first[s] + T[s], dtype=torch.int32, device="cuda") for s in range(N)]
+    adapter = [torch.randint(-1, S, (t,), generator=g).int().cuda() for t in T]
+    want, mag = (torch.zeros(sum(T), H, dtype=torch.float64, device="cuda") for _ in range(2))
+    recs = [buf.worker_receive(f, bucket=bucket) for f in range(F)]
+    for f, rec in enumerate(recs):
+        sl = slice(f * El, (f + 1) * El)
+        cut = lambda t: None if t is None else _dev(t[sl].contiguous())   # noqa: E731
+        ex = afd.Experts(cut(u["w"]), cut(d["w"]), cut(u["ws"]), cut(d["ws"]))
+        ad = afd.ExpertAdapters(*(afd.LowRank(c["low"][0][:, sl].contiguous().cuda(), c["low"][1][:, sl].contiguous().cuda(),
+                                              c["low"][2].cuda()) for c in (u, d)))
+        tags, rows = buf.worker_tags(f, adapter, rec), buf.worker_tags(f, token, rec).long()
+        reply = buf.worker_experts(f, rec, ex, adapters=ad, row_adapters=tags)
+        again = afd.expert_ffn(rec.rows, rec.ends, ex, alignment=alpha, x_scales=rec.scales, adapters=ad, row_adapters=tags,
+                               rows_per_expert=-(-sum(T) * K // E))
+        live = rows >= 0
+        assert torch.equal(reply[live], again[live])
+        part = rec.weights[live].double()[:, None] * reply[live].double()
+        want.index_add_(0, rows[live], part)
+        mag.index_add_(0, rows[live], part.abs())
+        buf.worker_reply(f, reply, rec.receipt)
+    for s in range(N):
+        got = buf.source_collect(s).double()
+        at = slice(first[s], first[s] + T[s])
+        # K products and K sums in float32, then BF16
+        assert ((got - want[at]).abs() <= ref.rounded(want[at], 2 * K * ref.F32 * mag[at])).all(), f"source {s}"

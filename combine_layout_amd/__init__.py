@@ -7,4 +7,6 @@ not been built (``python -m combine_layout_amd.build``).
 """
 from .buffer import Buffer, Received, topk_idx_dtype  # noqa: F401
 from .experts import ExpertAdapters, Experts, LowRank, PackedWeights, expert_ffn, expert_product, pack_weights  # noqa: F401
+from .source import (Balance, Normed, Routes, balance_loss, balance_loss_grad, rms_norm, rms_norm_grad,  # noqa: F401
+                     route_tokens, route_tokens_grad)
 from ._native import AfdError  # noqa: F401

@@ -19,7 +19,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "afd.h")
 
 AFD_OK, AFD_E_ARG, AFD_E_SHAPE, AFD_E_ORDER, AFD_E_CAPACITY, AFD_E_ROUTE, AFD_E_HIP, AFD_E_TIMEOUT = \
     0, -1, -2, -3, -4, -5, -6, -7
-AFD_BF16, AFD_FP8_E4M3 = 0, 1
+AFD_BF16, AFD_FP8_E4M3, AFD_FP32 = 0, 1, 2
 AFD_COMBINE_ONCE, AFD_COMBINE_PER_STAGE, AFD_COMBINE_PER_STAGE_FP8 = 0, 1, 2
 COMBINE_MODES = {"once": AFD_COMBINE_ONCE, "per_stage": AFD_COMBINE_PER_STAGE,
                  "per_stage_fp8": AFD_COMBINE_PER_STAGE_FP8}
@@ -32,6 +32,8 @@ AFD_ACT_NONE, AFD_ACT_SWIGLU = 0, 1
 ACTIVATIONS = {None: AFD_ACT_NONE, "swiglu": AFD_ACT_SWIGLU}
 WEIGHTS_ROWS, WEIGHTS_PACKED = 0, 1
 MAX_ADAPTERS, MAX_RANK = 65536, 128
+MAX_NORM_HIDDEN, NO_RESIDUAL = 65536, -1
+SCORINGS = {"softmax": 0, "sigmoid": 1}
 
 STATUS_NAMES = {0: "AFD_OK", -1: "AFD_E_ARG", -2: "AFD_E_SHAPE", -3: "AFD_E_ORDER",
                 -4: "AFD_E_CAPACITY", -5: "AFD_E_ROUTE", -6: "AFD_E_HIP", -7: "AFD_E_TIMEOUT"}
@@ -77,6 +79,16 @@ class FfnConfig(ctypes.Structure):
                 ("rank", ctypes.c_int32), ("weight_layout", ctypes.c_int32), ("rows_per_expert", ctypes.c_int32)]
 
 
+class NormConfig(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class RouteConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scoring", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 DISPATCH_PATHS = {0: "none", 1: "one_kernel", 2: "tiled", 3: "cached", 4: "empty", 5: "one_launch"}
 
 
@@ -114,6 +126,15 @@ SIGNATURES = {
     "afd_expert_ffn": ([ctypes.POINTER(FfnConfig), _I64, _P, _P, _P, _P, ctypes.POINTER(ProductWeights),
                         ctypes.POINTER(ProductWeights), _P, _P, ctypes.c_size_t, _P], _I32),
     "afd_worker_tags": ([_P, _I32, ctypes.POINTER(_P), _P, _I64, ctypes.POINTER(Receipt), _P], _I32),
+    "afd_norm": ([ctypes.POINTER(NormConfig), _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P], _I32),
+    "afd_norm_grad_query": ([ctypes.POINTER(NormConfig), _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "afd_norm_grad": ([ctypes.POINTER(NormConfig), _I64, _P, _P, _P, _I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P], _I32),
+    "afd_route": ([ctypes.POINTER(RouteConfig), _I64, _P, _I64, _P, _P, _P, _P, _P], _I32),
+    "afd_route_grad": ([ctypes.POINTER(RouteConfig), _I64, _P, _P, _I64, _P, _P, _P], _I32),
+    "afd_balance_query": ([ctypes.POINTER(RouteConfig), _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "afd_balance": ([ctypes.POINTER(RouteConfig), _I64, _P, _I64, _P, ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P],
+                    _I32),
+    "afd_balance_grad": ([ctypes.POINTER(RouteConfig), _I64, _P, _P, _I64, _P, _P, _P, _P], _I32),
     "afd_status_string": ([_I32], ctypes.c_char_p),
 }
 

@@ -16,6 +16,7 @@ import torch
 
 from . import _native as nat
 from . import experts as _experts
+from . import source as _source
 
 topk_idx_dtype = torch.int32
 
@@ -222,6 +223,31 @@ class Buffer:
                                        _stream(self.device))
         nat.check(st, "worker_reply")
         self._round_refs[("reply", f)] = rows
+
+    # -- the source's side, between its collect and its dispatch -----------------
+    def _source_rows(self, s, t, columns, what):
+        if not 0 <= s < self.N:
+            raise ValueError(f"source {s} of {self.N}")
+        if t.dim() != 2 or t.shape[1] != columns or t.shape[0] > self.capacity:
+            raise ValueError(f"{what} must be [T, {columns}] with at most {self.capacity} tokens, got {list(t.shape)}")
+        if t.device != self.arenas[0][2].device:
+            raise ValueError(f"{what} must be on the buffer's device")
+
+    def source_norm(self, s, x, weight, residual=None, *, eps=1e-6, residual_out=None) -> _source.Normed:
+        """The rows that source_dispatch takes, from what source_collect gave: rms_norm in the
+        buffer's format.  In FP8 its rows and scales are source_dispatch's x and x_scale.
+        residual: the stream that x joins; residual_out as in rms_norm."""
+        self._source_rows(s, x, self.H, "x")
+        return _source.rms_norm(x, weight, residual, eps=eps, residual_out=residual_out,
+                                dtype=torch.float8_e4m3fn if self.fp8 else torch.bfloat16)
+
+    def source_route(self, s, logits, *, scoring="softmax", bias=None, renormalize=True, scale=1.0,
+                     live=None) -> _source.Routes:
+        """The ids and weights that source_dispatch takes, from the router's logits [T, E]:
+        route_tokens with the buffer's topk."""
+        self._source_rows(s, logits, self.E, "logits")
+        return _source.route_tokens(logits, self.K, scoring=scoring, bias=bias, renormalize=renormalize, scale=scale,
+                                    live=live)
 
     # -- the experts' side of a partition, between its receive and its reply -----
     def worker_tags(self, f, tags, received, *, out=None) -> torch.Tensor:

@@ -160,6 +160,53 @@ int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *, int32_t *o
     return g_fail;
 }
 
+int be_launch_norm(const NormPlan &p, void *)
+{
+    logf("norm H=%d x32=%d res=%d r32=%d w32=%d out8=%d rows=%lld xs=%lld rs=%lld hs=%lld x=%p r=%p out=%p outs=%p h=%p rstd=%p",
+         p.H, p.x32, p.res, p.r32, p.w32, p.out8, static_cast<long long>(p.rows), static_cast<long long>(p.xs),
+         static_cast<long long>(p.rs), static_cast<long long>(p.hs), p.x, p.r, p.out, static_cast<void *>(p.outs), p.h,
+         static_cast<void *>(p.rstd));
+    return g_fail;
+}
+
+int be_launch_norm_grad(const NormGradPlan &p, void *)
+{
+    logf("norm_grad H=%d h32=%d w32=%d rows=%lld hs=%lld g=%p gr=%p h=%p dh=%p dw=%p groups=%d part=%p", p.H, p.h32, p.w32,
+         static_cast<long long>(p.rows), static_cast<long long>(p.hs), p.g, p.gr, p.h, p.dh, static_cast<void *>(p.dw),
+         p.groups, static_cast<void *>(p.part));
+    return g_fail;
+}
+
+int be_launch_route(const RoutePlan &p, void *)
+{
+    logf("route E=%d K=%d l32=%d sigmoid=%d renorm=%d scale=%g rows=%lld ls=%lld bias=%d live=%d", p.E, p.K, p.l32, p.sigmoid,
+         p.renorm, double(p.scale), static_cast<long long>(p.rows), static_cast<long long>(p.ls), p.bias != nullptr,
+         p.live != nullptr);
+    return g_fail;
+}
+
+int be_launch_route_grad(const RoutePlan &p, void *)
+{
+    logf("route_grad E=%d K=%d l32=%d sigmoid=%d renorm=%d scale=%g rows=%lld ls=%lld", p.E, p.K, p.l32, p.sigmoid, p.renorm,
+         double(p.scale), static_cast<long long>(p.rows), static_cast<long long>(p.ls));
+    return g_fail;
+}
+
+int be_launch_balance(const BalancePlan &p, void *)
+{
+    logf("balance E=%d K=%d l32=%d sigmoid=%d rows=%lld ls=%lld coefficient=%g groups=%d share=%p count=%p tokens=%p", p.r.E, p.r.K,
+         p.r.l32, p.r.sigmoid, static_cast<long long>(p.r.rows), static_cast<long long>(p.r.ls), double(p.coefficient),
+         p.groups, static_cast<void *>(p.share), static_cast<void *>(p.count), static_cast<void *>(p.tokens));
+    return g_fail;
+}
+
+int be_launch_balance_grad(const RoutePlan &p, void *)
+{
+    logf("balance_grad E=%d K=%d l32=%d sigmoid=%d rows=%lld ls=%lld", p.E, p.K, p.l32, p.sigmoid,
+         static_cast<long long>(p.rows), static_cast<long long>(p.ls));
+    return g_fail;
+}
+
 int be_device_sync()
 {
     logf("sync");

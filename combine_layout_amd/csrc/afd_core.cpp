@@ -8,6 +8,7 @@
 // receives once and replies once with its receipt, then every source
 // collects once.
 
+#include <cfloat>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -355,6 +356,94 @@ afd_status plan_ffn(const afd_ffn_config *c, int64_t rows, FfnPlan *f)
     f->t = f->hs + (fp8 ? align256(size_t(rows) * size_t(c->inner / 128) * 4) : 0);
     f->total = f->t + product_workspace(f->up, rows);
     return AFD_OK;
+}
+
+// ---- the source's side ----
+
+constexpr int64_t kMaxStride = int64_t(1) << 31;
+
+struct Span {
+    const void *at;
+    size_t bytes;
+};
+
+// The bytes from the first to the last element of `rows` rows, gaps included.
+Span span(const void *at, int64_t rows, int64_t stride, int64_t columns, size_t element)
+{
+    return {at, rows > 0 ? size_t((rows - 1) * stride + columns) * element : 0};
+}
+
+// Whether two arrays share a byte; an absent or empty one shares none.
+bool overlap(const Span &a, const Span &b)
+{
+    return a.at && b.at && a.bytes > 0 && b.bytes > 0 && overlap(a.at, a.bytes, b.at, b.bytes);
+}
+
+bool stride_ok(int64_t stride, int64_t columns) { return stride >= columns && stride < kMaxStride; }
+
+size_t element_of(int32_t dtype) { return dtype == AFD_FP32 ? 4 : dtype == AFD_BF16 ? 2 : 1; }
+
+afd_status check_norm(const afd_norm_config *c, int64_t rows)
+{
+    if (!c || rows < 0 || rows >= (int64_t(1) << 24)) return AFD_E_ARG;
+    if (c->x_dtype != AFD_BF16 && c->x_dtype != AFD_FP32) return AFD_E_SHAPE;
+    if (c->residual_dtype != AFD_BF16 && c->residual_dtype != AFD_FP32 && c->residual_dtype != AFD_NO_RESIDUAL)
+        return AFD_E_SHAPE;
+    if (c->weight_dtype != AFD_BF16 && c->weight_dtype != AFD_FP32) return AFD_E_SHAPE;
+    if (c->out_dtype != AFD_BF16 && c->out_dtype != AFD_FP8_E4M3) return AFD_E_SHAPE;
+    if (c->hidden < 1 || c->hidden > AFD_MAX_NORM_HIDDEN || c->hidden % (c->out_dtype == AFD_FP8_E4M3 ? 128 : 8) != 0)
+        return AFD_E_SHAPE;
+    if (!(c->eps >= FLT_MIN && c->eps <= FLT_MAX)) return AFD_E_SHAPE;
+    return AFD_OK;
+}
+
+size_t norm_grad_workspace(const afd_norm_config &c, int64_t rows)
+{
+    return align256(size_t(norm_grad_groups(rows)) * size_t(c.hidden) * 4);
+}
+
+afd_status check_route(const afd_route_config *c, int64_t rows)
+{
+    if (!c || rows < 0 || rows >= (int64_t(1) << 24)) return AFD_E_ARG;
+    if (c->num_experts < 1 || c->num_experts > kMaxExperts) return AFD_E_SHAPE;
+    if (c->topk < 1 || c->topk > kMaxTopk || c->topk > c->num_experts) return AFD_E_SHAPE;
+    if (c->dtype != AFD_BF16 && c->dtype != AFD_FP32) return AFD_E_SHAPE;
+    if (c->scoring != AFD_SCORE_SOFTMAX && c->scoring != AFD_SCORE_SIGMOID) return AFD_E_SHAPE;
+    if (c->renormalize != 0 && c->renormalize != 1) return AFD_E_SHAPE;
+    if (!(c->scale >= -FLT_MAX && c->scale <= FLT_MAX)) return AFD_E_SHAPE;
+    return AFD_OK;
+}
+
+// The logits' pointer and stride.
+bool logits_ok(const afd_route_config &c, const void *logits, int64_t stride)
+{
+    return logits && aligned(logits, element_of(c.dtype)) && stride_ok(stride, c.num_experts);
+}
+
+RoutePlan plan_route(const afd_route_config &c, int64_t rows, const void *logits, int64_t stride)
+{
+    RoutePlan p;
+    p.E = c.num_experts;
+    p.K = c.topk;
+    p.l32 = c.dtype == AFD_FP32;
+    p.sigmoid = c.scoring == AFD_SCORE_SIGMOID;
+    p.renorm = c.renormalize != 0;
+    p.scale = c.scale;
+    p.rows = rows;
+    p.l = logits;
+    p.ls = stride;
+    return p;
+}
+
+// Workspace of the balance loss.
+struct BalanceSpace {
+    size_t share, count, tokens, total;
+};
+
+BalanceSpace balance_space(const afd_route_config &c, int64_t rows)
+{
+    const size_t g = size_t(balance_groups(rows)), each = align256(g * size_t(c.num_experts) * 4);
+    return {0, each, 2 * each, 2 * each + align256(g * 4)};
 }
 
 }  // namespace
@@ -773,6 +862,244 @@ afd_status afd_worker_tags(afd_ctx *c, int32_t f, const int32_t *const *tags, in
         if (c->T[s] > 0 && (!tags[s] || !aligned(tags[s], 4))) return AFD_E_ARG;
     if (c->plan.ntok == 0) return AFD_OK;
     return be_launch_tags(c->plan, f, tags, out, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_norm(const afd_norm_config *cfg, int64_t rows, const void *x, int64_t x_stride, const void *residual,
+                    int64_t residual_stride, const void *weight, void *out, float *out_scales, void *residual_out,
+                    int64_t residual_out_stride, float *rstd, void *stream)
+{
+    const afd_status st = check_norm(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (rows == 0) return AFD_OK;
+    const int64_t H = cfg->hidden;
+    const bool res = cfg->residual_dtype != AFD_NO_RESIDUAL, out8 = cfg->out_dtype == AFD_FP8_E4M3;
+    const size_t xe = element_of(cfg->x_dtype), re = res ? element_of(cfg->residual_dtype) : 0;
+    if (!x || !aligned(x, 16) || !stride_ok(x_stride, H) || x_stride % 8 != 0) return AFD_E_ARG;
+    if (!weight || !aligned(weight, 16) || !out || !aligned(out, 16)) return AFD_E_ARG;
+    if (res) {
+        if (!residual || !aligned(residual, 16) || !stride_ok(residual_stride, H) || residual_stride % 8 != 0)
+            return AFD_E_ARG;
+        if (!residual_out || !aligned(residual_out, 16) || !stride_ok(residual_out_stride, H) || residual_out_stride % 8 != 0)
+            return AFD_E_ARG;
+    } else if (residual || residual_out) {
+        return AFD_E_ARG;
+    }
+    if (out8 ? !out_scales || !aligned(out_scales, 4) : out_scales != nullptr) return AFD_E_ARG;
+    if (rstd && !aligned(rstd, 4)) return AFD_E_ARG;
+    // A row is read whole by the workgroup that writes it, and an element by the lane that
+    // writes it: an output in place of an input of the same layout is safe, any other overlap not.
+    const Span in[3] = {span(x, rows, x_stride, H, xe), span(residual, rows, residual_stride, H, re),
+                        {weight, size_t(H) * element_of(cfg->weight_dtype)}};
+    const Span to[4] = {span(out, rows, H, H, out8 ? 1 : 2), span(residual_out, rows, residual_out_stride, H, re),
+                        {out_scales, size_t(rows) * size_t(H / 128) * 4}, {rstd, size_t(rows) * 4}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(to[i], to[j])) return AFD_E_ARG;
+        for (int j = 0; j < 3; ++j) {
+            if (!overlap(to[i], in[j])) continue;
+            const bool in_place =
+                (i == 0 && j == 0 && out == x && x_stride == H && cfg->x_dtype == AFD_BF16 && !out8) ||
+                (i == 1 && j == 0 && residual_out == x && x_stride == residual_out_stride && xe == re) ||
+                (i == 1 && j == 1 && residual_out == residual && residual_stride == residual_out_stride);
+            if (!in_place) return AFD_E_ARG;
+        }
+    }
+    NormPlan p;
+    p.H = int(H);
+    p.x32 = cfg->x_dtype == AFD_FP32;
+    p.r32 = cfg->residual_dtype == AFD_FP32;
+    p.res = res;
+    p.w32 = cfg->weight_dtype == AFD_FP32;
+    p.out8 = out8;
+    p.eps = cfg->eps;
+    p.rows = rows;
+    p.x = x;
+    p.r = residual;
+    p.w = weight;
+    p.xs = x_stride;
+    p.rs = residual_stride;
+    p.hs = residual_out_stride;
+    p.out = out;
+    p.h = residual_out;
+    p.outs = out_scales;
+    p.rstd = rstd;
+    return be_launch_norm(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_norm_grad_query(const afd_norm_config *cfg, int64_t rows, size_t *workspace_bytes)
+{
+    if (!workspace_bytes) return AFD_E_ARG;
+    const afd_status st = check_norm(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (cfg->out_dtype != AFD_BF16) return AFD_E_SHAPE;
+    *workspace_bytes = norm_grad_workspace(*cfg, rows);
+    return AFD_OK;
+}
+
+afd_status afd_norm_grad(const afd_norm_config *cfg, int64_t rows, const void *grad, const void *grad_residual,
+                         const void *h, int64_t h_stride, const void *weight, const float *rstd, void *dh,
+                         float *dweight, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const afd_status st = check_norm(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (cfg->out_dtype != AFD_BF16) return AFD_E_SHAPE;
+    const int64_t H = cfg->hidden;
+    const int32_t type = cfg->residual_dtype != AFD_NO_RESIDUAL ? cfg->residual_dtype : cfg->x_dtype;
+    if (dweight && !aligned(dweight, 4)) return AFD_E_ARG;
+    if (rows > 0) {
+        if (!grad || !aligned(grad, 16) || (grad_residual && !aligned(grad_residual, 16))) return AFD_E_ARG;
+        if (!h || !aligned(h, 16) || !stride_ok(h_stride, H) || h_stride % 8 != 0) return AFD_E_ARG;
+        if (!weight || !aligned(weight, 16) || !rstd || !aligned(rstd, 4) || !dh || !aligned(dh, 16)) return AFD_E_ARG;
+        const size_t need = dweight ? norm_grad_workspace(*cfg, rows) : 0;
+        if (need > 0 && (!workspace || !aligned(workspace, 256))) return AFD_E_ARG;
+        if (workspace_bytes < need) return AFD_E_CAPACITY;
+        const Span in[5] = {span(grad, rows, H, H, 2), span(grad_residual, rows, H, H, element_of(type)),
+                            span(h, rows, h_stride, H, element_of(type)), {weight, size_t(H) * element_of(cfg->weight_dtype)},
+                            {rstd, size_t(rows) * 4}};
+        const Span to[3] = {span(dh, rows, H, H, element_of(type)), {dweight, size_t(H) * 4}, {workspace, need}};
+        for (int i = 0; i < 3; ++i) {
+            for (int j = 0; j < i; ++j)
+                if (overlap(to[i], to[j])) return AFD_E_ARG;
+            for (int j = 0; j < 5; ++j)
+                if (overlap(to[i], in[j]) && !(i == 0 && ((j == 0 && dh == grad && type == AFD_BF16) || (j == 1 && dh == grad_residual))))
+                    return AFD_E_ARG;
+        }
+    } else if (!dweight) {
+        return AFD_OK;
+    }
+    NormGradPlan p;
+    p.H = int(H);
+    p.h32 = type == AFD_FP32;
+    p.w32 = cfg->weight_dtype == AFD_FP32;
+    p.rows = rows;
+    p.hs = h_stride;
+    p.g = grad;
+    p.gr = grad_residual;
+    p.h = h;
+    p.w = weight;
+    p.rstd = rstd;
+    p.dh = dh;
+    p.dw = dweight;
+    p.part = static_cast<float *>(workspace);
+    p.groups = norm_grad_groups(rows);
+    return be_launch_norm_grad(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_route(const afd_route_config *cfg, int64_t rows, const void *logits, int64_t logit_stride,
+                     const float *bias, const uint8_t *live, int32_t *ids, float *weights, void *stream)
+{
+    const afd_status st = check_route(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (rows == 0) return AFD_OK;
+    if (!logits_ok(*cfg, logits, logit_stride)) return AFD_E_ARG;
+    if (!ids || !aligned(ids, 4) || !weights || !aligned(weights, 4) || (bias && !aligned(bias, 4))) return AFD_E_ARG;
+    const Span in[3] = {span(logits, rows, logit_stride, cfg->num_experts, element_of(cfg->dtype)),
+                        {bias, size_t(cfg->num_experts) * 4}, {live, size_t(rows)}};
+    const Span to[2] = {span(ids, rows, cfg->topk, cfg->topk, 4), span(weights, rows, cfg->topk, cfg->topk, 4)};
+    if (overlap(to[0], to[1])) return AFD_E_ARG;
+    for (const Span &o : to)
+        for (const Span &i : in)
+            if (overlap(o, i)) return AFD_E_ARG;
+    RoutePlan p = plan_route(*cfg, rows, logits, logit_stride);
+    p.bias = bias;
+    p.live = live;
+    p.ids = ids;
+    p.w = weights;
+    return be_launch_route(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_route_grad(const afd_route_config *cfg, int64_t rows, const float *grad, const void *logits,
+                          int64_t logit_stride, const int32_t *ids, void *dlogits, void *stream)
+{
+    const afd_status st = check_route(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (rows == 0) return AFD_OK;
+    const size_t e = element_of(cfg->dtype);
+    if (!logits_ok(*cfg, logits, logit_stride)) return AFD_E_ARG;
+    if (!grad || !aligned(grad, 4) || !ids || !aligned(ids, 4) || !dlogits || !aligned(dlogits, e)) return AFD_E_ARG;
+    const Span to = span(dlogits, rows, cfg->num_experts, cfg->num_experts, e);
+    if (overlap(to, span(logits, rows, logit_stride, cfg->num_experts, e)) || overlap(to, span(grad, rows, cfg->topk, cfg->topk, 4)) ||
+        overlap(to, span(ids, rows, cfg->topk, cfg->topk, 4)))
+        return AFD_E_ARG;
+    RoutePlan p = plan_route(*cfg, rows, logits, logit_stride);
+    p.g = grad;
+    p.ids = const_cast<int32_t *>(ids);
+    p.dl = dlogits;
+    return be_launch_route_grad(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_balance_query(const afd_route_config *cfg, int64_t rows, size_t *workspace_bytes)
+{
+    if (!workspace_bytes) return AFD_E_ARG;
+    const afd_status st = check_route(cfg, rows);
+    if (st != AFD_OK) return st;
+    *workspace_bytes = balance_space(*cfg, rows).total;
+    return AFD_OK;
+}
+
+afd_status afd_balance(const afd_route_config *cfg, int64_t rows, const void *logits, int64_t logit_stride,
+                       const int32_t *ids, float coefficient, float *loss, int32_t *counts, float *slope,
+                       void *workspace, size_t workspace_bytes, void *stream)
+{
+    const afd_status st = check_route(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (!(coefficient >= -FLT_MAX && coefficient <= FLT_MAX)) return AFD_E_ARG;
+    if (!loss || !aligned(loss, 4) || !counts || !aligned(counts, 4) || !slope || !aligned(slope, 4)) return AFD_E_ARG;
+    const BalanceSpace need = balance_space(*cfg, rows);
+    const size_t E = size_t(cfg->num_experts);
+    Span in[2] = {};
+    if (rows > 0) {
+        if (!logits_ok(*cfg, logits, logit_stride) || !ids || !aligned(ids, 4)) return AFD_E_ARG;
+        if (!workspace || !aligned(workspace, 256)) return AFD_E_ARG;
+        if (workspace_bytes < need.total) return AFD_E_CAPACITY;
+        in[0] = span(logits, rows, logit_stride, cfg->num_experts, element_of(cfg->dtype));
+        in[1] = span(ids, rows, cfg->topk, cfg->topk, 4);
+    }
+    const Span to[4] = {{loss, 4}, {counts, E * 4}, {slope, E * 4}, {rows > 0 ? workspace : nullptr, need.total}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(to[i], to[j])) return AFD_E_ARG;
+        for (const Span &s : in)
+            if (overlap(to[i], s)) return AFD_E_ARG;
+    }
+    BalancePlan p;
+    p.r = plan_route(*cfg, rows, logits, logit_stride);
+    p.r.ids = const_cast<int32_t *>(ids);
+    p.coefficient = coefficient;
+    p.loss = loss;
+    p.counts = counts;
+    p.slope = slope;
+    p.groups = balance_groups(rows);
+    char *ws = static_cast<char *>(workspace);
+    if (rows > 0) {
+        p.share = reinterpret_cast<float *>(ws + need.share);
+        p.count = reinterpret_cast<int32_t *>(ws + need.count);
+        p.tokens = reinterpret_cast<int32_t *>(ws + need.tokens);
+    }
+    return be_launch_balance(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
+}
+
+afd_status afd_balance_grad(const afd_route_config *cfg, int64_t rows, const float *grad, const void *logits,
+                            int64_t logit_stride, const int32_t *ids, const float *slope, void *dlogits,
+                            void *stream)
+{
+    const afd_status st = check_route(cfg, rows);
+    if (st != AFD_OK) return st;
+    if (rows == 0) return AFD_OK;
+    const size_t e = element_of(cfg->dtype);
+    if (!logits_ok(*cfg, logits, logit_stride)) return AFD_E_ARG;
+    if (!grad || !aligned(grad, 4) || !ids || !aligned(ids, 4) || !slope || !aligned(slope, 4)) return AFD_E_ARG;
+    if (!dlogits || !aligned(dlogits, e)) return AFD_E_ARG;
+    const Span to = span(dlogits, rows, cfg->num_experts, cfg->num_experts, e);
+    if (overlap(to, span(logits, rows, logit_stride, cfg->num_experts, e)) || overlap(to, Span{grad, 4}) ||
+        overlap(to, span(ids, rows, cfg->topk, cfg->topk, 4)) || overlap(to, Span{slope, size_t(cfg->num_experts) * 4}))
+        return AFD_E_ARG;
+    RoutePlan p = plan_route(*cfg, rows, logits, logit_stride);
+    p.g = grad;
+    p.ids = const_cast<int32_t *>(ids);
+    p.slope = slope;
+    p.dl = dlogits;
+    return be_launch_balance_grad(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
 }
 
 afd_status afd_get_partials(afd_ctx *c, int32_t s, int32_t f, const void **rows, int64_t *row_bytes)

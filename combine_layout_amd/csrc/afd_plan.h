@@ -230,6 +230,67 @@ struct LoadCursor {
     }
 };
 
+// ---- the source's side: norms, routes, the balance loss ----
+
+struct NormPlan {
+    int H = 0;
+    bool x32 = false, r32 = false, res = false, w32 = false, out8 = false;
+    float eps = 0.f;
+    int64_t rows = 0;
+    const void *x = nullptr, *r = nullptr, *w = nullptr;
+    int64_t xs = 0, rs = 0, hs = 0;   // row strides (elements) of x, the residual and h
+    void *out = nullptr, *h = nullptr;
+    float *outs = nullptr, *rstd = nullptr;
+};
+
+// Workgroups of the norm's gradient: each sums dweight over its rows in registers and
+// leaves one partial row of float32, and a second launch adds these up.
+constexpr int kNormGradGroups = 512;
+inline int norm_grad_groups(int64_t rows) { return int(std::min<int64_t>((rows + 3) / 4, kNormGradGroups)); }
+
+struct NormGradPlan {
+    int H = 0;
+    bool h32 = false, w32 = false;
+    int64_t rows = 0, hs = 0;
+    const void *g = nullptr, *gr = nullptr, *h = nullptr, *w = nullptr;
+    const float *rstd = nullptr;
+    void *dh = nullptr;
+    float *dw = nullptr, *part = nullptr;   // part: [groups][H]
+    int groups = 0;
+};
+
+struct RoutePlan {
+    int E = 0, K = 0;
+    bool l32 = false, sigmoid = false, renorm = false;
+    float scale = 1.f;
+    int64_t rows = 0, ls = 0;
+    const void *l = nullptr;
+    const float *bias = nullptr;
+    const uint8_t *live = nullptr;
+    int32_t *ids = nullptr;
+    float *w = nullptr;
+    const float *g = nullptr;      // the gradient calls': of the weights, or of the loss
+    const float *slope = nullptr;  // (balance)
+    void *dl = nullptr;
+};
+
+// Workgroups of the balance loss's first launch; each leaves its sums of the shares, its
+// counts and its number of counting tokens.
+constexpr int kBalanceGroups = 256;
+inline int balance_groups(int64_t rows) { return int(std::min<int64_t>((rows + 15) / 16, kBalanceGroups)); }
+
+struct BalancePlan {
+    RoutePlan r;
+    float coefficient = 1.f;
+    float *loss = nullptr;
+    int32_t *counts = nullptr;
+    float *slope = nullptr;
+    int groups = 0;
+    float *share = nullptr;       // [groups][E]
+    int32_t *count = nullptr;     // [groups][E]
+    int32_t *tokens = nullptr;    // [groups]
+};
+
 // Contexts made by afd_create_static use a static scratch array of this many
 // bytes per GPU as their workspace (one such context per device at a time).
 constexpr size_t kStaticScratchBytes = size_t(AFD_STATIC_SCRATCH_BYTES);
@@ -254,6 +315,13 @@ int be_launch_product(const ProductPlan &p, void *stream);
 int be_launch_pack(const void *w, void *out, int64_t rows, int64_t row_bytes, void *stream);
 // tags[s][t] to the receive rows of partition f, from the round's slot map.
 int be_launch_tags(const RoundPlan &p, int f, const int32_t *const *tags, int32_t *out, void *stream);
+// The source's side.
+int be_launch_norm(const NormPlan &p, void *stream);
+int be_launch_norm_grad(const NormGradPlan &p, void *stream);
+int be_launch_route(const RoutePlan &p, void *stream);
+int be_launch_route_grad(const RoutePlan &p, void *stream);
+int be_launch_balance(const BalancePlan &p, void *stream);
+int be_launch_balance_grad(const RoutePlan &p, void *stream);
 int be_device_sync();
 // The current device and the address of its static scratch array (found
 // once per device); no allocation.

@@ -1,0 +1,453 @@
+"""Python binding of the source's side of a round: the norm with the residual's
+addition, the router's choice, the balance loss, and their gradients.
+
+Argument checks and marshalling only: the arithmetic runs in the HIP library.
+rms_norm, route_tokens and balance_loss are differentiable where an input asks
+for a gradient; their gradients are also calls of their own (rms_norm_grad,
+route_tokens_grad, balance_loss_grad), which is how a captured graph has them.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import NamedTuple, Optional
+
+import torch
+from torch.autograd import forward_ad
+from torch.autograd.function import once_differentiable
+
+from . import _native as nat
+from .experts import SCALE_BLOCK, on_device, raw_stream
+
+_CODES = {torch.bfloat16: nat.AFD_BF16, torch.float32: nat.AFD_FP32}
+
+
+class Normed(NamedTuple):
+    rows: torch.Tensor                # [T, H] bfloat16 or float8_e4m3fn
+    scales: Optional[torch.Tensor]    # [T, H/128] float32 (float8 only)
+    residual: Optional[torch.Tensor]  # [T, H] the stream, x + residual (None without a residual)
+    rstd: Optional[torch.Tensor]      # [T] float32 (with keep_rstd)
+
+
+class Routes(NamedTuple):
+    ids: torch.Tensor      # [T, topk] int32, -1: no expert
+    weights: torch.Tensor  # [T, topk] float32
+
+
+class Balance(NamedTuple):
+    loss: torch.Tensor    # [] float32
+    counts: torch.Tensor  # [E] int32: choices of every expert
+    slope: torch.Tensor   # [E] float32: of the loss by the expert's sum of shares
+
+
+def _asks(*tensors):
+    """Whether a tensor asks for a gradient; what carries a forward one is refused."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("the source's calls have no forward gradients: pass the primal of a dual tensor")
+    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
+
+
+def _plain(call, *tensors):
+    if _asks(*tensors):
+        raise ValueError(f"{call}: no gradient reaches these arguments: detach them or call under no_grad()")
+
+
+def _recorded(call, device, *given):
+    """A call that autograd records makes its own outputs, and outside of a capture: the backward
+    pass of a captured graph meets whatever other graphs hold of the same leaves."""
+    if any(given):
+        raise ValueError(f"{call}: outputs that are given, and float8 rows, have no gradient: leave them out, or call "
+                         f"under no_grad() and {call}_grad for the gradient")
+    if device.type == "cuda":
+        with on_device(device):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError(f"{call}: autograd does not record a captured call: call it under no_grad(), and "
+                                 f"{call}_grad for the gradient")
+
+
+def _rows(t, what, device=None):
+    """[rows, columns] with its columns next to each other; returns the row stride."""
+    if t.dim() != 2 or t.device.type != "cuda" or device is not None and t.device != device or \
+            t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must be a [rows, columns] tensor on {device or 'a GPU'} whose columns lie next to each "
+                         f"other, got {list(t.shape)} with strides {t.stride()} on {t.device}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{what}: rows that share memory (row stride {t.stride(0)} of {t.shape[1]} columns)")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _wide_rows(t, what, device=None):
+    """_rows for a norm: 16-byte pieces."""
+    stride = _rows(t, what, device)
+    if t.numel() and (t.data_ptr() % 16 or stride % 8):
+        raise ValueError(f"{what} must be 16-byte aligned with a row stride in multiples of 8, got {stride} elements")
+    return stride
+
+
+def _want(t, what, dtype, shape, device):
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}, got " + (
+            "None" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}"))
+    return t.data_ptr()
+
+
+def _code(t, what):
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what} must be bfloat16 or float32, got {t.dtype}") from None
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_config(hidden, x, residual, weight, out, eps):
+    if not 0 < hidden <= nat.MAX_NORM_HIDDEN or hidden % (SCALE_BLOCK if out == nat.AFD_FP8_E4M3 else 8):
+        raise ValueError(f"a norm's columns are a multiple of 8 (of 128 for float8 rows) up to {nat.MAX_NORM_HIDDEN}, got "
+                         f"{hidden}")
+    if not torch.finfo(torch.float32).tiny <= eps <= torch.finfo(torch.float32).max:
+        raise ValueError(f"eps must be a normal positive float32, got {eps}")
+    return nat.NormConfig(hidden, x, residual, weight, out, eps)
+
+
+def _normed_checked(x, weight, residual, eps, dtype):
+    """(configuration, strides) of a norm whose inputs are checked."""
+    xs = _wide_rows(x, "x")
+    T, H = x.shape
+    rs, rc = 0, nat.NO_RESIDUAL
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must be {list(x.shape)} like x, got {list(residual.shape)}")
+        rs, rc = _wide_rows(residual, "residual", x.device), _code(residual, "residual")
+    if dtype is not torch.bfloat16 and dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"dtype must be bfloat16 or float8_e4m3fn, got {dtype}")
+    if weight.data_ptr() % 16:
+        raise ValueError("weight must be 16-byte aligned")
+    _want(weight, "weight", weight.dtype, (H,), x.device)
+    cfg = _norm_config(H, _code(x, "x"), rc, _code(weight, "weight"),
+                       nat.AFD_BF16 if dtype is torch.bfloat16 else nat.AFD_FP8_E4M3, float(eps))
+    return cfg, xs, rs
+
+
+def _norm(x, weight, residual, eps, dtype, out, out_scales, residual_out, keep_rstd):
+    cfg, xs, rs = _normed_checked(x, weight, residual, eps, dtype)
+    T, H = x.shape
+    dev, fp8 = x.device, dtype is torch.float8_e4m3fn
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=dev)
+    po = _want(out, "out", dtype, (T, H), dev)
+    ps = pr = ph = None
+    hs = 0
+    if fp8:
+        if out_scales is None:
+            out_scales = torch.empty((T, H // SCALE_BLOCK), dtype=torch.float32, device=dev)
+        ps = _want(out_scales, "out_scales", torch.float32, (T, H // SCALE_BLOCK), dev)
+    elif out_scales is not None:
+        raise ValueError("out_scales belong to float8_e4m3fn rows")
+    if residual is not None:
+        if residual_out is None:
+            residual_out = torch.empty((T, H), dtype=residual.dtype, device=dev)
+        elif residual_out.dtype is not residual.dtype or residual_out.shape != residual.shape:
+            raise ValueError(f"residual_out must be {residual.dtype} {list(residual.shape)} like residual")
+        hs, pr, ph = _wide_rows(residual_out, "residual_out", dev), residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if keep_rstd else None
+    with on_device(dev):
+        st = nat.load().afd_norm(cfg, T, x.data_ptr(), xs, pr, rs, weight.data_ptr(), po, ps, ph, hs,
+                                 rstd.data_ptr() if keep_rstd else None, raw_stream(dev))
+    nat.check(st, "rms_norm")
+    return Normed(out, out_scales, residual_out, rstd)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        n = _norm(x, weight, residual, eps, torch.bfloat16, None, None, None, True)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(n.rstd)
+        ctx.save_for_backward(x if residual is None else n.residual, weight, n.rstd)
+        ctx.types = x.dtype, None if residual is None else residual.dtype
+        return n.rows, n.residual, n.rstd
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad, grad_residual, _):
+        if grad is None and grad_residual is None:
+            return None, None, None, None
+        h, weight, rstd = ctx.saved_tensors
+        xt, rt = ctx.types
+        dw = None
+        if grad is None:
+            dh = grad_residual
+        else:
+            with on_device(h.device):
+                if torch.cuda.is_current_stream_capturing():
+                    raise ValueError("rms_norm: its backward pass is not captured: call rms_norm_grad")
+            dh, dw = rms_norm_grad(_dense(grad), h, weight, rstd,
+                                   grad_residual=None if grad_residual is None else _dense(grad_residual),
+                                   weight_grad=ctx.needs_input_grad[1])
+        return (dh.to(xt) if ctx.needs_input_grad[0] else None, None if dw is None else dw.to(weight.dtype),
+                dh if rt is not None and ctx.needs_input_grad[2] else None, None)
+
+
+def _dense(t):
+    """A gradient as autograd hands it on, in memory as the calls take it."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def rms_norm(x, weight, residual=None, *, eps=1e-6, dtype=torch.bfloat16, out=None, out_scales=None, residual_out=None,
+             keep_rstd=False) -> Normed:
+    """The root-mean-square norm of h = x + residual (or of x), rows y = h / sqrt(mean(h^2) + eps) * weight.
+
+    x [T, H], residual [T, H] and weight [H] are bfloat16 or float32 each; H is a multiple
+    of 8 up to 65536.  h is the float32 sum in the residual's type, kept in residual_out (new
+    memory, the residual itself, or x itself where type and strides are the same) and
+    normalised as kept.  dtype torch.float8_e4m3fn (H a multiple of 128) gives codes with
+    their scales per 128 columns, as source_dispatch takes them: scale = amax / 448 of the
+    float32 y, 0 below 2^-126.  x, residual and residual_out may have gaps between rows
+    (16-byte aligned, strides in multiples of 8); out is contiguous, and may be a bfloat16 x.
+    keep_rstd: also 1 / sqrt(mean(h^2) + eps), for rms_norm_grad.
+
+    Differentiable by x, residual and weight with bfloat16 rows in new memory, outside of
+    a capture; the rounding of h counts as none, and x and residual share one gradient.
+    Runs on x's device and its current stream."""
+    _plain("rms_norm", out, out_scales, residual_out)
+    if _asks(x, weight, residual):
+        _recorded("rms_norm", x.device, out is not None, out_scales is not None, residual_out is not None,
+                  dtype is not torch.bfloat16)
+        rows, h, rstd = _RmsNorm.apply(x, weight, residual, eps)
+        return Normed(rows, None, h, rstd if keep_rstd else None)
+    return _norm(x, weight, residual, eps, dtype, out, out_scales, residual_out, keep_rstd)
+
+
+def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight_grad=True):
+    """The gradients (dh, dweight) of rms_norm with bfloat16 rows.
+
+    grad bfloat16 [T, H], of the rows; h as rms_norm kept it (or x, without a residual), and
+    its rstd; grad_residual: of h as the stream goes on, contiguous in h's type.  dh, in h's
+    type, is the gradient of x and of the residual alike; out may be grad_residual, or a
+    grad of h's type.  dweight is float32 [H], None without weight_grad."""
+    _plain("rms_norm_grad", grad, h, weight, rstd, grad_residual, out)
+    hs = _wide_rows(h, "h")
+    T, H = h.shape
+    dev, lib = h.device, nat.load()
+    if weight.data_ptr() % 16:
+        raise ValueError("weight must be 16-byte aligned")
+    pw, pg = _want(weight, "weight", weight.dtype, (H,), dev), _want(grad, "grad", torch.bfloat16, (T, H), dev)
+    pr = None if grad_residual is None else _want(grad_residual, "grad_residual", h.dtype, (T, H), dev)
+    ps = _want(rstd, "rstd", torch.float32, (T,), dev)
+    cfg = _norm_config(H, _code(h, "h"), nat.NO_RESIDUAL, _code(weight, "weight"), nat.AFD_BF16, 1.0)
+    if out is None:
+        out = torch.empty((T, H), dtype=h.dtype, device=dev)
+    po = _want(out, "out", h.dtype, (T, H), dev)
+    for what, t in (("grad", grad), ("grad_residual", grad_residual), ("out", out)):
+        if t is not None and t.data_ptr() % 16:
+            raise ValueError(f"{what} must be 16-byte aligned")
+    dw = ws = None
+    need = 0
+    if weight_grad:
+        need = _norm_grad_need(H, T)
+        dw = torch.empty(H, dtype=torch.float32, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    with on_device(dev):
+        st = lib.afd_norm_grad(cfg, T, pg, pr, h.data_ptr(), hs, pw, ps, po, dw.data_ptr() if weight_grad else None,
+                               ws.data_ptr() if need else None, need, raw_stream(dev))
+    nat.check(st, "rms_norm_grad")
+    return out, dw
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_grad_need(hidden, rows):
+    c, ws = _norm_config(hidden, nat.AFD_BF16, nat.NO_RESIDUAL, nat.AFD_BF16, nat.AFD_BF16, 1.0), ctypes.c_size_t(0)
+    nat.check(nat.load().afd_norm_grad_query(ctypes.byref(c), rows, ctypes.byref(ws)), "rms_norm_grad")
+    return ws.value
+
+
+@functools.lru_cache(maxsize=256)
+def _route_config(experts, topk, code, scoring, renormalize, scale):
+    if not 0 < experts <= nat.MAX_EXPERTS:
+        raise ValueError(f"logits must have 1 to {nat.MAX_EXPERTS} experts, got {experts}")
+    if not 0 < topk <= min(nat.MAX_TOPK, experts):
+        raise ValueError(f"topk must be 1 to {min(nat.MAX_TOPK, experts)} of {experts} experts, got {topk}")
+    if scoring not in nat.SCORINGS:
+        raise ValueError(f"scoring must be one of {sorted(nat.SCORINGS)}, got {scoring!r}")
+    if not abs(scale) <= torch.finfo(torch.float32).max:
+        raise ValueError(f"scale must be a finite float32, got {scale}")
+    return nat.RouteConfig(experts, topk, code, nat.SCORINGS[scoring], int(renormalize), scale)
+
+
+def _topk_of(t, what, logits, dtype):
+    """The checked pointer of [T, topk] beside the logits."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be [T, topk], got {list(t.shape)}")
+    return _want(t, what, dtype, (logits.shape[0], t.shape[1]), logits.device)
+
+
+def _route(logits, topk, scoring, bias, renormalize, scale, live, ids, weights):
+    ls = _rows(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    cfg = _route_config(E, int(topk), _code(logits, "logits"), scoring, bool(renormalize), float(scale))
+    pb = None if bias is None else _want(bias, "bias", torch.float32, (E,), dev)
+    pl = None if live is None else _want(live, "live", torch.bool, (T,), dev)
+    if ids is None:
+        ids = torch.empty((T, cfg.topk), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, cfg.topk), dtype=torch.float32, device=dev)
+    pi = _want(ids, "ids", torch.int32, (T, cfg.topk), dev)
+    pw = _want(weights, "weights", torch.float32, (T, cfg.topk), dev)
+    with on_device(dev):
+        st = nat.load().afd_route(cfg, T, logits.data_ptr(), ls, pb, pl, pi, pw, raw_stream(dev))
+    nat.check(st, "route_tokens")
+    return Routes(ids, weights)
+
+
+class _RouteTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk, scoring, bias, renormalize, scale, live):
+        r = _route(logits, topk, scoring, bias, renormalize, scale, live, None, None)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(r.ids)
+        ctx.save_for_backward(logits, r.ids)
+        ctx.how = dict(scoring=scoring, renormalize=renormalize, scale=scale)
+        return r.ids, r.weights
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, grad):
+        if grad is None:
+            return (None,) * 7
+        logits, ids = ctx.saved_tensors
+        with on_device(logits.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("route_tokens: its backward pass is not captured: call route_tokens_grad")
+        return (route_tokens_grad(grad.contiguous(), logits, ids, **ctx.how),) + (None,) * 6
+
+
+def route_tokens(logits, topk, *, scoring="softmax", bias=None, renormalize=True, scale=1.0, live=None, ids=None,
+                 weights=None) -> Routes:
+    """Every token's topk experts and their weights, as source_dispatch takes them.
+
+    logits [T, E] bfloat16 or float32, E up to 512, topk up to 32; rows may have gaps.
+    Scores are the logits' "softmax" or "sigmoid".  ids are in falling order of score, with
+    bias (float32 [E]) of score + bias, the lower id first where equal (compared as 64-bit
+    scores with a bias, as logits without).  weights are scale * score, with renormalize
+    divided by the sum of the token's chosen scores; the bias is not in them.  live (bool
+    [T]): tokens that are False have ids -1 and weights 0.  An expert whose logit (or score
+    + bias) is minus infinity or NaN is never chosen; ids that are left over are -1, with
+    weight 0.  ids and weights: memory for the results.
+
+    The weights are differentiable by the logits, outside of a capture; the choice has no
+    gradient.  Runs on the logits' device and its current stream."""
+    _plain("route_tokens", bias, live, ids, weights)
+    if _asks(logits):
+        _recorded("route_tokens", logits.device, ids is not None, weights is not None)
+        return Routes(*_RouteTokens.apply(logits, topk, scoring, bias, renormalize, scale, live))
+    return _route(logits, topk, scoring, bias, renormalize, scale, live, ids, weights)
+
+
+def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True, scale=1.0, out=None):
+    """The logits' gradient, [T, E] of their type, through the weights of route_tokens: grad float32
+    [T, topk], ids as they were chosen (any outside [0, E) takes no part)."""
+    _plain("route_tokens_grad", grad, logits, ids, out)
+    ls = _rows(logits, "logits")
+    pi, pg = _topk_of(ids, "ids", logits, torch.int32), _topk_of(grad, "grad", logits, torch.float32)
+    if grad.shape != ids.shape:
+        raise ValueError("grad and ids must have one shape")
+    (T, E), dev = logits.shape, logits.device
+    cfg = _route_config(E, ids.shape[1], _code(logits, "logits"), scoring, bool(renormalize), float(scale))
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    po = _want(out, "out", logits.dtype, (T, E), dev)
+    with on_device(dev):
+        st = nat.load().afd_route_grad(cfg, T, pg, logits.data_ptr(), ls, pi, po, raw_stream(dev))
+    nat.check(st, "route_tokens_grad")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _balance_need(rows, *cfg):
+    ws = ctypes.c_size_t(0)
+    nat.check(nat.load().afd_balance_query(ctypes.byref(_route_config(*cfg)), rows, ctypes.byref(ws)), "balance_loss")
+    return ws.value
+
+
+def _balance(logits, ids, scoring, coefficient):
+    ls = _rows(logits, "logits")
+    pi = _topk_of(ids, "ids", logits, torch.int32)
+    (T, E), dev = logits.shape, logits.device
+    key = E, ids.shape[1], _code(logits, "logits"), scoring, False, 1.0
+    cfg, need = _route_config(*key), _balance_need(T, *key)
+    coefficient = float(coefficient)
+    if not abs(coefficient) <= torch.finfo(torch.float32).max:
+        raise ValueError(f"coefficient must be a finite float32, got {coefficient}")
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    slope = torch.empty(E, dtype=torch.float32, device=dev)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    with on_device(dev):
+        st = nat.load().afd_balance(cfg, T, logits.data_ptr(), ls, pi, coefficient, loss.data_ptr(), counts.data_ptr(),
+                                    slope.data_ptr(), ws.data_ptr(), need, raw_stream(dev))
+    nat.check(st, "balance_loss")
+    return Balance(loss, counts, slope)
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, scoring, coefficient):
+        b = _balance(logits, ids, scoring, coefficient)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(b.counts, b.slope)
+        ctx.save_for_backward(logits, ids, b.slope)
+        ctx.scoring = scoring
+        return tuple(b)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad, *_):
+        if grad is None:
+            return None, None, None, None
+        logits, ids, slope = ctx.saved_tensors
+        with on_device(logits.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("balance_loss: its backward pass is not captured: call balance_loss_grad")
+        return balance_loss_grad(grad, logits, ids, slope, scoring=ctx.scoring), None, None, None
+
+
+def balance_loss(logits, ids, *, scoring="softmax", coefficient=1.0) -> Balance:
+    """The experts' loads and the loss that keeps them even, of the tokens that have an expert.
+
+    logits [T, E] as in route_tokens, ids int32 [T, topk] (route_tokens' or any; those
+    outside [0, E) are skipped, and a token with no other does not count).  With n counting
+    tokens, C choices in all and share[t, e] a token's softmax (or its sigmoids, divided by
+    their sum): slope[e] = coefficient * E * counts[e] / (C * n) and loss = sum of slope[e] *
+    share[t, e] over counting tokens and experts, which is the coefficient where use and
+    shares are even.  Without a counting token the loss is 0.
+
+    The loss is differentiable by the logits, through the shares, outside of a capture.
+    Runs on the logits' device and its current stream."""
+    _plain("balance_loss", ids)
+    if _asks(logits):
+        _recorded("balance_loss", logits.device)
+        return Balance(*_BalanceLoss.apply(logits, ids, scoring, coefficient))
+    return _balance(logits, ids, scoring, coefficient)
+
+
+def balance_loss_grad(grad, logits, ids, slope, *, scoring="softmax", out=None):
+    """The logits' gradient, [T, E] of their type: grad float32 [], of the loss on the GPU;
+    ids and slope as balance_loss had and gave them.  Tokens that do not count have 0."""
+    _plain("balance_loss_grad", grad, logits, ids, slope, out)
+    ls = _rows(logits, "logits")
+    pi = _topk_of(ids, "ids", logits, torch.int32)
+    (T, E), dev = logits.shape, logits.device
+    pg, ps = _want(grad, "grad", torch.float32, (), dev), _want(slope, "slope", torch.float32, (E,), dev)
+    cfg = _route_config(E, ids.shape[1], _code(logits, "logits"), scoring, False, 1.0)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    po = _want(out, "out", logits.dtype, (T, E), dev)
+    with on_device(dev):
+        st = nat.load().afd_balance_grad(cfg, T, pg, logits.data_ptr(), ls, pi, ps, po, raw_stream(dev))
+    nat.check(st, "balance_loss_grad")
+    return out

@@ -57,7 +57,8 @@ typedef enum {
     AFD_E_TIMEOUT = -7    /* a one-launch dispatch gave up waiting between workgroups */
 } afd_status;
 
-typedef enum { AFD_BF16 = 0, AFD_FP8_E4M3 = 1 } afd_dtype;
+/* AFD_FP32: only where a call says so (the source's side). */
+typedef enum { AFD_BF16 = 0, AFD_FP8_E4M3 = 1, AFD_FP32 = 2 } afd_dtype;
 
 /*
  * How the combine rounds (afdEP-comm design page; section 6 on rounding per
@@ -570,6 +571,190 @@ afd_status afd_expert_ffn(const afd_ffn_config *cfg, int64_t rows, const void *x
  */
 afd_status afd_worker_tags(afd_ctx *ctx, int32_t f, const int32_t *const *tags, int32_t *out, int64_t receive_rows,
                            const afd_receipt *receipt, void *stream);
+
+/*
+ * ---- the source's side of a round -------------------------------------------
+ *
+ * What an Attention source computes around the exchange: behind
+ * afd_source_collect the collected sum joins the residual stream and is
+ * normalised into the rows that the next afd_source_dispatch takes (BF16, or
+ * E4M3 codes with their scales); from its router's logits come the ids and
+ * weights of the same call, and the loss that keeps the experts evenly used.
+ * The calls take no context, keep no state and enqueue on `stream` (of the
+ * current device); calls on several streams may run at the same time, with
+ * different workspaces.  rows is below 2^24; a row stride counts elements, is
+ * at least the row's length and below 2^31.  Every sum is float32, in an order
+ * that the sizes alone decide: the same inputs give the same bits.
+ *
+ * The gradients are calls of their own.  They end at the exchange: a round
+ * carries none.
+ */
+
+#define AFD_MAX_NORM_HIDDEN 65536
+#define AFD_NO_RESIDUAL (-1)
+
+/*
+ * Root-mean-square norm, with the residual's addition in front:
+ *     h = x + residual in float32, rounded to the residual's type (without a residual h = x),
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ * of every row.  What is normalised is h as it is stored, so the gradient,
+ * which starts from the stored h, belongs to this y.
+ *   hidden          columns, a positive multiple of 8 (of 128 with an FP8 output), at
+ *                   most AFD_MAX_NORM_HIDDEN
+ *   x_dtype         AFD_BF16 or AFD_FP32
+ *   residual_dtype  the same, or AFD_NO_RESIDUAL
+ *   weight_dtype    AFD_BF16 or AFD_FP32
+ *   out_dtype       AFD_BF16, or AFD_FP8_E4M3: per row and 128 columns scale = amax / 448
+ *                   and code = e4m3(y * (1 / scale)) to nearest even, from the float32 y; a
+ *                   scale below 2^-126 counts as 0 and gives codes 0.  A block with an
+ *                   infinity has the scale infinity, NaN codes for its infinities and 0 for the rest.
+ *   eps             at least float32's smallest normal number
+ */
+typedef struct {
+    int32_t hidden;
+    int32_t x_dtype;        /* afd_dtype */
+    int32_t residual_dtype; /* afd_dtype or AFD_NO_RESIDUAL */
+    int32_t weight_dtype;   /* afd_dtype */
+    int32_t out_dtype;      /* afd_dtype */
+    float eps;
+} afd_norm_config;
+
+/*
+ * afd_norm:
+ *   x             device [rows, hidden], row stride x_stride
+ *   residual      device [rows, hidden], row stride residual_stride (NULL without)
+ *   weight        device [hidden]
+ *   out           device [rows, hidden], contiguous; may be x itself (BF16 x without gaps)
+ *   out_scales    device [rows, hidden/128] FP32 (FP8 output, else NULL)
+ *   residual_out  device [rows, hidden] of the residual's type, row stride
+ *                 residual_out_stride: h (NULL without a residual); may be the residual
+ *                 itself, or x itself where type and stride are the same
+ *   rstd          device [rows] FP32, 1 / sqrt(mean(h^2) + eps), for afd_norm_grad, or NULL
+ * x, residual, out and residual_out are 16-byte aligned and their strides multiples of 8.
+ * Otherwise no output may share its span, gaps included, with an input or another output.
+ * Errors: AFD_E_ARG (pointers, alignment, strides, overlap, rows), AFD_E_SHAPE, AFD_E_HIP.
+ */
+afd_status afd_norm(const afd_norm_config *cfg, int64_t rows, const void *x, int64_t x_stride, const void *residual,
+                    int64_t residual_stride, const void *weight, void *out, float *out_scales, void *residual_out,
+                    int64_t residual_out_stride, float *rstd, void *stream);
+
+/* afd_norm_grad_query: workspace bytes of afd_norm_grad with a dweight (without, it
+ * takes none).  Pure host computation.  Errors: AFD_E_ARG, AFD_E_SHAPE. */
+afd_status afd_norm_grad_query(const afd_norm_config *cfg, int64_t rows, size_t *workspace_bytes);
+
+/*
+ * afd_norm_grad, of a norm with BF16 output.  With u = h * rstd and a = grad * weight:
+ *     dh = rstd * (a - u * mean(a * u)) + grad_residual,  dweight = sum over rows of grad * u.
+ * dh is the gradient of x and of the residual alike (the rounding of h counts as none).
+ *   grad           device [rows, hidden] BF16, of y
+ *   grad_residual  device [rows, hidden] of h's type, of h as the stream goes on, or NULL (none)
+ *   h              device [rows, hidden], row stride h_stride: residual_out, or x without a residual
+ *   rstd           device [rows], from afd_norm
+ *   dh             device [rows, hidden] of h's type; may be grad_residual itself, or grad
+ *                  itself where the types are the same; may not share memory with h
+ *   dweight        device [hidden] FP32, or NULL (not computed); written also where rows is 0
+ *   workspace      device, 256-byte aligned; in use until the call's work has run
+ * All arrays but h are contiguous; all but rstd and dweight are 16-byte aligned.
+ * Errors: as afd_norm, and AFD_E_CAPACITY (workspace); AFD_E_SHAPE for an FP8 output, whose
+ * rounding has no gradient.
+ */
+afd_status afd_norm_grad(const afd_norm_config *cfg, int64_t rows, const void *grad, const void *grad_residual,
+                         const void *h, int64_t h_stride, const void *weight, const float *rstd, void *dh,
+                         float *dweight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* An expert's score in a token's eyes, from the token's logits. */
+typedef enum {
+    AFD_SCORE_SOFTMAX = 0, /* exp(l_e) / sum of exp(l) over all experts */
+    AFD_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-l_e)) */
+} afd_scoring;
+
+/*
+ * A router's choice.
+ *   num_experts  E, 1..AFD_MAX_EXPERTS
+ *   topk         K, 1 <= K <= min(AFD_MAX_TOPK, E)
+ *   dtype        of the logits and their gradient: AFD_BF16 or AFD_FP32
+ *   scoring      afd_scoring
+ *   renormalize  1: a token's weights are divided by their sum; 0: not
+ *   scale        finite; factor of every weight
+ * afd_balance and afd_balance_grad take no notice of renormalize and scale.
+ */
+typedef struct {
+    int32_t num_experts;
+    int32_t topk;
+    int32_t dtype;   /* afd_dtype */
+    int32_t scoring; /* afd_scoring */
+    int32_t renormalize;
+    float scale;
+} afd_route_config;
+
+/*
+ * afd_route: every token's K experts and their weights, as afd_source_dispatch takes them.
+ *   logits   device [rows, E], row stride logit_stride
+ *   bias     device [E] FP32, or NULL: experts are chosen by score + bias, weighted by
+ *            their scores alone
+ *   live     device [rows] bytes, or NULL: a token with 0 has no experts
+ *   ids      device [rows, K] int32: in falling order of score (+ bias), the lower id first
+ *            where they are equal; scores are compared as 64-bit numbers with a bias, and
+ *            as their logits without
+ *   weights  device [rows, K] FP32: scale * score, divided by the sum of the chosen scores
+ *            with renormalize
+ * An expert whose logit is minus infinity or NaN, or whose score + bias is, is never
+ * chosen; where fewer than K are left, the remaining ids are -1 with weight 0.  Among the
+ * softmax's terms a NaN counts as minus infinity; experts at plus infinity share it evenly.
+ * logits need the alignment of their type alone (16 bytes and a stride in multiples of four
+ * elements are faster).
+ * Errors: AFD_E_ARG (pointers, alignment, rows, stride), AFD_E_SHAPE, AFD_E_HIP.
+ */
+afd_status afd_route(const afd_route_config *cfg, int64_t rows, const void *logits, int64_t logit_stride,
+                     const float *bias, const uint8_t *live, int32_t *ids, float *weights, void *stream);
+
+/*
+ * afd_route_grad: the logits' gradient through the weights, with the choice as it was.
+ *   grad     device [rows, K] FP32, of the weights
+ *   ids      device [rows, K], from afd_route; any outside [0, E) takes no part
+ *   dlogits  device [rows, E], contiguous, of the logits' type; not overlapping an input
+ * Errors: as afd_route.
+ */
+afd_status afd_route_grad(const afd_route_config *cfg, int64_t rows, const float *grad, const void *logits,
+                          int64_t logit_stride, const int32_t *ids, void *dlogits, void *stream);
+
+/* afd_balance_query: workspace bytes of afd_balance.  Pure host computation.  Errors:
+ * AFD_E_ARG, AFD_E_SHAPE. */
+afd_status afd_balance_query(const afd_route_config *cfg, int64_t rows, size_t *workspace_bytes);
+
+/*
+ * afd_balance: the experts' loads and the balance loss of a batch of routes.  A token
+ * counts if one of its ids is in [0, E); n such tokens made C choices, counts[e] of them
+ * expert e.  share[t, e] is a token's softmax, or with AFD_SCORE_SIGMOID its scores divided
+ * by their sum:
+ *     slope[e] = coefficient * E * counts[e] / (C * n)
+ *     loss     = sum over e of slope[e] * sum over counting tokens of share[t, e]
+ * so that even use with even shares gives the coefficient.  No counting token: loss 0.
+ *   ids        device [rows, K] int32; any outside [0, E) is skipped, and one that stands
+ *              twice in a token counts twice
+ *   loss       device, one FP32
+ *   counts     device [E] int32
+ *   slope      device [E] FP32, for afd_balance_grad
+ *   workspace  device, at least afd_balance_query bytes, 256-byte aligned; in use until the
+ *              call's work has run
+ * loss, counts and slope are written also where rows is 0.
+ * Errors: AFD_E_ARG (pointers, alignment, rows, stride, coefficient not finite), AFD_E_SHAPE,
+ * AFD_E_CAPACITY (workspace), AFD_E_HIP.
+ */
+afd_status afd_balance(const afd_route_config *cfg, int64_t rows, const void *logits, int64_t logit_stride,
+                       const int32_t *ids, float coefficient, float *loss, int32_t *counts, float *slope,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * afd_balance_grad: the logits' gradient of the loss, through the shares (the counts have none).
+ *   grad     device, one FP32: of the loss
+ *   dlogits  device [rows, E], contiguous, of the logits' type; not overlapping an input
+ * A token that does not count has the gradient 0.
+ * Errors: as afd_route.
+ */
+afd_status afd_balance_grad(const afd_route_config *cfg, int64_t rows, const float *grad, const void *logits,
+                            int64_t logit_stride, const int32_t *ids, const float *slope, void *dlogits,
+                            void *stream);
 
 /* afd_status_string: a static description of a status. */
 const char *afd_status_string(afd_status st);

@@ -194,9 +194,10 @@ int be_launch_route_grad(const RoutePlan &p, void *)
 
 int be_launch_balance(const BalancePlan &p, void *)
 {
-    logf("balance E=%d K=%d l32=%d sigmoid=%d rows=%lld ls=%lld coefficient=%g groups=%d share=%p count=%p tokens=%p", p.r.E, p.r.K,
+    logf("balance E=%d K=%d l32=%d sigmoid=%d rows=%lld ls=%lld coefficient=%g groups=%d wide=%d share=%p count=%p totals=%p part=%p done=%p", p.r.E, p.r.K,
          p.r.l32, p.r.sigmoid, static_cast<long long>(p.r.rows), static_cast<long long>(p.r.ls), double(p.coefficient),
-         p.groups, static_cast<void *>(p.share), static_cast<void *>(p.count), static_cast<void *>(p.tokens));
+         p.groups, p.wide, static_cast<void *>(p.share), static_cast<void *>(p.count), static_cast<void *>(p.totals),
+         static_cast<void *>(p.part), static_cast<void *>(p.done));
     return g_fail;
 }
 

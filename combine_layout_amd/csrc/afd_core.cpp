@@ -437,13 +437,19 @@ RoutePlan plan_route(const afd_route_config &c, int64_t rows, const void *logits
 
 // Workspace of the balance loss.
 struct BalanceSpace {
-    size_t share, count, tokens, total;
+    size_t share, count, totals, part, done, total;
 };
 
 BalanceSpace balance_space(const afd_route_config &c, int64_t rows)
 {
-    const size_t g = size_t(balance_groups(rows)), each = align256(g * size_t(c.num_experts) * 4);
-    return {0, each, 2 * each, 2 * each + align256(g * 4)};
+    const size_t g = size_t(balance_groups(rows, c.num_experts)), E = size_t(c.num_experts);
+    BalanceSpace s{};
+    s.count = align256(g * E * 4);
+    s.totals = s.count + align256(g * E * 4);
+    s.part = s.totals + align256(g * 8);
+    s.done = s.part + align256((E + 15) / 16 * 8);
+    s.total = rows > 0 ? s.done + 256 : 0;
+    return s;
 }
 
 }  // namespace
@@ -1069,12 +1075,15 @@ afd_status afd_balance(const afd_route_config *cfg, int64_t rows, const void *lo
     p.loss = loss;
     p.counts = counts;
     p.slope = slope;
-    p.groups = balance_groups(rows);
+    p.groups = balance_groups(rows, cfg->num_experts);
+    p.wide = balance_wide(rows, cfg->num_experts);
     char *ws = static_cast<char *>(workspace);
     if (rows > 0) {
         p.share = reinterpret_cast<float *>(ws + need.share);
         p.count = reinterpret_cast<int32_t *>(ws + need.count);
-        p.tokens = reinterpret_cast<int32_t *>(ws + need.tokens);
+        p.totals = reinterpret_cast<int32_t *>(ws + need.totals);
+        p.part = reinterpret_cast<double *>(ws + need.part);
+        p.done = reinterpret_cast<uint32_t *>(ws + need.done);
     }
     return be_launch_balance(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
 }

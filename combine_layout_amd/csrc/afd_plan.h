@@ -274,10 +274,19 @@ struct RoutePlan {
     void *dl = nullptr;
 };
 
-// Workgroups of the balance loss's first launch; each leaves its sums of the shares, its
-// counts and its number of counting tokens.
+// Lanes that hold a token's logits.
+inline int lanes_of(int E) { return E <= 128 ? 16 : E <= 256 ? 32 : 64; }
+
+// Workgroups of the balance loss's first launch: each leaves its sums of the shares, its
+// counts, and its numbers of counting tokens and of choices.
 constexpr int kBalanceGroups = 256;
-inline int balance_groups(int64_t rows) { return int(std::min<int64_t>((rows + 15) / 16, kBalanceGroups)); }
+inline int balance_groups(int64_t rows, int E)
+{
+    const int64_t each = 256 / lanes_of(E);
+    return int(std::min<int64_t>((rows + each - 1) / each, kBalanceGroups));
+}
+// Workgroups of 1024 threads instead of 256 where those would take more than two turns.
+inline bool balance_wide(int64_t rows, int E) { return rows > int64_t(2) * kBalanceGroups * (256 / lanes_of(E)); }
 
 struct BalancePlan {
     RoutePlan r;
@@ -286,9 +295,12 @@ struct BalancePlan {
     int32_t *counts = nullptr;
     float *slope = nullptr;
     int groups = 0;
+    bool wide = false;
     float *share = nullptr;       // [groups][E]
     int32_t *count = nullptr;     // [groups][E]
-    int32_t *tokens = nullptr;    // [groups]
+    int32_t *totals = nullptr;    // [groups][2] counting tokens, choices
+    double *part = nullptr;       // [(E + 15) / 16] of the loss
+    uint32_t *done = nullptr;     // workgroups of the second launch that have left theirs
 };
 
 // Contexts made by afd_create_static use a static scratch array of this many

@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "afd_plan.h"
 
@@ -33,7 +34,10 @@ struct Sum {
 struct Max {
     __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
-struct Min {
+struct MaxInt {
+    __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
+};
+struct MinInt {
     __device__ __forceinline__ int operator()(int a, int b) const { return min(a, b); }
 };
 
@@ -349,21 +353,25 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm_grad(NormGr
     }
 }
 
-// dweight: 64 columns a workgroup, 16 wavefronts that share the partial rows.
+// dweight: 64 columns a workgroup, four a thread, the partial rows over 64 of its threads.
 __global__ __launch_bounds__(1024) void k_norm_grad_join(const float *part, float *dw, int H, int groups)
 {
-    __shared__ float join[16][kWave];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * kWave + lane;
-    float s = 0.f;
-    if (c < H)
-        for (int g = wave; g < groups; g += 16) s += part[int64_t(g) * H + c];
-    join[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && c < H) {
-        s = 0.f;
+    __shared__ f32x4 join[64][16];
+    const int col = threadIdx.x % 16, slice = threadIdx.x / 16, c = blockIdx.x * 64 + col * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (c < H) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += join[i][lane];
-        dw[c] = s;
+        for (int i = 0; i < kNormGradGroups / 64; ++i)
+            if (i * 64 + slice < groups) s += *reinterpret_cast<const f32x4 *>(part + int64_t(i * 64 + slice) * H + c);
+    }
+    join[slice][col] = s;
+    __syncthreads();
+    const int one = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && one < H) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) t += reinterpret_cast<const float *>(join[i])[threadIdx.x];
+        dw[one] = t;
     }
 }
 
@@ -377,8 +385,16 @@ constexpr float kMinusInf = -__builtin_inff();
 __device__ __forceinline__ float exp_neg(float x)
 {
     x = fmaxf(x, -120.f);
-    const float hi = x * 1.44269504f, lo = fmaf(x, 1.44269504f, -hi) + x * 1.92596300e-8f;
-    return __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.693147181f, 1.0f);
+    const float hi = x * 1.44269504f, lo = fmaf(x, 1.92596300e-8f, fmaf(x, 1.44269504f, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return fmaf(e, lo * 0.693147181f, e);
+}
+
+// 1 / d for d in [1, 2]: the hardware's reciprocal and one step of Newton's.
+__device__ __forceinline__ float inverse(float d)
+{
+    const float r = __builtin_amdgcn_rcpf(d);
+    return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
 struct RouteArgs {
@@ -392,19 +408,21 @@ struct RouteArgs {
     int64_t ls;
     int rows, E, K;
     float scale;
-    bool sigmoid, renorm, vec;
+    bool sigmoid, renorm;
 };
 
-// A token's logits over LANES lanes, V a lane in runs of four: value i of a lane is of
-// expert (i / 4) * 4 * LANES + 4 * lane + i % 4.  Experts behind the last, and NaNs, are
-// minus infinity.
-template <bool L32, int LANES, int V>
+// A token's logits over LANES lanes, V a lane in runs of four, so that the lanes of a load or
+// store touch one run of memory (eight consecutive ones a lane: 47 us instead of 31 for the
+// balance loss's gradient of 32768 tokens and 512 experts).  Experts behind the last, and
+// NaNs, are minus infinity.
+template <bool L32, int LANES, int V, bool VEC>
 struct Row {
-    static constexpr int kRows = 256 / LANES;   // tokens of a workgroup
+    static constexpr int kLanes = LANES, kV = V;
+    static constexpr int kRows = 256 / LANES;   // tokens of a workgroup of 256
     static constexpr int kSlots = (kMaxTopk + LANES - 1) / LANES;
 
     __device__ static __forceinline__ int lane() { return threadIdx.x & (LANES - 1); }
-    __device__ static __forceinline__ int expert(int i) { return (i / 4) * 4 * LANES + 4 * lane() + i % 4; }
+    __device__ static __forceinline__ int expert(int i) { return (i & 4) * LANES + 4 * lane() + (i & 3); }
 
     __device__ static __forceinline__ float one(const RouteArgs &a, int64_t at)
     {
@@ -412,30 +430,50 @@ struct Row {
         return from_bf16(static_cast<const uint16_t *>(a.l)[at]);
     }
 
-    __device__ static __forceinline__ void load(const RouteArgs &a, int64_t row, float *v)
-    {
-        const int64_t base = row * a.ls;
+    // Logits as they lie in memory, so that nothing waits for a load before it is needed.
+    struct Raw {
+        typename std::conditional<L32, f32x4, u32x2>::type q[V / 4];
+
+        __device__ __forceinline__ void load(const RouteArgs &a, int64_t row)
+        {
+            const int64_t base = row * a.ls;
 #pragma unroll
-        for (int q = 0; q < V / 4; ++q) {
-            const int e = expert(q * 4);
-            f32x4 x = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};
-            if (a.vec) {
-                if (e < a.E) {
-                    if (L32) {
-                        x = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.l) + base + e);
-                    } else {
-                        const u32x2 u = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(a.l) + base + e);
-                        x = f32x4{from_bf16(u[0] & 0xFFFFu), from_bf16(u[0] >> 16), from_bf16(u[1] & 0xFFFFu), from_bf16(u[1] >> 16)};
+            for (int i = 0; i < V / 4; ++i) {
+                const int e = expert(i * 4);
+                q[i] = {};
+                if constexpr (VEC) {
+                    if (e < a.E) {
+                        if constexpr (L32) q[i] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.l) + base + e);
+                        else q[i] = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(a.l) + base + e);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (e + j >= a.E) continue;
+                        if constexpr (L32) q[i][j] = static_cast<const float *>(a.l)[base + e + j];
+                        else q[i][j / 2] |= uint32_t(static_cast<const uint16_t *>(a.l)[base + e + j]) << (16 * (j & 1));
                     }
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (e + j < a.E) x[j] = one(a, base + e + j);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[q * 4 + j] = x[j] == x[j] ? x[j] : kMinusInf;
         }
+
+        __device__ __forceinline__ void values(const RouteArgs &a, float *v) const
+        {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float x;
+                if constexpr (L32) x = q[i / 4][i & 3];
+                else x = from_bf16(i & 1 ? q[i / 4][(i & 3) / 2] >> 16 : q[i / 4][(i & 3) / 2] & 0xFFFFu);
+                v[i] = expert(i) < a.E && x == x ? x : kMinusInf;
+            }
+        }
+    };
+
+    __device__ static __forceinline__ void load(const RouteArgs &a, int64_t row, float *v)
+    {
+        Raw r;
+        r.load(a, row);
+        r.values(a, v);
     }
 
     __device__ static __forceinline__ void store(const RouteArgs &a, int64_t row, const float *d)
@@ -445,7 +483,7 @@ struct Row {
         for (int q = 0; q < V / 4; ++q) {
             const int e = expert(q * 4);
             const float *x = d + q * 4;
-            if (a.vec) {
+            if constexpr (VEC) {
                 if (e < a.E) {
                     if (L32) *reinterpret_cast<f32x4 *>(static_cast<float *>(a.dl) + base + e) = f32x4{x[0], x[1], x[2], x[3]};
                     else *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.dl) + base + e) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
@@ -481,8 +519,12 @@ struct Row {
     // is infinite its holders have the term 1: an infinity less itself is no number.
     __device__ static __forceinline__ float terms(const float *v, float m, float *t)
     {
+        const float top = m == kMinusInf ? -kMinusInf : m;   // without an expert every term is 0
 #pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = v[i] == kMinusInf ? 0.f : v[i] == m ? 1.f : exp_neg(v[i] - m);
+        for (int i = 0; i < V; ++i) {
+            const float e = exp_neg(v[i] - top);
+            t[i] = v[i] == top ? 1.f : e;
+        }
         return total(t);
     }
 
@@ -491,22 +533,22 @@ struct Row {
     // left: 1 - sigmoid.
     __device__ static __forceinline__ float sigmoids(const float *v, float m, float *t, float *left)
     {
-        const float lift = fminf(m, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float z = exp_neg(-fabsf(v[i])), d = 1.0f / (1.0f + z);
-            t[i] = v[i] == kMinusInf ? 0.f : (v[i] >= 0.f ? 1.f : lift < -40.f ? exp_neg(v[i] - lift) : z) * d;
+            const float z = exp_neg(-fabsf(v[i])), d = inverse(1.0f + z);
+            t[i] = (v[i] >= 0.f ? 1.f : z) * d;   // of minus infinity 0
             left[i] = (v[i] >= 0.f ? z : 1.f) * d;
+        }
+        if (__any(m < -40.f)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float e = exp_neg(v[i] - m);   // 1 - sigmoid is 1 here; of no expert 0
+                t[i] = m < -40.f ? e : t[i];
+            }
         }
         return total(t);
     }
 };
-
-__device__ __forceinline__ double across_max(double v, int lanes)
-{
-    for (int d = 1; d < lanes; d *= 2) v = fmax(v, __shfl_xor(v, d));
-    return v;
-}
 
 // The weights of a token's chosen logits, one a lane and slot (NaN: none), and their
 // relation to the scores: w = scale * weight.
@@ -530,8 +572,8 @@ __device__ __forceinline__ void weights_of(const RouteArgs &a, const float *l, c
         if (!a.sigmoid) {
             w[s] = l[s] == top ? 1.f : exp_neg(l[s] - top);
         } else {
-            const float z = exp_neg(-fabsf(l[s])), lift = fminf(top, 0.f);
-            w[s] = (l[s] >= 0.f ? 1.f : a.renorm ? exp_neg(l[s] - lift) : z) / (1.0f + z);
+            const float z = exp_neg(-fabsf(l[s])), far = exp_neg(l[s] - fminf(top, 0.f));
+            w[s] = (l[s] >= 0.f ? 1.f : a.renorm ? far : z) * inverse(1.0f + z);
         }
         if (!on[s] || l[s] == kMinusInf) w[s] = 0.f;
         t += w[s];
@@ -542,86 +584,186 @@ __device__ __forceinline__ void weights_of(const RouteArgs &a, const float *l, c
     for (int s = 0; s < SLOTS; ++s) w[s] = t > 0.f ? w[s] / t : 0.f;
 }
 
-// One token per LANES lanes: its logits in registers, the largest key taken K times.
-template <bool L32, int LANES, int V>
+// Integers in the order of the floats they stand for (the two zeros are one).
+constexpr int kNoKey = int(0x807FFFFF);   // minus infinity
+__device__ __forceinline__ int key_of(float v)
+{
+    const int b = __builtin_bit_cast(int, v + 0.f);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7FFFFFFF)); }
+
+// A lane's keys in falling order, and the place that each came from, four bits each.  Only
+// neighbours change places, and only where the second is larger: equal keys stay in order.
+template <int V>
+__device__ __forceinline__ uint32_t sort_keys(int *k)
+{
+    int at[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) at[i] = i;
+#pragma unroll
+    for (int r = 0; r < V; ++r) {
+#pragma unroll
+        for (int i = r & 1; i + 1 < V; i += 2) {
+            const int a = k[i], b = k[i + 1];
+            // by differences: a choice between two elements becomes an index that is not
+            // known, and 1000 instructions for the eight
+            const int d = b > a ? at[i] ^ at[i + 1] : 0;
+            k[i] = max(a, b);
+            k[i + 1] = min(a, b);
+            at[i] ^= d;
+            at[i + 1] ^= d;
+        }
+    }
+    uint32_t order = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) order |= uint32_t(at[i]) << (4 * i);
+    return order;
+}
+
+struct Pick {
+    int id, key;
+};
+
+// Orders one wavefront's accesses to LDS: its own lanes read what others of them wrote.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The largest `rounds` of a token's keys, one after another: the lanes' first keys are
+// compared, the one that holds the largest writes it down and goes on to its next; of
+// several, the one with the lowest expert.  Returns whether two keys that follow each
+// other were nearer than `near` allows.
+template <typename R, int LANES, int V, typename Near>
+__device__ __forceinline__ bool take(int *k, int rounds, Pick *picks, Near near)
+{
+    uint32_t order = sort_keys<V>(k);
+    bool close = false;
+    float before = __builtin_inff();
+    const int base = (threadIdx.x & 63) & ~(LANES - 1);
+    for (int r = 0; r < rounds; ++r) {
+        const int m = across<LANES>(k[0], MaxInt()), e = R::expert(order & 7);
+        bool mine = k[0] == m;
+        uint64_t hit = __ballot(mine) >> base;
+        if (LANES < 64) hit &= (uint64_t(1) << (LANES & 63)) - 1;
+        if (__any((hit & (hit - 1)) != 0)) {
+            const int low = across<LANES>(mine ? e : INT32_MAX, MinInt());   // by every lane of the wavefront
+            mine = mine && low == e;
+        }
+        mine = mine && m != kNoKey;
+        if (mine && r < kMaxTopk) picks[r] = Pick{e, m};
+        order = mine ? order >> 4 : order;
+#pragma unroll
+        for (int i = 0; i < V; ++i) k[i] = !mine ? k[i] : i + 1 < V ? k[i + 1] : kNoKey;
+        close = m != kNoKey ? near(before, of_key(m)) || close : close;
+        before = of_key(m);
+    }
+    return close;
+}
+
+// The choice by 64-bit scores, for the tokens whose 32-bit ones are too near to tell.
+template <typename R>
+__device__ __forceinline__ void take_exactly(const RouteArgs &a, int64_t row, Pick *picks)
+{
+    constexpr int V = R::kV, LANES = R::kLanes;
+    float v[V];
+    R::load(a, row, v);   // again, rather than held by all who need none of this
+    const float m = R::largest(v);
+    double key[V], t = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const double x = double(v[i]);
+        if (a.sigmoid) key[i] = 1.0 / (1.0 + exp(-x));
+        else key[i] = v[i] == kMinusInf ? 0.0 : v[i] == m ? 1.0 : exp(x - double(m));
+        t += key[i];
+    }
+    for (int d = 1; d < LANES; d *= 2) t += __shfl_xor(t, d);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = R::expert(i);
+        const double x = (a.sigmoid ? key[i] : key[i] / t) + (e < a.E ? double(a.bias[e]) : 0.0);
+        key[i] = v[i] == kMinusInf || !(x == x) ? -__builtin_inf() : x;
+    }
+    for (int k = 0; k < a.K; ++k) {
+        double top = key[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = key[i] > top ? key[i] : top;
+        for (int d = 1; d < LANES; d *= 2) {
+            const double o = __shfl_xor(top, d);
+            top = o > top ? o : top;
+        }
+        int e = INT32_MAX;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i) e = key[i] == top ? R::expert(i) : e;
+        for (int d = 1; d < LANES; d *= 2) e = min(e, __shfl_xor(e, d));
+        if (R::lane() == 0) picks[k].id = top == -__builtin_inf() ? -1 : e;
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = R::expert(i) == e ? -__builtin_inf() : key[i];
+    }
+}
+
+// One token per LANES lanes, its logits in registers from the load on.  What bounds it is
+// the choice: a round is one reduction over the lanes, so a lane's logits are sorted once
+// and only the first of them takes part.
+template <bool L32, int LANES, int V, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a)
 {
-    using R = Row<L32, LANES, V>;
+    using R = Row<L32, LANES, V, VEC>;
+    __shared__ Pick picked[R::kRows][kMaxTopk];
     const int lane = R::lane();
     const int64_t row_ = int64_t(blockIdx.x) * R::kRows + threadIdx.x / LANES, row = min(row_, int64_t(a.rows - 1));
+    Pick *picks = picked[threadIdx.x / LANES];
     float v[V];
     R::load(a, row, v);
     const bool live = !a.live || a.live[row] != 0;
-    const float m = R::largest(v);
-    float sum = 1.f, l[R::kSlots];
-    int id[R::kSlots];
 #pragma unroll
-    for (int s = 0; s < R::kSlots; ++s) {
-        id[s] = -1;
-        l[s] = kMinusInf;
-    }
-    if (!a.bias) {
-        if (!a.sigmoid && !a.renorm) {
-            float t[V];
-            sum = R::terms(v, m, t);
-        }
-        for (int k = 0; k < a.K; ++k) {
-            const float top = R::largest(v);
-            int e = INT32_MAX;
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i) e = v[i] == top ? R::expert(i) : e;
-            e = across<LANES>(e, Min());
-#pragma unroll
-            for (int s = 0; s < R::kSlots; ++s) {
-                if (k == s * LANES + lane && top != kMinusInf) {
-                    id[s] = e;
-                    l[s] = top;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = R::expert(i) == e ? kMinusInf : v[i];
-        }
-    } else {
-        double key[V], t = 0.0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const double x = double(v[i]);
-            if (a.sigmoid) key[i] = 1.0 / (1.0 + exp(-x));
-            else key[i] = v[i] == kMinusInf ? 0.0 : v[i] == m ? 1.0 : exp(x - double(m));
-            t += key[i];
-        }
-        for (int d = 1; d < LANES; d *= 2) t += __shfl_xor(t, d);
-        sum = float(t);
+    for (int s = 0; s < R::kSlots; ++s)
+        if (s * LANES + lane < kMaxTopk) picks[s * LANES + lane] = Pick{-1, kNoKey};
+    wave_sync();
+    float m = 0.f, sum = 1.f;
+    int key[V];
+    if constexpr (BIAS) {
+        float t[V];
+        m = R::largest(v);
+        if (!a.sigmoid) sum = R::terms(v, m, t);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = R::expert(i);
-            const double b = e < a.E ? double(a.bias[e]) : 0.0, s = a.sigmoid ? key[i] : key[i] / t;
-            const double x = s + b;
-            key[i] = v[i] == kMinusInf || !(x == x) ? -__builtin_inf() : x;
+            const float z = exp_neg(-fabsf(v[i])), x = (a.sigmoid ? (v[i] >= 0.f ? 1.f : z) * inverse(1.0f + z) : t[i] / sum) + (e < a.E ? a.bias[e] : 0.f);
+            key[i] = v[i] == kMinusInf || !(x == x) ? kNoKey : key_of(x);
         }
-        for (int k = 0; k < a.K; ++k) {
-            double top = key[0];
-#pragma unroll
-            for (int i = 1; i < V; ++i) top = fmax(top, key[i]);
-            top = across_max(top, LANES);
-            int e = INT32_MAX;
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i) e = key[i] == top ? R::expert(i) : e;
-            e = across<LANES>(e, Min());
-#pragma unroll
-            for (int s = 0; s < R::kSlots; ++s)
-                if (k == s * LANES + lane && top != -__builtin_inf()) id[s] = e;
-#pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = R::expert(i) == e ? -__builtin_inf() : key[i];
+        // A score is off by less than 32 roundings of 1, and the sum with the bias by one of
+        // its own size: keys that are 128 of both apart are in order.  One round more than
+        // there are places, for the border behind the last.
+        const bool close = take<R, LANES, V>(key, a.K + 1, picks, [](float hi, float lo) {
+            return !(hi - lo > 0x1p-17f * (1.f + fabsf(lo)));
+        });
+        if (__any(close)) take_exactly<R>(a, row, picks);
+    } else {
+        if (!a.sigmoid && !a.renorm) {
+            float t[V];
+            m = R::largest(v);
+            sum = R::terms(v, m, t);
         }
 #pragma unroll
-        for (int s = 0; s < R::kSlots; ++s)
-            if (id[s] >= 0) l[s] = R::one(a, row * a.ls + id[s]);
+        for (int i = 0; i < V; ++i) key[i] = key_of(v[i]);
+        take<R, LANES, V>(key, a.K, picks, [](float, float) { return false; });
     }
+    wave_sync();
     bool on[R::kSlots];
-    float w[R::kSlots];
+    float w[R::kSlots], l[R::kSlots];
+    int id[R::kSlots];
 #pragma unroll
-    for (int s = 0; s < R::kSlots; ++s) on[s] = id[s] >= 0;
+    for (int s = 0; s < R::kSlots; ++s) {
+        const int k = s * LANES + lane;
+        const Pick p = k < a.K ? picks[k] : Pick{-1, kNoKey};
+        id[s] = p.id;
+        on[s] = p.id >= 0;
+        if (BIAS) l[s] = on[s] ? R::one(a, row * a.ls + p.id) : kMinusInf;
+        else l[s] = of_key(p.key);
+    }
     weights_of<LANES, R::kSlots>(a, l, on, m, sum, w);
 #pragma unroll
     for (int s = 0; s < R::kSlots; ++s) {
@@ -633,23 +775,27 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
     }
 }
 
-template <bool L32, int LANES, int V>
+// Slot k's value in every lane of its token.
+template <int LANES, typename T>
+__device__ __forceinline__ T slot(T v, int k)
+{
+    if constexpr (LANES == 64) return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), k));
+    return __shfl(v, k % LANES, LANES);
+}
+
+template <bool L32, int LANES, int V, bool VEC>
 __global__ __launch_bounds__(256) void k_route_grad(RouteArgs a)
 {
-    using R = Row<L32, LANES, V>;
+    using R = Row<L32, LANES, V, VEC>;
+    __shared__ float spread[R::kRows][LANES * V];
     const int lane = R::lane();
     const int64_t row_ = int64_t(blockIdx.x) * R::kRows + threadIdx.x / LANES, row = min(row_, int64_t(a.rows - 1));
+    float *to = spread[threadIdx.x / LANES];
     const bool dense = !a.sigmoid && !a.renorm;   // every logit of the softmax's sum has a gradient
-    float m = 0.f, sum = 1.f, p[V];
-    if (dense) {
-        float v[V];
-        R::load(a, row, v);
-        m = R::largest(v);
-        sum = R::terms(v, m, p);
-    }
-    float l[R::kSlots], g[R::kSlots], w[R::kSlots], dot = 0.f;
+    float l[R::kSlots], g[R::kSlots], w[R::kSlots], dot = 0.f, v[V];
     int id[R::kSlots];
     bool on[R::kSlots];
+    if (dense) R::load(a, row, v);
 #pragma unroll
     for (int s = 0; s < R::kSlots; ++s) {
         const int k = s * LANES + lane;
@@ -659,159 +805,227 @@ __global__ __launch_bounds__(256) void k_route_grad(RouteArgs a)
         const float x = on[s] ? R::one(a, row * a.ls + id[s]) : kMinusInf;
         l[s] = x == x ? x : kMinusInf;
     }
+    float m = 0.f, sum = 1.f, p[V];
+    if (dense) {
+        m = R::largest(v);
+        sum = R::terms(v, m, p);
+    }
     weights_of<LANES, R::kSlots>(a, l, on, m, sum, w);
 #pragma unroll
     for (int s = 0; s < R::kSlots; ++s) dot += w[s] > 0.f ? g[s] * w[s] : 0.f;
     dot = across<LANES>(dot, Sum());
-    float c[R::kSlots];   // what a slot adds to its expert's gradient
+    float c[R::kSlots], all[R::kSlots];   // what a slot adds to its expert's gradient, and every slot of that expert
 #pragma unroll
     for (int s = 0; s < R::kSlots; ++s) {
-        const float z = exp_neg(-fabsf(l[s])), left = (l[s] >= 0.f ? z : 1.f) / (1.0f + z);
-        c[s] = w[s] * (a.renorm ? g[s] - dot : g[s]) * (a.sigmoid ? left : 1.f);
-        if (!(w[s] > 0.f)) c[s] = 0.f;
-    }
-    float d[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = dense ? -(p[i] / sum) * dot : 0.f;
-    if (dense && !(sum > 0.f)) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = 0.f;
+        const float z = exp_neg(-fabsf(l[s])), left = (l[s] >= 0.f ? z : 1.f) * inverse(1.0f + z);
+        c[s] = w[s] > 0.f ? w[s] * (a.renorm ? g[s] - dot : g[s]) * (a.sigmoid ? left : 1.f) : 0.f;
+        all[s] = 0.f;
+        if (!on[s]) id[s] = -1;
     }
     for (int k = 0; k < a.K; ++k) {
-        int e = -1;
+        int e = 0;
         float x = 0.f;
 #pragma unroll
         for (int s = 0; s < R::kSlots; ++s) {
             if (k / LANES != s) continue;
-            e = __shfl(on[s] ? id[s] : -1, k % LANES, LANES);
-            x = __shfl(c[s], k % LANES, LANES);
+            e = slot<LANES>(id[s], k);
+            x = slot<LANES>(c[s], k);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] += R::expert(i) == e ? x : 0.f;
+        for (int s = 0; s < R::kSlots; ++s) all[s] += id[s] == e ? x : 0.f;
     }
+    // to the experts' lanes through LDS; slots of one expert write the same sum
+#pragma unroll
+    for (int i = 0; i < V; ++i) to[R::expert(i)] = 0.f;
+    wave_sync();
+#pragma unroll
+    for (int s = 0; s < R::kSlots; ++s)
+        if (on[s]) to[id[s]] = all[s];
+    wave_sync();
+    const float part = dense && sum > 0.f ? -dot / sum : 0.f;
+    float d[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = to[R::expert(i)] + (dense ? p[i] * part : 0.f);
     if (row_ < a.rows) R::store(a, row, d);
 }
 
 // ------------------------------------------------------------ balance loss ----
 
-// A token's shares, whether it counts, and with LEFT the factor 1 - sigmoid.
-template <typename R, int LANES, int V>
-__device__ __forceinline__ bool shares(const RouteArgs &a, int64_t row, bool in, float *p, float *left, int32_t *hist)
-{
-    float v[V];
-    R::load(a, row, v);
-    int none = 1;
+// What a token's shares come from, on its way.
+template <typename R>
+struct Token {
+    typename R::Raw l;
+    int32_t id[R::kSlots];
+    __device__ __forceinline__ void load(const RouteArgs &a, int64_t row)
+    {
+        l.load(a, row);
 #pragma unroll
-    for (int s = 0; s < R::kSlots; ++s) {
-        const int k = s * LANES + R::lane();
-        const int id = k < a.K ? a.ids[row * a.K + k] : -1;
-        if (in && id >= 0 && id < a.E) {
-            none = 0;
-            if (hist) atomicAdd(hist + id, 1);
+        for (int s = 0; s < R::kSlots; ++s) {
+            const int k = s * R::kLanes + R::lane();
+            id[s] = k < a.K ? a.ids[row * a.K + k] : -1;
         }
     }
-    const bool on = across<LANES>(none, Min()) == 0;
+};
+
+// A token's shares (0 where it does not count), with sigmoids the factors 1 - sigmoid, and
+// whether it counts.  chosen: the lane's choices.
+template <typename R>
+__device__ __forceinline__ bool shares(const RouteArgs &a, const Token<R> &t, bool in, float *p, float *left, int32_t *hist,
+                                       int &chosen)
+{
+    bool any = false;
+#pragma unroll
+    for (int s = 0; s < R::kSlots; ++s) {
+        if (in && t.id[s] >= 0 && t.id[s] < a.E) {
+            any = true;
+            ++chosen;
+            if (hist) atomicAdd(hist + t.id[s], 1);
+        }
+    }
+    const uint64_t who = __ballot(any) >> ((threadIdx.x & 63) & ~(R::kLanes - 1));
+    const bool on = R::kLanes == 64 ? who != 0 : (who & ((uint64_t(1) << (R::kLanes & 63)) - 1)) != 0;
+    float v[R::kV];
+    t.l.values(a, v);
     const float m = R::largest(v), sum = a.sigmoid ? R::sigmoids(v, m, p, left) : R::terms(v, m, p);
     const float inv = on && sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] *= inv;
+    for (int i = 0; i < R::kV; ++i) p[i] *= inv;
     return on;
 }
 
 struct BalanceArgs {
     RouteArgs r;
     float *share;
-    int32_t *count, *tokens;
+    int32_t *count, *totals;
+    uint32_t *done;
 };
 
-template <bool L32, int LANES, int V>
-__global__ __launch_bounds__(256) void k_balance(BalanceArgs b)
+// Sums of the shares over tokens in registers, counts in LDS; a token's logits and ids are
+// on their way while the one before is worked on.
+template <bool L32, int LANES, int V, bool VEC, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_balance(BalanceArgs b)
 {
-    using R = Row<L32, LANES, V>;
+    using R = Row<L32, LANES, V, VEC>;
+    constexpr int kRows = THREADS / LANES;
     const RouteArgs &a = b.r;
-    __shared__ int32_t hist[LANES * V], live;
-    __shared__ float join[R::kRows][LANES * V];
-    for (int e = threadIdx.x; e < LANES * V; e += 256) hist[e] = 0;
-    if (threadIdx.x == 0) live = 0;
+    __shared__ int32_t hist[LANES * V], total[2];
+    __shared__ float join[kRows][LANES * V];
+    for (int e = threadIdx.x; e < LANES * V; e += THREADS) hist[e] = 0;
+    if (threadIdx.x < 2) total[threadIdx.x] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *b.done = 0;   // for the launch behind this one
     __syncthreads();
     float acc[V] = {};
-    int mine = 0;
-    for (int64_t at = int64_t(blockIdx.x) * R::kRows; at < a.rows; at += int64_t(gridDim.x) * R::kRows) {
-        const int64_t row = at + threadIdx.x / LANES;
+    int tokens = 0, chosen = 0;
+    const int64_t last = a.rows - 1, step = int64_t(gridDim.x) * kRows;
+    int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / LANES;
+    Token<R> next;
+    next.load(a, min(row, last));
+    for (int64_t at = int64_t(blockIdx.x) * kRows; at < a.rows; at += step, row += step) {
+        const Token<R> t = next;
+        if (at + step < a.rows) next.load(a, min(row + step, last));
         float p[V], left[V];
-        mine += shares<R, LANES, V>(a, min(row, int64_t(a.rows - 1)), row < a.rows, p, left, hist);
+        tokens += shares<R>(a, t, row <= last, p, left, hist, chosen);
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] += p[i];
     }
-    if (R::lane() == 0) atomicAdd(&live, mine);
+    if (R::lane() == 0) atomicAdd(&total[0], tokens);
+    atomicAdd(&total[1], chosen);
 #pragma unroll
     for (int i = 0; i < V; ++i) join[threadIdx.x / LANES][R::expert(i)] = acc[i];
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 256) {
+    for (int e = threadIdx.x; e < a.E; e += THREADS) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < R::kRows; ++i) s += join[i][e];
+        for (int i = 0; i < kRows; ++i) s += join[i][e];
         b.share[int64_t(blockIdx.x) * a.E + e] = s;
         b.count[int64_t(blockIdx.x) * a.E + e] = hist[e];
     }
-    if (threadIdx.x == 0) b.tokens[blockIdx.x] = live;
+    if (threadIdx.x < 2) b.totals[blockIdx.x * 2 + threadIdx.x] = total[threadIdx.x];
 }
 
 struct BalanceJoinArgs {
     const float *share;
-    const int32_t *count, *tokens;
+    const int32_t *count, *totals;
+    double *part;
+    uint32_t *done;
     float *loss, *slope;
     int32_t *counts;
     int E, groups;
     float coefficient;
 };
 
-// One workgroup: every expert's sums, then the loss.
-__global__ __launch_bounds__(1024) void k_balance_join(BalanceJoinArgs a)
+// Sixteen experts a workgroup, sixteen threads for each; the workgroup that is done last
+// adds the parts of the loss, in their order.
+__global__ __launch_bounds__(256) void k_balance_join(BalanceJoinArgs a)
 {
-    __shared__ double part[16];
-    __shared__ int all[2];
-    if (threadIdx.x < 2) all[threadIdx.x] = 0;
+    __shared__ double share[16][16];
+    __shared__ int count[16][16], total[2];
+    const int col = threadIdx.x % 16, slice = threadIdx.x / 16, e = blockIdx.x * 16 + col;
+    if (threadIdx.x < 2) total[threadIdx.x] = 0;
     __syncthreads();
-    double share = 0.0;
-    int count = 0, tokens = 0;
-    const int e = threadIdx.x;
-    if (e < a.E) {
-        for (int g = 0; g < a.groups; ++g) {
-            share += double(a.share[int64_t(g) * a.E + e]);
-            count += a.count[int64_t(g) * a.E + e];
+    double s = 0.0;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kBalanceGroups / 16; ++i) {
+        const int g = i * 16 + slice;
+        if (g < a.groups && e < a.E) {
+            s += double(a.share[int64_t(g) * a.E + e]);
+            c += a.count[int64_t(g) * a.E + e];
         }
-        a.counts[e] = count;
-        atomicAdd(&all[0], count);
     }
-    for (int g = threadIdx.x; g < a.groups; g += 1024) tokens += a.tokens[g];
-    atomicAdd(&all[1], tokens);
+    static_assert(kBalanceGroups <= 256, "a thread for every group's totals");
+    if (int(threadIdx.x) < a.groups) {
+        atomicAdd(&total[0], a.totals[threadIdx.x * 2]);
+        atomicAdd(&total[1], a.totals[threadIdx.x * 2 + 1]);
+    }
+    share[slice][col] = s;
+    count[slice][col] = c;
     __syncthreads();
-    const double n = double(all[0]) * double(all[1]);
-    float slope = 0.f;
+    if (threadIdx.x >= 16) return;
+    s = 0.0;
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        s += share[i][col];
+        c += count[i][col];
+    }
+    const double n = double(total[0]) * double(total[1]);
+    const float slope = n > 0.0 ? float(double(a.coefficient) * double(a.E) * double(c) / n) : 0.f;
     if (e < a.E) {
-        slope = n > 0.0 ? float(double(a.coefficient) * double(a.E) * double(count) / n) : 0.f;
+        a.counts[e] = c;
         a.slope[e] = slope;
     }
-    double loss = double(slope) * share;
-    for (int d = 1; d < kWave; d *= 2) loss += __shfl_xor(loss, d);
-    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = loss;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        loss = 0.0;
-        for (int i = 0; i < 16; ++i) loss += part[i];
-        a.loss[0] = float(loss);
+    double loss = e < a.E ? double(slope) * s : 0.0;
+    for (int d = 1; d < 16; d *= 2) loss += __shfl_xor(loss, d);
+    if (threadIdx.x != 0) return;
+    __hip_atomic_store(a.part + blockIdx.x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) != gridDim.x - 1) return;
+    loss = 0.0;
+    for (unsigned i = 0; i < gridDim.x; ++i) loss += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.loss[0] = float(loss);
+}
+
+// No tokens.
+__global__ __launch_bounds__(kMaxExperts) void k_balance_none(float *loss, float *slope, int32_t *counts, int E)
+{
+    if (threadIdx.x == 0) loss[0] = 0.f;
+    if (int(threadIdx.x) < E) {
+        slope[threadIdx.x] = 0.f;
+        counts[threadIdx.x] = 0;
     }
 }
 
-template <bool L32, int LANES, int V>
+template <bool L32, int LANES, int V, bool VEC>
 __global__ __launch_bounds__(256) void k_balance_grad(RouteArgs a)
 {
-    using R = Row<L32, LANES, V>;
+    using R = Row<L32, LANES, V, VEC>;
     const int64_t row_ = int64_t(blockIdx.x) * R::kRows + threadIdx.x / LANES, row = min(row_, int64_t(a.rows - 1));
     float p[V], left[V], d[V], dot = 0.f;
     const float g = a.g[0];
-    const bool on = shares<R, LANES, V>(a, row, true, p, left, nullptr);
+    Token<R> t;
+    t.load(a, row);
+    int chosen = 0;
+    const bool on = shares<R>(a, t, true, p, left, nullptr, chosen);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = R::expert(i);
@@ -896,57 +1110,68 @@ RouteArgs route_args(const RoutePlan &p)
     a.scale = p.scale;
     a.sigmoid = p.sigmoid;
     a.renorm = p.renorm;
-    const uintptr_t each = p.l32 ? 16 : 8;   // four logits at a time
-    a.vec = p.E % 4 == 0 && p.ls % 4 == 0 && reinterpret_cast<uintptr_t>(p.l) % each == 0 &&
-            reinterpret_cast<uintptr_t>(p.dl) % each == 0;
     return a;
 }
 
 // The lanes of a token: 16 with four or eight logits each, then 32 and 64 with eight.
-template <template <bool, int, int> class Launch, typename... Args>
-int by_experts(int E, bool l32, Args... args)
+template <template <bool, int, int, bool> class Launch, bool L32, bool VEC, typename... Args>
+int by_experts(int E, Args... args)
 {
-    if (E <= 64) return l32 ? Launch<true, 16, 4>::run(args...) : Launch<false, 16, 4>::run(args...);
-    if (E <= 128) return l32 ? Launch<true, 16, 8>::run(args...) : Launch<false, 16, 8>::run(args...);
-    if (E <= 256) return l32 ? Launch<true, 32, 8>::run(args...) : Launch<false, 32, 8>::run(args...);
-    return l32 ? Launch<true, 64, 8>::run(args...) : Launch<false, 64, 8>::run(args...);
+    if (E <= 64) return Launch<L32, 16, 4, VEC>::run(args...);
+    if (E <= 128) return Launch<L32, 16, 8, VEC>::run(args...);
+    if (E <= 256) return Launch<L32, 32, 8, VEC>::run(args...);
+    return Launch<L32, 64, 8, VEC>::run(args...);
 }
 
-template <bool L32, int LANES, int V>
+template <template <bool, int, int, bool> class Launch, typename... Args>
+int by_logits(const RoutePlan &p, Args... args)
+{
+    // four logits at a time, where they and their gradients lie for it
+    const uintptr_t each = p.l32 ? 16 : 8;
+    const bool vec = p.E % 4 == 0 && p.ls % 4 == 0 && reinterpret_cast<uintptr_t>(p.l) % each == 0 &&
+                     reinterpret_cast<uintptr_t>(p.dl) % each == 0;
+    if (p.l32) return vec ? by_experts<Launch, true, true>(p.E, args...) : by_experts<Launch, true, false>(p.E, args...);
+    return vec ? by_experts<Launch, false, true>(p.E, args...) : by_experts<Launch, false, false>(p.E, args...);
+}
+
+template <bool L32, int LANES, int V, bool VEC>
 struct RouteLaunch {
     static int run(const RouteArgs &a, hipStream_t st)
     {
-        constexpr int rows = Row<L32, LANES, V>::kRows;
-        hipLaunchKernelGGL((k_route<L32, LANES, V>), dim3(unsigned((a.rows + rows - 1) / rows)), dim3(256), 0, st, a);
+        constexpr int rows = Row<L32, LANES, V, VEC>::kRows;
+        const dim3 grid(unsigned((a.rows + rows - 1) / rows));
+        if (a.bias) hipLaunchKernelGGL((k_route<L32, LANES, V, VEC, true>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_route<L32, LANES, V, VEC, false>), grid, dim3(256), 0, st, a);
         return launched();
     }
 };
 
-template <bool L32, int LANES, int V>
+template <bool L32, int LANES, int V, bool VEC>
 struct RouteGradLaunch {
     static int run(const RouteArgs &a, hipStream_t st)
     {
-        constexpr int rows = Row<L32, LANES, V>::kRows;
-        hipLaunchKernelGGL((k_route_grad<L32, LANES, V>), dim3(unsigned((a.rows + rows - 1) / rows)), dim3(256), 0, st, a);
+        constexpr int rows = Row<L32, LANES, V, VEC>::kRows;
+        hipLaunchKernelGGL((k_route_grad<L32, LANES, V, VEC>), dim3(unsigned((a.rows + rows - 1) / rows)), dim3(256), 0, st, a);
         return launched();
     }
 };
 
-template <bool L32, int LANES, int V>
+template <bool L32, int LANES, int V, bool VEC>
 struct BalanceLaunch {
-    static int run(const BalanceArgs &a, int groups, hipStream_t st)
+    static int run(const BalanceArgs &a, int groups, bool wide, hipStream_t st)
     {
-        hipLaunchKernelGGL((k_balance<L32, LANES, V>), dim3(unsigned(groups)), dim3(256), 0, st, a);
+        if (wide) hipLaunchKernelGGL((k_balance<L32, LANES, V, VEC, 1024>), dim3(unsigned(groups)), dim3(1024), 0, st, a);
+        else hipLaunchKernelGGL((k_balance<L32, LANES, V, VEC, 256>), dim3(unsigned(groups)), dim3(256), 0, st, a);
         return launched();
     }
 };
 
-template <bool L32, int LANES, int V>
+template <bool L32, int LANES, int V, bool VEC>
 struct BalanceGradLaunch {
     static int run(const RouteArgs &a, hipStream_t st)
     {
-        constexpr int rows = Row<L32, LANES, V>::kRows;
-        hipLaunchKernelGGL((k_balance_grad<L32, LANES, V>), dim3(unsigned((a.rows + rows - 1) / rows)), dim3(256), 0, st, a);
+        constexpr int rows = Row<L32, LANES, V, VEC>::kRows;
+        hipLaunchKernelGGL((k_balance_grad<L32, LANES, V, VEC>), dim3(unsigned((a.rows + rows - 1) / rows)), dim3(256), 0, st, a);
         return launched();
     }
 };
@@ -971,36 +1196,38 @@ int be_launch_norm_grad(const NormGradPlan &p, void *stream)
         if (rc != 0) return rc;
     }
     if (!p.dw) return 0;
-    hipLaunchKernelGGL(k_norm_grad_join, dim3(unsigned((p.H + kWave - 1) / kWave)), dim3(1024), 0, st, p.part, p.dw, p.H, p.groups);
+    hipLaunchKernelGGL(k_norm_grad_join, dim3(unsigned((p.H + 63) / 64)), dim3(1024), 0, st, p.part, p.dw, p.H, p.groups);
     return launched();
 }
 
 int be_launch_route(const RoutePlan &p, void *stream)
 {
-    return by_experts<RouteLaunch>(p.E, p.l32, route_args(p), static_cast<hipStream_t>(stream));
+    return by_logits<RouteLaunch>(p, route_args(p), static_cast<hipStream_t>(stream));
 }
 
 int be_launch_route_grad(const RoutePlan &p, void *stream)
 {
-    return by_experts<RouteGradLaunch>(p.E, p.l32, route_args(p), static_cast<hipStream_t>(stream));
+    return by_logits<RouteGradLaunch>(p, route_args(p), static_cast<hipStream_t>(stream));
 }
 
 int be_launch_balance(const BalancePlan &p, void *stream)
 {
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (p.groups > 0) {
-        BalanceArgs a{route_args(p.r), p.share, p.count, p.tokens};
-        const int rc = by_experts<BalanceLaunch>(p.r.E, p.r.l32, a, p.groups, st);
-        if (rc != 0) return rc;
+    if (p.groups == 0) {
+        hipLaunchKernelGGL(k_balance_none, dim3(1), dim3(kMaxExperts), 0, st, p.loss, p.slope, p.counts, p.r.E);
+        return launched();
     }
-    BalanceJoinArgs j{p.share, p.count, p.tokens, p.loss, p.slope, p.counts, p.r.E, p.groups, p.coefficient};
-    hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(1024), 0, st, j);
+    BalanceArgs a{route_args(p.r), p.share, p.count, p.totals, p.done};
+    const int rc = by_logits<BalanceLaunch>(p.r, a, p.groups, p.wide, st);
+    if (rc != 0) return rc;
+    BalanceJoinArgs j{p.share, p.count, p.totals, p.part, p.done, p.loss, p.slope, p.counts, p.r.E, p.groups, p.coefficient};
+    hipLaunchKernelGGL(k_balance_join, dim3(unsigned((p.r.E + 15) / 16)), dim3(256), 0, st, j);
     return launched();
 }
 
 int be_launch_balance_grad(const RoutePlan &p, void *stream)
 {
-    return by_experts<BalanceGradLaunch>(p.E, p.l32, route_args(p), static_cast<hipStream_t>(stream));
+    return by_logits<BalanceGradLaunch>(p, route_args(p), static_cast<hipStream_t>(stream));
 }
 
 }  // namespace afd

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -46,7 +47,11 @@ def _asks(*tensors):
         for t in tensors:
             if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
                 raise ValueError("the source's calls have no forward gradients: pass the primal of a dual tensor")
-    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def _plain(call, *tensors):
@@ -67,6 +72,30 @@ def _recorded(call, device, *given):
                                  f"{call}_grad for the gradient")
 
 
+def _launch(device, call, *args):
+    """A call of the library on the device and its current stream."""
+    if device.index == torch._C._cuda_getDevice():
+        return call(*args, raw_stream(device))
+    with on_device(device):
+        return call(*args, raw_stream(device))
+
+
+def _layout(t):
+    """What the checks of a tensor look at, but for its address."""
+    return None if t is None else (t.dtype, t.shape, t.stride(), t.device)
+
+
+_CHECKED = 1024      # layouts of arguments that the calls keep as checked
+_norms, _norm_grads, _routes, _balances = {}, {}, {}, {}
+
+
+def _keep(plans, key, plan):
+    if len(plans) >= _CHECKED:
+        plans.clear()
+    plans[key] = plan
+    return plan
+
+
 def _rows(t, what, device=None):
     """[rows, columns] with its columns next to each other; returns the row stride."""
     if t.dim() != 2 or t.device.type != "cuda" or device is not None and t.device != device or \
@@ -81,9 +110,16 @@ def _rows(t, what, device=None):
 def _wide_rows(t, what, device=None):
     """_rows for a norm: 16-byte pieces."""
     stride = _rows(t, what, device)
-    if t.numel() and (t.data_ptr() % 16 or stride % 8):
-        raise ValueError(f"{what} must be 16-byte aligned with a row stride in multiples of 8, got {stride} elements")
+    if t.numel() and stride % 8:
+        raise ValueError(f"{what} must have a row stride in multiples of 8, got {stride} elements")
     return stride
+
+
+def _aligned(t, what):
+    p = t.data_ptr()
+    if p % 16:
+        raise ValueError(f"{what} must be 16-byte aligned")
+    return p
 
 
 def _want(t, what, dtype, shape, device):
@@ -110,53 +146,57 @@ def _norm_config(hidden, x, residual, weight, out, eps):
     return nat.NormConfig(hidden, x, residual, weight, out, eps)
 
 
-def _normed_checked(x, weight, residual, eps, dtype):
-    """(configuration, strides) of a norm whose inputs are checked."""
+def _norm_plan(x, weight, residual, eps, dtype, out, out_scales, residual_out):
+    """(configuration, strides of x, residual and residual_out) of a norm whose arguments' layouts fit."""
     xs = _wide_rows(x, "x")
-    T, H = x.shape
-    rs, rc = 0, nat.NO_RESIDUAL
+    (T, H), dev = x.shape, x.device
+    rs, hs, rc = 0, H, nat.NO_RESIDUAL
     if residual is not None:
         if residual.shape != x.shape:
             raise ValueError(f"residual must be {list(x.shape)} like x, got {list(residual.shape)}")
-        rs, rc = _wide_rows(residual, "residual", x.device), _code(residual, "residual")
+        rs, rc = _wide_rows(residual, "residual", dev), _code(residual, "residual")
     if dtype is not torch.bfloat16 and dtype is not torch.float8_e4m3fn:
         raise TypeError(f"dtype must be bfloat16 or float8_e4m3fn, got {dtype}")
-    if weight.data_ptr() % 16:
-        raise ValueError("weight must be 16-byte aligned")
-    _want(weight, "weight", weight.dtype, (H,), x.device)
+    _want(weight, "weight", weight.dtype, (H,), dev)
     cfg = _norm_config(H, _code(x, "x"), rc, _code(weight, "weight"),
                        nat.AFD_BF16 if dtype is torch.bfloat16 else nat.AFD_FP8_E4M3, float(eps))
-    return cfg, xs, rs
+    if out is not None:
+        _want(out, "out", dtype, (T, H), dev)
+    if out_scales is not None:
+        if dtype is torch.bfloat16:
+            raise ValueError("out_scales belong to float8_e4m3fn rows")
+        _want(out_scales, "out_scales", torch.float32, (T, H // SCALE_BLOCK), dev)
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out without a residual")
+        if residual_out.dtype is not residual.dtype or residual_out.shape != residual.shape:
+            raise ValueError(f"residual_out must be {residual.dtype} {list(residual.shape)} like residual")
+        hs = _wide_rows(residual_out, "residual_out", dev)
+    return cfg, xs, rs, hs
 
 
 def _norm(x, weight, residual, eps, dtype, out, out_scales, residual_out, keep_rstd):
-    cfg, xs, rs = _normed_checked(x, weight, residual, eps, dtype)
-    T, H = x.shape
-    dev, fp8 = x.device, dtype is torch.float8_e4m3fn
+    key = (x.dtype, x.shape, x.stride(), x.device, weight.dtype, weight.shape, weight.stride(), weight.device,
+           _layout(residual), eps, dtype, _layout(out), _layout(out_scales), _layout(residual_out))
+    plan = _norms.get(key) or _keep(_norms, key, _norm_plan(x, weight, residual, eps, dtype, out, out_scales, residual_out))
+    cfg, xs, rs, hs = plan
+    (T, H), dev = x.shape, x.device
     if out is None:
         out = torch.empty((T, H), dtype=dtype, device=dev)
-    po = _want(out, "out", dtype, (T, H), dev)
     ps = pr = ph = None
-    hs = 0
-    if fp8:
+    if dtype is torch.float8_e4m3fn:
         if out_scales is None:
             out_scales = torch.empty((T, H // SCALE_BLOCK), dtype=torch.float32, device=dev)
-        ps = _want(out_scales, "out_scales", torch.float32, (T, H // SCALE_BLOCK), dev)
-    elif out_scales is not None:
-        raise ValueError("out_scales belong to float8_e4m3fn rows")
+        ps = out_scales.data_ptr()
     if residual is not None:
         if residual_out is None:
             residual_out = torch.empty((T, H), dtype=residual.dtype, device=dev)
-        elif residual_out.dtype is not residual.dtype or residual_out.shape != residual.shape:
-            raise ValueError(f"residual_out must be {residual.dtype} {list(residual.shape)} like residual")
-        hs, pr, ph = _wide_rows(residual_out, "residual_out", dev), residual.data_ptr(), residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
+        pr, ph = _aligned(residual, "residual"), _aligned(residual_out, "residual_out")
     rstd = torch.empty(T, dtype=torch.float32, device=dev) if keep_rstd else None
-    with on_device(dev):
-        st = nat.load().afd_norm(cfg, T, x.data_ptr(), xs, pr, rs, weight.data_ptr(), po, ps, ph, hs,
-                                 rstd.data_ptr() if keep_rstd else None, raw_stream(dev))
-    nat.check(st, "rms_norm")
+    st = _launch(dev, nat.load().afd_norm, cfg, T, _aligned(x, "x"), xs, pr, rs, _aligned(weight, "weight"),
+                 _aligned(out, "out"), ps, ph, hs, rstd.data_ptr() if keep_rstd else None)
+    if st:
+        nat.check(st, "rms_norm")
     return Normed(out, out_scales, residual_out, rstd)
 
 
@@ -230,39 +270,39 @@ def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight
     type, is the gradient of x and of the residual alike; out may be grad_residual, or a
     grad of h's type.  dweight is float32 [H], None without weight_grad."""
     _plain("rms_norm_grad", grad, h, weight, rstd, grad_residual, out)
-    hs = _wide_rows(h, "h")
-    T, H = h.shape
-    dev, lib = h.device, nat.load()
-    if weight.data_ptr() % 16:
-        raise ValueError("weight must be 16-byte aligned")
-    pw, pg = _want(weight, "weight", weight.dtype, (H,), dev), _want(grad, "grad", torch.bfloat16, (T, H), dev)
-    pr = None if grad_residual is None else _want(grad_residual, "grad_residual", h.dtype, (T, H), dev)
-    ps = _want(rstd, "rstd", torch.float32, (T,), dev)
-    cfg = _norm_config(H, _code(h, "h"), nat.NO_RESIDUAL, _code(weight, "weight"), nat.AFD_BF16, 1.0)
+    key = (h.dtype, h.shape, h.stride(), h.device, weight.dtype, weight.shape, weight.stride(), weight.device,
+           _layout(grad), _layout(grad_residual), _layout(rstd), _layout(out))
+    plan = _norm_grads.get(key) or _keep(_norm_grads, key, _norm_grad_plan(grad, h, weight, rstd, grad_residual, out))
+    cfg, hs, need = plan
+    (T, H), dev = h.shape, h.device
     if out is None:
         out = torch.empty((T, H), dtype=h.dtype, device=dev)
-    po = _want(out, "out", h.dtype, (T, H), dev)
-    for what, t in (("grad", grad), ("grad_residual", grad_residual), ("out", out)):
-        if t is not None and t.data_ptr() % 16:
-            raise ValueError(f"{what} must be 16-byte aligned")
-    dw = ws = None
-    need = 0
+    dw = ws = pd = pw = None
     if weight_grad:
-        need = _norm_grad_need(H, T)
-        dw = torch.empty(H, dtype=torch.float32, device=dev)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    with on_device(dev):
-        st = lib.afd_norm_grad(cfg, T, pg, pr, h.data_ptr(), hs, pw, ps, po, dw.data_ptr() if weight_grad else None,
-                               ws.data_ptr() if need else None, need, raw_stream(dev))
-    nat.check(st, "rms_norm_grad")
+        dw, ws = torch.empty(H, dtype=torch.float32, device=dev), torch.empty(need, dtype=torch.uint8, device=dev)
+        pd, pw = dw.data_ptr(), ws.data_ptr()
+    st = _launch(dev, nat.load().afd_norm_grad, cfg, T, _aligned(grad, "grad"),
+                 None if grad_residual is None else _aligned(grad_residual, "grad_residual"), _aligned(h, "h"), hs,
+                 _aligned(weight, "weight"), rstd.data_ptr(), _aligned(out, "out"), pd, pw, need if weight_grad else 0)
+    if st:
+        nat.check(st, "rms_norm_grad")
     return out, dw
 
 
-@functools.lru_cache(maxsize=256)
-def _norm_grad_need(hidden, rows):
-    c, ws = _norm_config(hidden, nat.AFD_BF16, nat.NO_RESIDUAL, nat.AFD_BF16, nat.AFD_BF16, 1.0), ctypes.c_size_t(0)
-    nat.check(nat.load().afd_norm_grad_query(ctypes.byref(c), rows, ctypes.byref(ws)), "rms_norm_grad")
-    return ws.value
+def _norm_grad_plan(grad, h, weight, rstd, grad_residual, out):
+    """(configuration, row stride of h, workspace bytes) of a norm's gradient whose arguments' layouts fit."""
+    hs = _wide_rows(h, "h")
+    (T, H), dev = h.shape, h.device
+    _want(weight, "weight", weight.dtype, (H,), dev)
+    _want(grad, "grad", torch.bfloat16, (T, H), dev)
+    if grad_residual is not None:
+        _want(grad_residual, "grad_residual", h.dtype, (T, H), dev)
+    _want(rstd, "rstd", torch.float32, (T,), dev)
+    if out is not None:
+        _want(out, "out", h.dtype, (T, H), dev)
+    cfg, ws = _norm_config(H, _code(h, "h"), nat.NO_RESIDUAL, _code(weight, "weight"), nat.AFD_BF16, 1.0), ctypes.c_size_t(0)
+    nat.check(nat.load().afd_norm_grad_query(ctypes.byref(cfg), T, ctypes.byref(ws)), "rms_norm_grad")
+    return cfg, hs, ws.value
 
 
 @functools.lru_cache(maxsize=256)
@@ -278,29 +318,45 @@ def _route_config(experts, topk, code, scoring, renormalize, scale):
     return nat.RouteConfig(experts, topk, code, nat.SCORINGS[scoring], int(renormalize), scale)
 
 
-def _topk_of(t, what, logits, dtype):
-    """The checked pointer of [T, topk] beside the logits."""
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be [T, topk], got {list(t.shape)}")
-    return _want(t, what, dtype, (logits.shape[0], t.shape[1]), logits.device)
+def _ids_of(ids, logits):
+    """ids [T, topk] beside the logits."""
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be [T, topk], got {list(ids.shape)}")
+    _want(ids, "ids", torch.int32, (logits.shape[0], ids.shape[1]), logits.device)
+    return ids.shape[1]
+
+
+def _route_plan(logits, topk, scoring, bias, renormalize, scale, live, ids, weights):
+    """(configuration, row stride) of a choice whose arguments' layouts fit."""
+    ls = _rows(logits, "logits")
+    (T, E), dev = logits.shape, logits.device
+    cfg = _route_config(E, operator.index(topk), _code(logits, "logits"), scoring, bool(renormalize), float(scale))
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,), dev)
+    if live is not None:
+        _want(live, "live", torch.bool, (T,), dev)
+    if ids is not None:
+        _want(ids, "ids", torch.int32, (T, cfg.topk), dev)
+    if weights is not None:
+        _want(weights, "weights", torch.float32, (T, cfg.topk), dev)
+    return cfg, ls
 
 
 def _route(logits, topk, scoring, bias, renormalize, scale, live, ids, weights):
-    ls = _rows(logits, "logits")
-    T, E = logits.shape
-    dev = logits.device
-    cfg = _route_config(E, int(topk), _code(logits, "logits"), scoring, bool(renormalize), float(scale))
-    pb = None if bias is None else _want(bias, "bias", torch.float32, (E,), dev)
-    pl = None if live is None else _want(live, "live", torch.bool, (T,), dev)
+    key = (logits.dtype, logits.shape, logits.stride(), logits.device, topk, scoring, renormalize, scale, _layout(bias),
+           _layout(live), _layout(ids), _layout(weights))
+    plan = _routes.get(key) or _keep(_routes, key, _route_plan(logits, topk, scoring, bias, renormalize, scale, live, ids,
+                                                               weights))
+    cfg, ls = plan
+    T, dev = logits.shape[0], logits.device
     if ids is None:
         ids = torch.empty((T, cfg.topk), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, cfg.topk), dtype=torch.float32, device=dev)
-    pi = _want(ids, "ids", torch.int32, (T, cfg.topk), dev)
-    pw = _want(weights, "weights", torch.float32, (T, cfg.topk), dev)
-    with on_device(dev):
-        st = nat.load().afd_route(cfg, T, logits.data_ptr(), ls, pb, pl, pi, pw, raw_stream(dev))
-    nat.check(st, "route_tokens")
+    st = _launch(dev, nat.load().afd_route, cfg, T, logits.data_ptr(), ls, None if bias is None else bias.data_ptr(),
+                 None if live is None else live.data_ptr(), ids.data_ptr(), weights.data_ptr())
+    if st:
+        nat.check(st, "route_tokens")
     return Routes(ids, weights)
 
 
@@ -352,45 +408,51 @@ def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True,
     """The logits' gradient, [T, E] of their type, through the weights of route_tokens: grad float32
     [T, topk], ids as they were chosen (any outside [0, E) takes no part)."""
     _plain("route_tokens_grad", grad, logits, ids, out)
-    ls = _rows(logits, "logits")
-    pi, pg = _topk_of(ids, "ids", logits, torch.int32), _topk_of(grad, "grad", logits, torch.float32)
-    if grad.shape != ids.shape:
-        raise ValueError("grad and ids must have one shape")
-    (T, E), dev = logits.shape, logits.device
-    cfg = _route_config(E, ids.shape[1], _code(logits, "logits"), scoring, bool(renormalize), float(scale))
+    key = (logits.dtype, logits.shape, logits.stride(), logits.device, scoring, renormalize, scale, _layout(grad), _layout(ids),
+           _layout(out))
+    plan = _routes.get(key) or _keep(_routes, key, _route_grad_plan(grad, logits, ids, scoring, renormalize, scale, out))
+    cfg, ls = plan
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    po = _want(out, "out", logits.dtype, (T, E), dev)
-    with on_device(dev):
-        st = nat.load().afd_route_grad(cfg, T, pg, logits.data_ptr(), ls, pi, po, raw_stream(dev))
-    nat.check(st, "route_tokens_grad")
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    st = _launch(logits.device, nat.load().afd_route_grad, cfg, logits.shape[0], grad.data_ptr(), logits.data_ptr(), ls,
+                 ids.data_ptr(), out.data_ptr())
+    if st:
+        nat.check(st, "route_tokens_grad")
     return out
 
 
-@functools.lru_cache(maxsize=256)
-def _balance_need(rows, *cfg):
-    ws = ctypes.c_size_t(0)
-    nat.check(nat.load().afd_balance_query(ctypes.byref(_route_config(*cfg)), rows, ctypes.byref(ws)), "balance_loss")
-    return ws.value
+def _route_grad_plan(grad, logits, ids, scoring, renormalize, scale, out):
+    ls, topk = _rows(logits, "logits"), _ids_of(ids, logits)
+    _want(grad, "grad", torch.float32, tuple(ids.shape), logits.device)
+    if out is not None:
+        _want(out, "out", logits.dtype, tuple(logits.shape), logits.device)
+    return _route_config(logits.shape[1], topk, _code(logits, "logits"), scoring, bool(renormalize), float(scale)), ls
 
 
-def _balance(logits, ids, scoring, coefficient):
-    ls = _rows(logits, "logits")
-    pi = _topk_of(ids, "ids", logits, torch.int32)
-    (T, E), dev = logits.shape, logits.device
-    key = E, ids.shape[1], _code(logits, "logits"), scoring, False, 1.0
-    cfg, need = _route_config(*key), _balance_need(T, *key)
+def _balance_plan(logits, ids, scoring, coefficient):
+    """(configuration, row stride, workspace bytes, coefficient) of a loss whose arguments' layouts fit."""
+    ls, topk = _rows(logits, "logits"), _ids_of(ids, logits)
+    cfg, ws = _route_config(logits.shape[1], topk, _code(logits, "logits"), scoring, False, 1.0), ctypes.c_size_t(0)
     coefficient = float(coefficient)
     if not abs(coefficient) <= torch.finfo(torch.float32).max:
         raise ValueError(f"coefficient must be a finite float32, got {coefficient}")
+    nat.check(nat.load().afd_balance_query(ctypes.byref(cfg), logits.shape[0], ctypes.byref(ws)), "balance_loss")
+    return cfg, ls, ws.value, coefficient
+
+
+def _balance(logits, ids, scoring, coefficient):
+    key = logits.dtype, logits.shape, logits.stride(), logits.device, _layout(ids), scoring, coefficient
+    plan = _balances.get(key) or _keep(_balances, key, _balance_plan(logits, ids, scoring, coefficient))
+    cfg, ls, need, coefficient = plan
+    (T, E), dev = logits.shape, logits.device
     loss = torch.empty((), dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int32, device=dev)
     slope = torch.empty(E, dtype=torch.float32, device=dev)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    with on_device(dev):
-        st = nat.load().afd_balance(cfg, T, logits.data_ptr(), ls, pi, coefficient, loss.data_ptr(), counts.data_ptr(),
-                                    slope.data_ptr(), ws.data_ptr(), need, raw_stream(dev))
-    nat.check(st, "balance_loss")
+    st = _launch(dev, nat.load().afd_balance, cfg, T, logits.data_ptr(), ls, ids.data_ptr(), coefficient, loss.data_ptr(),
+                 counts.data_ptr(), slope.data_ptr(), ws.data_ptr(), need)
+    if st:
+        nat.check(st, "balance_loss")
     return Balance(loss, counts, slope)
 
 
@@ -439,15 +501,23 @@ def balance_loss_grad(grad, logits, ids, slope, *, scoring="softmax", out=None):
     """The logits' gradient, [T, E] of their type: grad float32 [], of the loss on the GPU;
     ids and slope as balance_loss had and gave them.  Tokens that do not count have 0."""
     _plain("balance_loss_grad", grad, logits, ids, slope, out)
-    ls = _rows(logits, "logits")
-    pi = _topk_of(ids, "ids", logits, torch.int32)
-    (T, E), dev = logits.shape, logits.device
-    pg, ps = _want(grad, "grad", torch.float32, (), dev), _want(slope, "slope", torch.float32, (E,), dev)
-    cfg = _route_config(E, ids.shape[1], _code(logits, "logits"), scoring, False, 1.0)
+    key = (logits.dtype, logits.shape, logits.stride(), logits.device, _layout(ids), scoring, _layout(grad), _layout(slope),
+           _layout(out))
+    plan = _balances.get(key) or _keep(_balances, key, _balance_grad_plan(grad, logits, ids, slope, scoring, out))
+    cfg, ls = plan
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    po = _want(out, "out", logits.dtype, (T, E), dev)
-    with on_device(dev):
-        st = nat.load().afd_balance_grad(cfg, T, pg, logits.data_ptr(), ls, pi, ps, po, raw_stream(dev))
-    nat.check(st, "balance_loss_grad")
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    st = _launch(logits.device, nat.load().afd_balance_grad, cfg, logits.shape[0], grad.data_ptr(), logits.data_ptr(), ls,
+                 ids.data_ptr(), slope.data_ptr(), out.data_ptr())
+    if st:
+        nat.check(st, "balance_loss_grad")
     return out
+
+
+def _balance_grad_plan(grad, logits, ids, slope, scoring, out):
+    ls, topk = _rows(logits, "logits"), _ids_of(ids, logits)
+    _want(grad, "grad", torch.float32, (), logits.device)
+    _want(slope, "slope", torch.float32, (logits.shape[1],), logits.device)
+    if out is not None:
+        _want(out, "out", logits.dtype, tuple(logits.shape), logits.device)
+    return _route_config(logits.shape[1], topk, _code(logits, "logits"), scoring, False, 1.0), ls

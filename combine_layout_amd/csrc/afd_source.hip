@@ -34,6 +34,9 @@ struct Sum {
 struct Max {
     __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
+struct SumInt {
+    __device__ __forceinline__ int operator()(int a, int b) const { return a + b; }
+};
 struct MaxInt {
     __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
 };
@@ -632,18 +635,38 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_wave_barrier();
 }
 
-// The largest `rounds` of a token's keys, one after another: the lanes' first keys are
-// compared, the one that holds the largest writes it down and goes on to its next; of
-// several, the one with the lowest expert.  Returns whether two keys that follow each
-// other were nearer than `near` allows.
-template <typename R, int LANES, int V, typename Near>
-__device__ __forceinline__ bool take(int *k, int rounds, Pick *picks, Near near)
+// What a token's choice leaves: up to kMost keys in falling order.
+template <int LANES>
+constexpr int kMost = LANES == 16 ? 48 : 64;
+
+// Whether two keys with biases may be out of order.  A sigmoid is off by less than 4
+// roundings of 1, a softmax by less than 25 (its sum's 14, the exponential's and the
+// division's); the sum with the bias by one of its own size.  Two keys that are 64 of both
+// apart are in order (2^-18 = 64 U).
+__device__ __forceinline__ bool too_near(int larger, int smaller)
+{
+    const float lo = of_key(smaller);
+    return smaller != kNoKey && !(of_key(larger) - lo > 0x1p-18f * (1.f + fabsf(lo)));
+}
+
+struct Taken {
+    int count;    // keys taken, the same for every token of the wavefront
+    bool close;   // two of this token's follow each other too nearly to be in order
+    bool open;    // so do the last two
+};
+
+// The largest keys of a token, one after another: the lanes' first keys are compared, the
+// lane that holds the largest writes it down and goes on to its next; of several, the one
+// with the lowest expert.  `rounds` of them, with NEAR one more for the border behind the
+// last place, and as many as are too near to it.
+template <typename R, int LANES, int V, bool NEAR>
+__device__ __forceinline__ Taken take(int *k, int rounds, Pick *picks)
 {
     uint32_t order = sort_keys<V>(k);
-    bool close = false;
-    float before = __builtin_inff();
+    Taken t{0, false, false};
+    int before = 0x7F800000;
     const int base = (threadIdx.x & 63) & ~(LANES - 1);
-    for (int r = 0; r < rounds; ++r) {
+    for (int r = 0; r < rounds || (NEAR && r <= rounds) || (NEAR && r < kMost<LANES> && __any(t.open)); ++r) {
         const int m = across<LANES>(k[0], MaxInt()), e = R::expert(order & 7);
         bool mine = k[0] == m;
         uint64_t hit = __ballot(mine) >> base;
@@ -653,37 +676,89 @@ __device__ __forceinline__ bool take(int *k, int rounds, Pick *picks, Near near)
             mine = mine && low == e;
         }
         mine = mine && m != kNoKey;
-        if (mine && r < kMaxTopk) picks[r] = Pick{e, m};
+        if (mine) picks[r] = Pick{e, m};
         order = mine ? order >> 4 : order;
 #pragma unroll
         for (int i = 0; i < V; ++i) k[i] = !mine ? k[i] : i + 1 < V ? k[i + 1] : kNoKey;
-        close = m != kNoKey ? near(before, of_key(m)) || close : close;
-        before = of_key(m);
+        if constexpr (NEAR) {
+            t.open = r > 0 && too_near(before, m);
+            t.close = t.close || t.open;
+            before = m;
+        }
+        t.count = r + 1;
     }
-    return close;
+    return t;
 }
 
-// The choice by 64-bit scores, for the tokens whose 32-bit ones are too near to tell.
+// The 64-bit score of a logit; `sum` of the softmax's terms.
+__device__ __forceinline__ double score(const RouteArgs &a, float l, float m, double sum)
+{
+    if (a.sigmoid) return 1.0 / (1.0 + exp(-double(l)));
+    return (l == kMinusInf ? 0.0 : l == m ? 1.0 : exp(double(l) - double(m))) / sum;
+}
+
+template <typename R>
+__device__ __forceinline__ double score_sum(const RouteArgs &a, const float *v, float m)
+{
+    if (a.sigmoid) return 1.0;
+    double t = 0.0;
+#pragma unroll
+    for (int i = 0; i < R::kV; ++i) t += score(a, v[i], m, 1.0);
+    for (int d = 1; d < R::kLanes; d *= 2) t += __shfl_xor(t, d);
+    return t;
+}
+
+// The order of the picked experts by their 64-bit scores: each compares itself with all.
+template <typename R>
+__device__ __forceinline__ void order_exactly(const RouteArgs &a, int64_t row, int count, Pick *picks)
+{
+    constexpr int LANES = R::kLanes, kEach = kMost<LANES> / LANES;
+    float v[R::kV];
+    R::load(a, row, v);   // again, rather than held by all who need none of this
+    const float m = R::largest(v);
+    const double sum = score_sum<R>(a, v, m);
+    double key[kEach];
+    int id[kEach], rank[kEach];
+#pragma unroll
+    for (int s = 0; s < kEach; ++s) {
+        id[s] = s * LANES + R::lane() < count ? picks[s * LANES + R::lane()].id : -1;
+        rank[s] = 0;
+        key[s] = -__builtin_inf();
+        if (id[s] >= 0) key[s] = score(a, R::one(a, row * a.ls + id[s]), m, sum) + double(a.bias[id[s]]);
+    }
+    for (int j = 0; j < count; ++j) {
+        double x = 0.0;
+        int e = -1;
+#pragma unroll
+        for (int s = 0; s < kEach; ++s) {
+            if (j / LANES != s) continue;
+            x = __shfl(key[s], j % LANES, LANES);
+            e = __shfl(id[s], j % LANES, LANES);
+        }
+#pragma unroll
+        for (int s = 0; s < kEach; ++s) rank[s] += e >= 0 && (x > key[s] || (x == key[s] && e < id[s]));
+    }
+    wave_sync();
+#pragma unroll
+    for (int s = 0; s < kEach; ++s)
+        if (id[s] >= 0) picks[rank[s]].id = id[s];
+}
+
+// The choice by 64-bit scores from the start, where more than kMost follow each other too
+// nearly.
 template <typename R>
 __device__ __forceinline__ void take_exactly(const RouteArgs &a, int64_t row, Pick *picks)
 {
     constexpr int V = R::kV, LANES = R::kLanes;
     float v[V];
-    R::load(a, row, v);   // again, rather than held by all who need none of this
+    R::load(a, row, v);
     const float m = R::largest(v);
-    double key[V], t = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const double x = double(v[i]);
-        if (a.sigmoid) key[i] = 1.0 / (1.0 + exp(-x));
-        else key[i] = v[i] == kMinusInf ? 0.0 : v[i] == m ? 1.0 : exp(x - double(m));
-        t += key[i];
-    }
-    for (int d = 1; d < LANES; d *= 2) t += __shfl_xor(t, d);
+    const double sum = score_sum<R>(a, v, m);
+    double key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = R::expert(i);
-        const double x = (a.sigmoid ? key[i] : key[i] / t) + (e < a.E ? double(a.bias[e]) : 0.0);
+        const double x = score(a, v[i], m, sum) + (e < a.E ? double(a.bias[e]) : 0.0);
         key[i] = v[i] == kMinusInf || !(x == x) ? -__builtin_inf() : x;
     }
     for (int k = 0; k < a.K; ++k) {
@@ -697,59 +772,129 @@ __device__ __forceinline__ void take_exactly(const RouteArgs &a, int64_t row, Pi
         int e = INT32_MAX;
 #pragma unroll
         for (int i = V - 1; i >= 0; --i) e = key[i] == top ? R::expert(i) : e;
-        for (int d = 1; d < LANES; d *= 2) e = min(e, __shfl_xor(e, d));
+        e = across<LANES>(e, MinInt());
         if (R::lane() == 0) picks[k].id = top == -__builtin_inf() ? -1 : e;
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = R::expert(i) == e ? -__builtin_inf() : key[i];
     }
 }
 
+// The choice of a wavefront with one token: a border that at least K of the lanes' largest
+// keys reach is found by halving, the keys that reach it (about K and a few) are brought
+// together, one a lane, and each counts the larger ones.  Returns the lane's key and its
+// rank, or false where more than 64 reach the border (many equal keys), with `k` as it was.
+template <typename R, int V>
+__device__ __forceinline__ bool take_above(const int *k, int K, Pick *picks, Pick &mine, int &rank, int &count)
+{
+    int head = k[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) head = max(head, k[i]);
+    int lo = __builtin_amdgcn_readfirstlane(across<kWave>(head, MinInt()));
+    int hi = __builtin_amdgcn_readfirstlane(across<kWave>(head, MaxInt()));
+    for (int i = 0; i < 12 && lo < hi; ++i) {
+        const int mid = lo + int(((uint32_t(hi) - uint32_t(lo)) >> 1) + ((uint32_t(hi) - uint32_t(lo)) & 1));
+        const int reach = __popcll(__ballot(head >= mid));
+        if (reach >= K) {
+            lo = mid;
+            if (reach <= K + 2) break;
+        } else {
+            hi = mid - 1;
+        }
+    }
+    lo = max(lo, kNoKey + 1);
+    count = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) count += __popcll(__ballot(k[i] >= lo));
+    if (count > kWave) return false;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint64_t in = __ballot(k[i] >= lo);
+        const int to = at + __builtin_amdgcn_mbcnt_hi(uint32_t(in >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(in), 0));
+        if (k[i] >= lo) picks[to] = Pick{R::expert(i), k[i]};
+        at += __popcll(in);
+    }
+    wave_sync();
+    mine = R::lane() < count ? picks[R::lane()] : Pick{-1, kNoKey};
+    rank = 0;
+    // key, then the lower expert, as one number
+    const uint64_t self = uint64_t(uint32_t(mine.key) ^ 0x80000000u) << 32 | uint32_t(~mine.id);
+    for (int j = 0; j < count; ++j) {
+        const uint64_t other = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(self >> 32), j))) << 32 |
+                               uint32_t(__builtin_amdgcn_readlane(int(self), j));
+        rank += other > self;
+    }
+    return true;
+}
+
 // One token per LANES lanes, its logits in registers from the load on.  What bounds it is
-// the choice: a round is one reduction over the lanes, so a lane's logits are sorted once
-// and only the first of them takes part.
+// the choice, which is arithmetic and not memory: a round of `take` is one reduction over
+// the lanes, so a lane's logits are sorted once and only the first of them takes part.
 template <bool L32, int LANES, int V, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a)
 {
     using R = Row<L32, LANES, V, VEC>;
-    __shared__ Pick picked[R::kRows][kMaxTopk];
+    __shared__ Pick picked[R::kRows][kMost<LANES>];
     const int lane = R::lane();
     const int64_t row_ = int64_t(blockIdx.x) * R::kRows + threadIdx.x / LANES, row = min(row_, int64_t(a.rows - 1));
     Pick *picks = picked[threadIdx.x / LANES];
     float v[V];
     R::load(a, row, v);
     const bool live = !a.live || a.live[row] != 0;
-#pragma unroll
-    for (int s = 0; s < R::kSlots; ++s)
-        if (s * LANES + lane < kMaxTopk) picks[s * LANES + lane] = Pick{-1, kNoKey};
-    wave_sync();
     float m = 0.f, sum = 1.f;
     int key[V];
-    if constexpr (BIAS) {
+    if (BIAS ? !a.sigmoid : !a.sigmoid && !a.renorm) {
         float t[V];
         m = R::largest(v);
-        if (!a.sigmoid) sum = R::terms(v, m, t);
+        sum = R::terms(v, m, t);
+        if constexpr (BIAS) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = __builtin_bit_cast(int, t[i] / sum);
+        }
+    }
+    if constexpr (BIAS) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = R::expert(i);
-            const float z = exp_neg(-fabsf(v[i])), x = (a.sigmoid ? (v[i] >= 0.f ? 1.f : z) * inverse(1.0f + z) : t[i] / sum) + (e < a.E ? a.bias[e] : 0.f);
+            const float z = exp_neg(-fabsf(v[i])), s = (v[i] >= 0.f ? 1.f : z) * inverse(1.0f + z);
+            const float x = (a.sigmoid ? s : __builtin_bit_cast(float, key[i])) + (e < a.E ? a.bias[e] : 0.f);
             key[i] = v[i] == kMinusInf || !(x == x) ? kNoKey : key_of(x);
         }
-        // A score is off by less than 32 roundings of 1, and the sum with the bias by one of
-        // its own size: keys that are 128 of both apart are in order.  One round more than
-        // there are places, for the border behind the last.
-        const bool close = take<R, LANES, V>(key, a.K + 1, picks, [](float hi, float lo) {
-            return !(hi - lo > 0x1p-17f * (1.f + fabsf(lo)));
-        });
-        if (__any(close)) take_exactly<R>(a, row, picks);
     } else {
-        if (!a.sigmoid && !a.renorm) {
-            float t[V];
-            m = R::largest(v);
-            sum = R::terms(v, m, t);
-        }
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = key_of(v[i]);
-        take<R, LANES, V>(key, a.K, picks, [](float, float) { return false; });
+    }
+    if constexpr (!BIAS && LANES == kWave) {
+        Pick mine;
+        int rank, count;
+        if (take_above<R, V>(key, a.K, picks, mine, rank, count)) {
+            const bool on = lane < count && rank < a.K;
+            const float l = of_key(mine.key);
+            float w;
+            weights_of<LANES, 1>(a, &l, &on, m, sum, &w);
+            if (row_ < a.rows) {
+                if (on) {
+                    a.ids[row * a.K + rank] = live ? mine.id : -1;
+                    a.w[row * a.K + rank] = live ? a.scale * w : 0.f;
+                }
+                if (lane >= count && lane < a.K) {
+                    a.ids[row * a.K + lane] = -1;
+                    a.w[row * a.K + lane] = 0.f;
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < kMost<LANES> / LANES; ++s) picks[s * LANES + lane] = Pick{-1, kNoKey};
+    wave_sync();
+    const Taken taken = take<R, LANES, V, BIAS>(key, a.K, picks);
+    if constexpr (BIAS) {
+        if (__any(taken.close)) {
+            wave_sync();
+            if (__any(taken.open)) take_exactly<R>(a, row, picks);
+            else order_exactly<R>(a, row, taken.count, picks);
+        }
     }
     wave_sync();
     bool on[R::kSlots];
@@ -928,8 +1073,12 @@ __global__ __launch_bounds__(THREADS) void k_balance(BalanceArgs b)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] += p[i];
     }
-    if (R::lane() == 0) atomicAdd(&total[0], tokens);
-    atomicAdd(&total[1], chosen);
+    tokens = across<kWave>(R::lane() == 0 ? tokens : 0, SumInt());
+    chosen = across<kWave>(chosen, SumInt());
+    if (threadIdx.x % kWave == 0) {
+        atomicAdd(&total[0], tokens);
+        atomicAdd(&total[1], chosen);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) join[threadIdx.x / LANES][R::expert(i)] = acc[i];
     __syncthreads();
@@ -959,24 +1108,33 @@ struct BalanceJoinArgs {
 __global__ __launch_bounds__(256) void k_balance_join(BalanceJoinArgs a)
 {
     __shared__ double share[16][16];
-    __shared__ int count[16][16], total[2];
+    __shared__ int count[16][16];
+    __shared__ int2 totals[4];
     const int col = threadIdx.x % 16, slice = threadIdx.x / 16, e = blockIdx.x * 16 + col;
-    if (threadIdx.x < 2) total[threadIdx.x] = 0;
-    __syncthreads();
+    // every load on its way before the first is used
+    constexpr int kTurns = kBalanceGroups / 16;
+    float sv[kTurns];
+    int cv[kTurns];
+    const int in = min(e, a.E - 1);
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int g = min(i * 16 + slice, a.groups - 1);
+        sv[i] = a.share[int64_t(g) * a.E + in];
+        cv[i] = a.count[int64_t(g) * a.E + in];
+    }
+    static_assert(kBalanceGroups <= 256, "a thread for every group's totals");
+    int2 mine = {0, 0};
+    if (int(threadIdx.x) < a.groups) mine = reinterpret_cast<const int2 *>(a.totals)[threadIdx.x];
+    mine.x = across<kWave>(mine.x, SumInt());
+    mine.y = across<kWave>(mine.y, SumInt());
+    if (threadIdx.x % kWave == 0) totals[threadIdx.x / kWave] = mine;
     double s = 0.0;
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < kBalanceGroups / 16; ++i) {
-        const int g = i * 16 + slice;
-        if (g < a.groups && e < a.E) {
-            s += double(a.share[int64_t(g) * a.E + e]);
-            c += a.count[int64_t(g) * a.E + e];
-        }
-    }
-    static_assert(kBalanceGroups <= 256, "a thread for every group's totals");
-    if (int(threadIdx.x) < a.groups) {
-        atomicAdd(&total[0], a.totals[threadIdx.x * 2]);
-        atomicAdd(&total[1], a.totals[threadIdx.x * 2 + 1]);
+    for (int i = 0; i < kTurns; ++i) {
+        const bool there = i * 16 + slice < a.groups;
+        s += there ? double(sv[i]) : 0.0;
+        c += there ? cv[i] : 0;
     }
     share[slice][col] = s;
     count[slice][col] = c;
@@ -989,7 +1147,13 @@ __global__ __launch_bounds__(256) void k_balance_join(BalanceJoinArgs a)
         s += share[i][col];
         c += count[i][col];
     }
-    const double n = double(total[0]) * double(total[1]);
+    int2 all = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        all.x += totals[i].x;
+        all.y += totals[i].y;
+    }
+    const double n = double(all.x) * double(all.y);
     const float slope = n > 0.0 ? float(double(a.coefficient) * double(a.E) * double(c) / n) : 0.f;
     if (e < a.E) {
         a.counts[e] = c;

@@ -32,7 +32,7 @@ AFD_ACT_NONE, AFD_ACT_SWIGLU = 0, 1
 ACTIVATIONS = {None: AFD_ACT_NONE, "swiglu": AFD_ACT_SWIGLU}
 WEIGHTS_ROWS, WEIGHTS_PACKED = 0, 1
 MAX_ADAPTERS, MAX_RANK = 65536, 128
-MAX_NORM_HIDDEN, NO_RESIDUAL = 65536, -1
+MAX_NORM_HIDDEN, NO_RESIDUAL = 16384, -1
 SCORINGS = {"softmax": 0, "sigmoid": 1}
 
 STATUS_NAMES = {0: "AFD_OK", -1: "AFD_E_ARG", -2: "AFD_E_SHAPE", -3: "AFD_E_ORDER",

@@ -174,7 +174,7 @@ struct NormArgs {
     void *out, *h;
     float *outs, *rstd;
     int64_t xs, rs, hs;
-    int rows, H;
+    int first, rows, H;   // rows [first, rows) in this launch
     float eps;
     bool w32;
 };
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm(NormArgs a)
 {
     constexpr int kRows = WPR >= 4 ? 1 : 4 / WPR;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = (wave % WPR) * kWave + lane, runs = a.H / 8;
-    const int64_t row = int64_t(blockIdx.x) * kRows + wave / WPR;
+    const int64_t row = a.first + int64_t(blockIdx.x) * kRows + wave / WPR;
     if (row >= a.rows) return;   // a whole workgroup, or a wavefront with a row of its own
     Eight<X32> x[C];
     Eight<RES == 2> r[RES ? C : 1];
@@ -293,16 +293,17 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm_grad(NormGr
                 w[i].load(a.w, c * 8, a.w32);
             }
         }
-        float d[C][8], m = 0.f;
+        float m = 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            w[i].values(d[i], a.w32);
+            float x[8];
+            w[i].values(x, a.w32);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float u = h[i].get(j) * rstd;
                 // columns behind the last hold whatever w holds: grad is 0 there
-                d[i][j] = i * WPR * kWave + t < runs ? g[i].get(j) * d[i][j] : 0.f;
-                m = fmaf(d[i][j], u, m);
+                x[j] = i * WPR * kWave + t < runs ? g[i].get(j) * x[j] : 0.f;
+                m = fmaf(x[j], u, m);
                 dw[i][j] = fmaf(g[i].get(j), u, dw[i][j]);
             }
         }
@@ -319,9 +320,12 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm_grad(NormGr
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = i * WPR * kWave + t;
+            if (c >= runs) continue;
+            float x[8];
+            w[i].values(x, a.w32);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[i][j] = fmaf(rstd, d[i][j] - h[i].get(j) * rstd * m, gr[i].get(j));
-            if (c < runs) store_eight<H32>(a.dh, row * a.H + c * 8, d[i]);
+            for (int j = 0; j < 8; ++j) x[j] = fmaf(rstd, g[i].get(j) * x[j] - h[i].get(j) * rstd * m, gr[i].get(j));
+            store_eight<H32>(a.dh, row * a.H + c * 8, x);
         }
     }
     if (!a.part) return;
@@ -677,9 +681,11 @@ __device__ __forceinline__ Taken take(int *k, int rounds, Pick *picks)
         }
         mine = mine && m != kNoKey;
         if (mine) picks[r] = Pick{e, m};
+        // by a mask: a choice between two elements becomes an index that is not known, and the keys go to scratch memory
+        const int pop = mine ? -1 : 0;
         order = mine ? order >> 4 : order;
 #pragma unroll
-        for (int i = 0; i < V; ++i) k[i] = !mine ? k[i] : i + 1 < V ? k[i + 1] : kNoKey;
+        for (int i = 0; i < V; ++i) k[i] = (pop & (i + 1 < V ? k[i + 1] : kNoKey)) | (~pop & k[i]);
         if constexpr (NEAR) {
             t.open = r > 0 && too_near(before, m);
             t.close = t.close || t.open;
@@ -1208,13 +1214,21 @@ __global__ __launch_bounds__(256) void k_balance_grad(RouteArgs a)
 
 // ---------------------------------------------------------------- launches ----
 
+// Rows of one launch: up to 1024 threads each, and a launch has fewer than 2^32.
+constexpr int kLaunchRows = 1 << 20;
+
 template <bool X32, int RES, bool OUT8, int WPR, int C>
-int norm_as(const NormArgs &a, hipStream_t st)
+int norm_as(NormArgs a, hipStream_t st)
 {
-    constexpr int rows = WPR >= 4 ? 1 : 4 / WPR;
-    hipLaunchKernelGGL((k_norm<X32, RES, OUT8, WPR, C>), dim3(unsigned((a.rows + rows - 1) / rows)), dim3(WPR > 4 ? WPR * kWave : 256),
-                       0, st, a);
-    return launched();
+    constexpr int each = WPR >= 4 ? 1 : 4 / WPR;
+    const int rows = a.rows;
+    for (; a.first < rows; a.first += kLaunchRows) {
+        a.rows = std::min(rows, a.first + kLaunchRows);
+        hipLaunchKernelGGL((k_norm<X32, RES, OUT8, WPR, C>), dim3(unsigned((a.rows - a.first + each - 1) / each)),
+                           dim3(WPR > 4 ? WPR * kWave : 256), 0, st, a);
+        if (launched() != 0) return 1;
+    }
+    return 0;
 }
 
 template <bool X32, int RES, bool OUT8>
@@ -1225,9 +1239,8 @@ int norm_of(const NormArgs &a, hipStream_t st)
     if (a.H <= 2048) return norm_as<X32, RES, OUT8, 1, 4>(a, st);
     if (a.H <= 4096) return norm_as<X32, RES, OUT8, 4, 2>(a, st);
     if (a.H <= 8192) return norm_as<X32, RES, OUT8, 4, 4>(a, st);
-    if (a.H <= 16384) return norm_as<X32, RES, OUT8, 16, 2>(a, st);
-    if (a.H <= 32768) return norm_as<X32, RES, OUT8, 16, 4>(a, st);
-    return norm_as<X32, RES, OUT8, 16, 8>(a, st);
+    static_assert(AFD_MAX_NORM_HIDDEN == 16 * kWave * 2 * 8, "the widest row");
+    return norm_as<X32, RES, OUT8, 16, 2>(a, st);
 }
 
 template <bool X32, int RES>
@@ -1251,9 +1264,7 @@ int norm_grad_of(const NormGradArgs &a, int groups, hipStream_t st)
     if (a.H <= 2048) return norm_grad_as<H32, 1, 4>(a, groups, st);
     if (a.H <= 4096) return norm_grad_as<H32, 4, 2>(a, groups, st);
     if (a.H <= 8192) return norm_grad_as<H32, 4, 4>(a, groups, st);
-    if (a.H <= 16384) return norm_grad_as<H32, 16, 2>(a, groups, st);
-    if (a.H <= 32768) return norm_grad_as<H32, 16, 4>(a, groups, st);
-    return norm_grad_as<H32, 16, 8>(a, groups, st);
+    return norm_grad_as<H32, 16, 2>(a, groups, st);
 }
 
 RouteArgs route_args(const RoutePlan &p)
@@ -1345,7 +1356,7 @@ struct BalanceGradLaunch {
 int be_launch_norm(const NormPlan &p, void *stream)
 {
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    NormArgs a{p.x, p.r, p.w, p.out, p.h, p.outs, p.rstd, p.xs, p.rs, p.hs, int(p.rows), p.H, p.eps, p.w32};
+    NormArgs a{p.x, p.r, p.w, p.out, p.h, p.outs, p.rstd, p.xs, p.rs, p.hs, 0, int(p.rows), p.H, p.eps, p.w32};
     if (!p.res) return p.x32 ? norm_out<true, 0>(a, p.out8, st) : norm_out<false, 0>(a, p.out8, st);
     if (!p.r32) return p.x32 ? norm_out<true, 1>(a, p.out8, st) : norm_out<false, 1>(a, p.out8, st);
     return p.x32 ? norm_out<true, 2>(a, p.out8, st) : norm_out<false, 2>(a, p.out8, st);

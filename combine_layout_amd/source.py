@@ -250,7 +250,7 @@ def rms_norm(x, weight, residual=None, *, eps=1e-6, dtype=torch.bfloat16, out=No
     """The root-mean-square norm of h = x + residual (or of x), rows y = h / sqrt(mean(h^2) + eps) * weight.
 
     x [T, H], residual [T, H] and weight [H] are bfloat16 or float32 each; H is a multiple
-    of 8 up to 65536.  h is the float32 sum in the residual's type, kept in residual_out (new
+    of 8 up to 16384.  h is the float32 sum in the residual's type, kept in residual_out (new
     memory, the residual itself, or x itself where type and strides are the same) and
     normalised as kept.  dtype torch.float8_e4m3fn (H a multiple of 128) gives codes with
     their scales per 128 columns, as source_dispatch takes them: scale = amax / 448 of the

@@ -590,7 +590,7 @@ afd_status afd_worker_tags(afd_ctx *ctx, int32_t f, const int32_t *const *tags, 
  * carries none.
  */
 
-#define AFD_MAX_NORM_HIDDEN 65536
+#define AFD_MAX_NORM_HIDDEN 16384
 #define AFD_NO_RESIDUAL (-1)
 
 /*

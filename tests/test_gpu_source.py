@@ -52,7 +52,7 @@ def _norm_case(seed, T, H, xt, rt, wt):
     return x, r, w
 
 
-WIDTHS = [8, 24, 128, 512, 520, 1024, 1160, 2048, 2056, 4096, 5000, 8192, 8200, 16384, 20000, 32768, 40000, 65536]
+WIDTHS = [8, 24, 128, 512, 520, 1024, 1160, 2048, 2056, 4096, 5000, 8192, 8200, 12000, 16376, 16384]
 
 
 @pytest.mark.parametrize("H", WIDTHS)
@@ -74,7 +74,7 @@ def test_norm(H, xt, rt, wt, T):
     assert n.rows.dtype is BF and n.rows.is_contiguous()
 
 
-@pytest.mark.parametrize("H", [128, 384, 1024, 2048, 4096, 5120, 8192, 16384, 20480, 65536])
+@pytest.mark.parametrize("H", [128, 384, 1024, 2048, 4096, 5120, 8192, 12288, 16384])
 @pytest.mark.parametrize("xt,rt,wt,T", [(BF, BF, BF, 5), (BF, None, F32, 3), (F32, F32, BF, 4), (BF, F32, F32, 1)])
 def test_norm_fp8(H, xt, rt, wt, T):
     afd = _afd()
@@ -716,3 +716,152 @@ def test_rounds_of_two_layers(dtype):
             # the round's experts and these may take different kernels: rows equal to a BF16 step, and one more for the sum
             size = tot.abs().amax(1, keepdim=True)
             assert ((x[s].float() - tot).abs() <= size * 2.0 ** -6).all(), (layer, s)
+
+
+# ------------------------------------------------ borders, sizes, refusals --
+
+@pytest.mark.parametrize("E,K", [(40, 6), (128, 8), (200, 9), (256, 32), (300, 8), (512, 8), (512, 32)])
+@pytest.mark.parametrize("levels", [1, 2, 4, 30, 200])
+@pytest.mark.parametrize("scoring,biased", [("softmax", False), ("sigmoid", True), ("softmax", True)])
+def test_route_ties(E, K, levels, scoring, biased):
+    """Logits of a few levels: many equal ones at every border, all of them where there is one level."""
+    afd = _afd()
+    _print("ties", E, K, levels, scoring, biased)
+    g = _gen(E + levels)
+    for dtype in (F32, BF):
+        l = (torch.randint(0, levels, (40, E), generator=g) / 64).to(dtype)
+        l[::5, ::3] = -INF
+        b = torch.randint(0, 3, (E,), generator=g) / 4 if biased else None
+        r = afd.route_tokens(l.cuda(), K, scoring=scoring, bias=None if b is None else b.cuda())
+        ids = r.ids.cpu().long()
+        want = ref.choose(l, K, scoring, b, None)
+        if b is None:
+            assert torch.equal(ids, want)
+        else:
+            # equal logits have equal scores whatever computes them; different ones with different biases may
+            # come within a 64-bit exponential's error of each other, or not: the keys have to agree
+            key = torch.where(ref.clean(l) == -INF, -INF, ref.scores(l, scoring) + b.double())
+            a, c = (torch.take_along_dim(key, i.clamp(min=0), 1) for i in (ids, want))
+            assert torch.equal(ids < 0, want < 0) and ((a - c).abs()[want >= 0] <= 2.0 ** -50).all()
+            same = (ids == want) | ((a - c).abs() <= 2.0 ** -50) & (a != c)
+            assert same.all() or torch.equal(a, c) and torch.equal(ids, want)
+
+
+@pytest.mark.parametrize("E,K", [(16, 4), (128, 8), (256, 8), (512, 8), (512, 32)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_scores_nearer_than_float32(E, K, scoring):
+    """Neighbouring float32 logits: scores that float32 cannot tell apart, 64 bits can."""
+    afd = _afd()
+    g = _gen(E)
+    base = torch.full((), 2.0) if scoring == "sigmoid" else torch.full((), 1.0)
+    step = torch.finfo(F32).eps * float(base)
+    l = torch.stack([base + step * torch.randperm(E, generator=g) for _ in range(50)]).float()
+    l[::2, E // 2:] = -1.0                          # fewer of them: settled among the picked
+    l[::7, 12:] = -1.0
+    b = torch.zeros(E)
+    r = afd.route_tokens(l.cuda(), K, scoring=scoring, bias=b.cuda())
+    assert torch.equal(r.ids.cpu().long(), ref.choose(l, K, scoring, b, None))
+
+
+def test_norm_of_more_rows_than_a_launch():
+    afd = _afd()
+    T, H = (1 << 20) + 5, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = torch.randn(T, H, generator=g, device="cuda").to(BF), torch.rand(H, generator=g, device="cuda")
+    n = afd.rms_norm(x, w, x, keep_rstd=True)
+    for at in (0, (1 << 20) - 3, T - 4):
+        s = slice(at, at + 4)
+        m = afd.rms_norm(x[s], w, x[s], keep_rstd=True)
+        assert all(a is None or torch.equal(a[s], b) for a, b in zip(n, m))
+
+
+def test_offsets_past_32_bits():
+    afd = _afd()
+    T, H = 140001, 16384                            # 2.3e9 elements
+    g = torch.Generator(device="cuda").manual_seed(2)
+    _print("offsets", T, H)
+    x = torch.empty(T, H, dtype=BF, device="cuda")
+    x[:1000] = torch.randn(1000, H, generator=g, device="cuda").to(BF)
+    x[1000:] = 0.5
+    x[-50:] = torch.randn(50, H, generator=g, device="cuda").to(BF)
+    w, tail = torch.rand(H, generator=g, device="cuda"), slice(T - 50, T)
+    n = afd.rms_norm(x, w, x, keep_rstd=True)
+    m = afd.rms_norm(x[tail].clone(), w, x[tail].clone(), keep_rstd=True)
+    assert all(a is None or torch.equal(a[tail], b) for a, b in zip(n, m))
+    f = afd.rms_norm(x, w, dtype=F8, out=torch.empty(T, H, dtype=F8, device="cuda"))
+    q = afd.rms_norm(x[tail].clone(), w, dtype=F8)
+    assert torch.equal(f.rows[tail].view(torch.uint8), q.rows.view(torch.uint8)) and torch.equal(f.scales[tail], q.scales)
+    del f
+    d, _ = afd.rms_norm_grad(n.rows, n.residual, w, n.rstd, out=x)
+    e, _ = afd.rms_norm_grad(m.rows, m.residual, w, m.rstd)
+    assert torch.equal(d[tail], e)
+    del d, n, x
+    T, E, K = (1 << 22) + 1001, 512, 8
+    l = torch.zeros(T, E, device="cuda")
+    l[-50:] = torch.randn(50, E, generator=g, device="cuda")
+    tail = slice(T - 50, T)
+    r = afd.route_tokens(l, K, renormalize=False)
+    t = l[tail].clone()
+    s = afd.route_tokens(t, K, renormalize=False)
+    assert torch.equal(r.ids[tail], s.ids) and torch.equal(r.weights[tail], s.weights)
+    assert torch.equal(r.ids[0].cpu(), torch.arange(K, dtype=torch.int32))
+    dw = torch.ones(T, K, device="cuda")
+    dw[-50:] = torch.randn(50, K, generator=g, device="cuda")
+    d = afd.route_tokens_grad(dw, l, r.ids, renormalize=False)
+    assert torch.equal(d[tail], afd.route_tokens_grad(dw[tail].clone(), t, s.ids, renormalize=False))
+    b = afd.balance_loss(l, r.ids)
+    assert int(b.counts.sum()) == T * K and int(b.counts[0]) >= T - 50
+    one = torch.ones((), device="cuda")
+    afd.balance_loss_grad(one, l, r.ids, b.slope, out=d)
+    assert torch.equal(d[tail], afd.balance_loss_grad(one, t, s.ids, b.slope))
+
+
+def test_refusals():
+    afd = _afd()
+    z = lambda *s, t=F32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    x, w, l, ids = z(4, 256, t=BF), z(256, t=BF), z(4, 8), z(4, 2, t=torch.int32)
+    flat = z(4 * 264 + 8, t=BF)
+    for call in (
+            lambda: afd.rms_norm(x[0], w), lambda: afd.rms_norm(x.t(), w), lambda: afd.rms_norm(x[:, ::2], w[:128].contiguous()),
+            lambda: afd.rms_norm(x, w[:128]), lambda: afd.rms_norm(x, w, x[:3]), lambda: afd.rms_norm(x, w, eps=0.0),
+            lambda: afd.rms_norm(x, w, eps=float("nan")), lambda: afd.rms_norm(z(4, 252, t=BF), w[:252]),
+            lambda: afd.rms_norm(z(4, 136, t=BF), w[:136], dtype=F8), lambda: afd.rms_norm(z(2, 16392, t=BF), z(16392)),
+            lambda: afd.rms_norm(x, w, out=z(4, 256)), lambda: afd.rms_norm(x, w, out=z(3, 256, t=BF)),
+            lambda: afd.rms_norm(x, w, out_scales=z(4, 2)), lambda: afd.rms_norm(x, w, residual_out=x),
+            lambda: afd.rms_norm(x, w, x, residual_out=z(4, 256)), lambda: afd.rms_norm(x, w, dtype=F8, out_scales=z(4, 1)),
+            lambda: afd.rms_norm(flat[1:1025].view(4, 256), w), lambda: afd.rms_norm(x, flat[1:257]),
+            lambda: afd.rms_norm(flat[:4 * 260].view(4, 260)[:, :256], w), lambda: afd.rms_norm(x[:1].expand(4, 256), w),
+            lambda: afd.rms_norm(x, w.cpu()), lambda: afd.rms_norm(x, w, x.cpu()),
+            lambda: afd.rms_norm_grad(x[:3], x, w, z(4)), lambda: afd.rms_norm_grad(x, x, w, z(3)),
+            lambda: afd.rms_norm_grad(x.float(), x, w, z(4)), lambda: afd.rms_norm_grad(x, x, w, z(4), grad_residual=z(4, 256)),
+            lambda: afd.rms_norm_grad(x, x, w, z(4), out=z(4, 256)),
+            lambda: afd.route_tokens(l, 0), lambda: afd.route_tokens(l, 9), lambda: afd.route_tokens(l[0], 2),
+            lambda: afd.route_tokens(l.t(), 2), lambda: afd.route_tokens(z(2, 513), 2), lambda: afd.route_tokens(z(2, 0), 1),
+            lambda: afd.route_tokens(l, 2, scoring="tanh"), lambda: afd.route_tokens(l, 2, scale=float("inf")),
+            lambda: afd.route_tokens(l, 2, bias=z(7)), lambda: afd.route_tokens(l, 2, bias=z(8, t=BF)),
+            lambda: afd.route_tokens(l, 2, live=z(4)), lambda: afd.route_tokens(l, 2, live=z(3, t=torch.bool)),
+            lambda: afd.route_tokens(l, 2, ids=z(4, 2)), lambda: afd.route_tokens(l, 2, weights=z(4, 3)),
+            lambda: afd.route_tokens(l[:1].expand(4, 8), 2),
+            lambda: afd.route_tokens_grad(z(4, 2), l, ids.long()), lambda: afd.route_tokens_grad(z(4, 3), l, ids),
+            lambda: afd.route_tokens_grad(z(4, 2), l, ids, out=z(4, 9)), lambda: afd.route_tokens_grad(z(4, 2), l, ids[:, 0]),
+            lambda: afd.balance_loss(l, ids[:3]), lambda: afd.balance_loss(l, ids, coefficient=float("nan")),
+            lambda: afd.balance_loss(l, z(4, 33, t=torch.int32)), lambda: afd.balance_loss_grad(z(1), l, ids, z(8)),
+            lambda: afd.balance_loss_grad(z(), l, ids, z(7)), lambda: afd.balance_loss_grad(torch.zeros(()), l, ids, z(8))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: afd.rms_norm(x.half(), w), lambda: afd.rms_norm(x, w.half()), lambda: afd.rms_norm(x, w, x.half()),
+                 lambda: afd.rms_norm(x, w, dtype=torch.float16), lambda: afd.route_tokens(l.double(), 2),
+                 lambda: afd.route_tokens(l, 2.5), lambda: afd.balance_loss(l.half(), ids)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: afd.rms_norm(x, w, x, out=x, residual_out=x), lambda: afd.rms_norm(x, w, out=w.expand(1, 256)),
+                 lambda: afd.rms_norm_grad(x, x, w, z(4), out=x)):
+        with pytest.raises((ValueError, afd.AfdError)):
+            call()
+    buf = afd.Buffer(1, 1, 8, 2, 256, capacity=4)
+    for call in (lambda: buf.source_norm(1, x, w), lambda: buf.source_norm(0, z(5, 256, t=BF), w),
+                 lambda: buf.source_norm(0, z(4, 128, t=BF), w[:128]), lambda: buf.source_route(0, z(4, 9)),
+                 lambda: buf.source_route(-1, l), lambda: buf.source_route(0, l.cpu())):
+        with pytest.raises(ValueError):
+            call()
+    assert buf.source_norm(0, x, w).rows.shape == (4, 256) and buf.source_route(0, l).ids.shape == (4, 2)

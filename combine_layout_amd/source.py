@@ -261,7 +261,8 @@ def rms_norm(x, weight, residual=None, *, eps=1e-6, dtype=torch.bfloat16, out=No
     Differentiable by x, residual and weight with bfloat16 rows in new memory, outside of
     a capture; the rounding of h counts as none, and x and residual share one gradient.
     Runs on x's device and its current stream."""
-    _plain("rms_norm", out, out_scales, residual_out)
+    if out is not None or out_scales is not None or residual_out is not None:
+        _plain("rms_norm", out, out_scales, residual_out)
     if _asks(x, weight, residual):
         _recorded("rms_norm", x.device, out is not None, out_scales is not None, residual_out is not None,
                   dtype is not torch.bfloat16)
@@ -405,7 +406,8 @@ def route_tokens(logits, topk, *, scoring="softmax", bias=None, renormalize=True
 
     The weights are differentiable by the logits, outside of a capture; the choice has no
     gradient.  Runs on the logits' device and its current stream."""
-    _plain("route_tokens", bias, live, ids, weights)
+    if bias is not None or live is not None or ids is not None or weights is not None:
+        _plain("route_tokens", bias, live, ids, weights)
     if _asks(logits):
         _recorded("route_tokens", logits.device, ids is not None, weights is not None)
         return Routes(*_RouteTokens.apply(logits, topk, scoring, bias, renormalize, scale, live))

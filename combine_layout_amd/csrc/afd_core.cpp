@@ -448,7 +448,7 @@ BalanceSpace balance_space(const afd_route_config &c, int64_t rows)
     s.totals = s.count + align256(g * E * 4);
     s.part = s.totals + align256(g * 8);
     s.done = s.part + align256((E + 15) / 16 * 8);
-    s.total = rows > 0 ? s.done + 256 : 0;
+    s.total = g > 1 ? s.done + 256 : 0;
     return s;
 }
 
@@ -1056,12 +1056,12 @@ afd_status afd_balance(const afd_route_config *cfg, int64_t rows, const void *lo
     Span in[2] = {};
     if (rows > 0) {
         if (!logits_ok(*cfg, logits, logit_stride) || !ids || !aligned(ids, 4)) return AFD_E_ARG;
-        if (!workspace || !aligned(workspace, 256)) return AFD_E_ARG;
+        if (need.total > 0 && (!workspace || !aligned(workspace, 256))) return AFD_E_ARG;
         if (workspace_bytes < need.total) return AFD_E_CAPACITY;
         in[0] = span(logits, rows, logit_stride, cfg->num_experts, element_of(cfg->dtype));
         in[1] = span(ids, rows, cfg->topk, cfg->topk, 4);
     }
-    const Span to[4] = {{loss, 4}, {counts, E * 4}, {slope, E * 4}, {rows > 0 ? workspace : nullptr, need.total}};
+    const Span to[4] = {{loss, 4}, {counts, E * 4}, {slope, E * 4}, {workspace, need.total}};
     for (int i = 0; i < 4; ++i) {
         for (int j = 0; j < i; ++j)
             if (overlap(to[i], to[j])) return AFD_E_ARG;
@@ -1078,7 +1078,7 @@ afd_status afd_balance(const afd_route_config *cfg, int64_t rows, const void *lo
     p.groups = balance_groups(rows, cfg->num_experts);
     p.wide = balance_wide(rows, cfg->num_experts);
     char *ws = static_cast<char *>(workspace);
-    if (rows > 0) {
+    if (need.total > 0) {
         p.share = reinterpret_cast<float *>(ws + need.share);
         p.count = reinterpret_cast<int32_t *>(ws + need.count);
         p.totals = reinterpret_cast<int32_t *>(ws + need.totals);

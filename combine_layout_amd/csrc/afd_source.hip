@@ -1086,11 +1086,22 @@ struct BalanceArgs {
     float *share;
     int32_t *count, *totals;
     uint32_t *done;
+    float *loss, *slope;   // with one workgroup
+    int32_t *counts;
+    float coefficient;
 };
 
+// The loss and the slope from an expert's sums, by the first E threads of a workgroup.
+__device__ __forceinline__ float slope_of(float coefficient, int E, int count, int tokens, int chosen)
+{
+    const double n = double(tokens) * double(chosen);
+    return n > 0.0 ? float(double(coefficient) * double(E) * double(count) / n) : 0.f;
+}
+
 // Sums of the shares over tokens in registers, counts in LDS; a token's logits and ids are
-// on their way while the one before is worked on.
-template <bool L32, int LANES, int V, bool VEC, int THREADS>
+// on their way while the one before is worked on.  SOLO: one workgroup has all tokens, and
+// ends with the results.
+template <bool L32, int LANES, int V, bool VEC, int THREADS, bool SOLO>
 __global__ __launch_bounds__(THREADS) void k_balance(BalanceArgs b)
 {
     using R = Row<L32, LANES, V, VEC>;
@@ -1100,7 +1111,7 @@ __global__ __launch_bounds__(THREADS) void k_balance(BalanceArgs b)
     __shared__ float join[kRows][LANES * V];
     for (int e = threadIdx.x; e < LANES * V; e += THREADS) hist[e] = 0;
     if (threadIdx.x < 2) total[threadIdx.x] = 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *b.done = 0;   // for the launch behind this one
+    if (!SOLO && blockIdx.x == 0 && threadIdx.x == 0) *b.done = 0;   // for the launch behind this one
     __syncthreads();
     float acc[V] = {};
     int tokens = 0, chosen = 0;
@@ -1125,6 +1136,30 @@ __global__ __launch_bounds__(THREADS) void k_balance(BalanceArgs b)
 #pragma unroll
     for (int i = 0; i < V; ++i) join[threadIdx.x / LANES][R::expert(i)] = acc[i];
     __syncthreads();
+    if constexpr (SOLO) {
+        static_assert(THREADS >= kMaxExperts, "a thread for every expert");
+        __shared__ double part[THREADS / kWave];
+        const int e = threadIdx.x;
+        double loss = 0.0;
+        if (e < a.E) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) s += join[i][e];
+            const float slope = slope_of(b.coefficient, a.E, hist[e], total[0], total[1]);
+            b.counts[e] = hist[e];
+            b.slope[e] = slope;
+            loss = double(slope) * double(s);
+        }
+        for (int d = 1; d < kWave; d *= 2) loss += __shfl_xor(loss, d);
+        if (e % kWave == 0) part[e / kWave] = loss;
+        __syncthreads();
+        if (e != 0) return;
+        loss = 0.0;
+#pragma unroll
+        for (int i = 0; i < THREADS / kWave; ++i) loss += part[i];
+        b.loss[0] = float(loss);
+        return;
+    }
     for (int e = threadIdx.x; e < a.E; e += THREADS) {
         float s = 0.f;
 #pragma unroll
@@ -1196,8 +1231,7 @@ __global__ __launch_bounds__(256) void k_balance_join(BalanceJoinArgs a)
         all.x += totals[i].x;
         all.y += totals[i].y;
     }
-    const double n = double(all.x) * double(all.y);
-    const float slope = n > 0.0 ? float(double(a.coefficient) * double(a.E) * double(c) / n) : 0.f;
+    const float slope = slope_of(a.coefficient, a.E, c, all.x, all.y);
     if (e < a.E) {
         a.counts[e] = c;
         a.slope[e] = slope;
@@ -1383,8 +1417,9 @@ template <bool L32, int LANES, int V, bool VEC>
 struct BalanceLaunch {
     static int run(const BalanceArgs &a, int groups, bool wide, hipStream_t st)
     {
-        if (wide) hipLaunchKernelGGL((k_balance<L32, LANES, V, VEC, 1024>), dim3(unsigned(groups)), dim3(1024), 0, st, a);
-        else hipLaunchKernelGGL((k_balance<L32, LANES, V, VEC, 256>), dim3(unsigned(groups)), dim3(256), 0, st, a);
+        if (groups == 1) hipLaunchKernelGGL((k_balance<L32, LANES, V, VEC, 1024, true>), dim3(1), dim3(1024), 0, st, a);
+        else if (wide) hipLaunchKernelGGL((k_balance<L32, LANES, V, VEC, 1024, false>), dim3(unsigned(groups)), dim3(1024), 0, st, a);
+        else hipLaunchKernelGGL((k_balance<L32, LANES, V, VEC, 256, false>), dim3(unsigned(groups)), dim3(256), 0, st, a);
         return launched();
     }
 };
@@ -1441,9 +1476,9 @@ int be_launch_balance(const BalancePlan &p, void *stream)
         hipLaunchKernelGGL(k_balance_none, dim3(1), dim3(kMaxExperts), 0, st, p.loss, p.slope, p.counts, p.r.E);
         return launched();
     }
-    BalanceArgs a{route_args(p.r), p.share, p.count, p.totals, p.done};
+    BalanceArgs a{route_args(p.r), p.share, p.count, p.totals, p.done, p.loss, p.slope, p.counts, p.coefficient};
     const int rc = by_logits<BalanceLaunch>(p.r, a, p.groups, p.wide, st);
-    if (rc != 0) return rc;
+    if (rc != 0 || p.groups == 1) return rc;
     BalanceJoinArgs j{p.share, p.count, p.totals, p.part, p.done, p.loss, p.slope, p.counts, p.r.E, p.groups, p.coefficient};
     hipLaunchKernelGGL(k_balance_join, dim3(unsigned((p.r.E + 15) / 16)), dim3(256), 0, st, j);
     return launched();

@@ -458,9 +458,9 @@ def _balance(logits, ids, scoring, coefficient):
     loss = torch.empty((), dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int32, device=dev)
     slope = torch.empty_like(counts, dtype=torch.float32)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = _launch(dev, nat.load().afd_balance, cfg, T, logits.data_ptr(), ls, ids.data_ptr(), coefficient, loss.data_ptr(),
-                 counts.data_ptr(), slope.data_ptr(), ws.data_ptr(), need)
+                 counts.data_ptr(), slope.data_ptr(), ws.data_ptr() if need else None, need)
     if st:
         nat.check(st, "balance_loss")
     return Balance(loss, counts, slope)

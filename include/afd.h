@@ -718,7 +718,7 @@ afd_status afd_route(const afd_route_config *cfg, int64_t rows, const void *logi
 afd_status afd_route_grad(const afd_route_config *cfg, int64_t rows, const float *grad, const void *logits,
                           int64_t logit_stride, const int32_t *ids, void *dlogits, void *stream);
 
-/* afd_balance_query: workspace bytes of afd_balance.  Pure host computation.  Errors:
+/* afd_balance_query: workspace bytes of afd_balance (0 for few rows).  Pure host computation.  Errors:
  * AFD_E_ARG, AFD_E_SHAPE. */
 afd_status afd_balance_query(const afd_route_config *cfg, int64_t rows, size_t *workspace_bytes);
 
@@ -736,7 +736,7 @@ afd_status afd_balance_query(const afd_route_config *cfg, int64_t rows, size_t *
  *   counts     device [E] int32
  *   slope      device [E] FP32, for afd_balance_grad
  *   workspace  device, at least afd_balance_query bytes, 256-byte aligned; in use until the
- *              call's work has run
+ *              call's work has run (NULL where there are none)
  * loss, counts and slope are written also where rows is 0.
  * Errors: AFD_E_ARG (pointers, alignment, rows, stride, coefficient not finite), AFD_E_SHAPE,
  * AFD_E_CAPACITY (workspace), AFD_E_HIP.

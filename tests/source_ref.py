@@ -149,8 +149,8 @@ def balance(logits, ids, scoring, coefficient):
     p = shares(logits, scoring) * on[:, None]
     loss = (p.sum(0) * slope).sum()
     rows = p.shape[0]
-    # a lane's tokens one after another, then up to 16 groups; the join is in 64 bits
-    terms = rows / 256 + 1 + 16
+    # a lane's tokens one after another, then up to 64 groups of a workgroup; the join is in 64 bits
+    terms = rows / 256 + 6 + 64
     worst = float((spread(logits)).max()) if rows else 0.0
     return loss, (terms + worst + 4) * U * (p.sum(0) * slope.abs()).sum() + TINY, counts, slope, p, on
 

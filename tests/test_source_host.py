@@ -232,7 +232,8 @@ ROWS_BAD = [dict(rows=-1), dict(rows=1 << 24), dict(l=None), dict(l=L + 2), dict
     (route_grad, dict(dl=DL + 2)), (route_grad, dict(dl=L)), (route_grad, dict(dl=G)), (route_grad, dict(dl=IDS - 4)),
     (balance, dict(ids=None)), (balance, dict(loss=None)), (balance, dict(loss=LOSS + 1)), (balance, dict(counts=None)),
     (balance, dict(slope=None)), (balance, dict(slope=COUNTS)), (balance, dict(loss=SLOPE + 4)), (balance, dict(counts=L)),
-    (balance, dict(ws=None)), (balance, dict(ws=WS + 128)), (balance, dict(ws=IDS)), (balance, dict(ws=SLOPE)),
+    (balance, dict(rows=1000, ws=None)), (balance, dict(rows=1000, ws=WS + 128)), (balance, dict(rows=1000, ws=IDS)),
+    (balance, dict(rows=1000, ws=SLOPE)),
     (balance, dict(co=NAN)), (balance, dict(co=INF)),
     (balance_grad, dict(g=None)), (balance_grad, dict(slope=None)), (balance_grad, dict(slope=SLOPE + 2)),
     (balance_grad, dict(ids=IDS + 2)), (balance_grad, dict(dl=None)), (balance_grad, dict(dl=L)), (balance_grad, dict(dl=SLOPE)),
@@ -264,12 +265,17 @@ def test_routes_without_rows(lib):
 
 
 @pytest.mark.parametrize("E,each", [(1, 16), (96, 16), (128, 16), (129, 8), (256, 8), (257, 4), (512, 4)])
-@pytest.mark.parametrize("rows", [1, 16, 17, 4096, 8192, 8193, ROWS])
+@pytest.mark.parametrize("rows", [1, 96, 97, 192, 193, 384, 385, 513, 4096, 8192, 8193, ROWS])
 def test_balance_workspace(lib, E, each, rows):
     """The first launch's sums, counts and totals, the loss's parts and the count of the done."""
     log(lib)
     c, need = rcfg(num_experts=E, topk=1), ctypes.c_size_t()
     assert lib.afd_balance_query(ctypes.byref(c), rows, ctypes.byref(need)) == 0
+    if rows <= 24 * each:                            # one workgroup's
+        assert need.value == 0
+        assert balance(lib, c, rows, ws=None, wsb=0) == 0
+        assert " groups=1 " in log(lib)[0]
+        return
     groups = min(-(-rows // each), 256)
     up = lambda v: -(-v // 256) * 256  # noqa: E731
     sizes = [up(groups * E * 4), up(groups * E * 4), up(groups * 8), up(-(-E // 16) * 8), 256]

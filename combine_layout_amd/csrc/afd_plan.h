@@ -244,9 +244,13 @@ struct NormPlan {
 };
 
 // Workgroups of the norm's gradient: each sums dweight over its rows in registers and
-// leaves one partial row of float32, and a second launch adds these up.
-constexpr int kNormGradGroups = 512;
-inline int norm_grad_groups(int64_t rows) { return int(std::min<int64_t>((rows + 3) / 4, kNormGradGroups)); }
+// leaves one partial row of float32, and a second launch adds these up.  Few rows (0 here)
+// take one launch, in which other workgroups read them again for dweight.
+constexpr int kNormGradGroups = 512, kNormGradFew = 512;
+inline int norm_grad_groups(int64_t rows)
+{
+    return rows <= kNormGradFew ? 0 : int(std::min<int64_t>((rows + 3) / 4, kNormGradGroups));
+}
 
 struct NormGradPlan {
     int H = 0;

@@ -259,11 +259,43 @@ struct NormGradArgs {
     const void *g, *gr, *h, *w;
     const float *rstd;
     void *dh;
-    float *part;
+    float *part, *dw;
     int64_t hs;
-    int rows, H;
+    int rows, H, groups;   // workgroups of rows; with dw, those behind them have 64 columns of it each
     bool w32;
 };
+
+// 64 columns of dweight over all rows, eight a thread.
+template <bool H32, int THREADS>
+__device__ __forceinline__ void norm_grad_columns(const NormGradArgs &a, int block)
+{
+    constexpr int kSlices = THREADS / 8;
+    __shared__ f32x4 join[kSlices][16];
+    const int slice = threadIdx.x / 8, c = block * 64 + threadIdx.x % 8 * 8;
+    float s[8] = {};
+    if (c < a.H) {
+#pragma unroll 4
+        for (int64_t row = slice; row < a.rows; row += kSlices) {
+            Eight<false> g;
+            Eight<H32> h;
+            g.load(a.g, row * a.H + c);
+            h.load(a.h, row * a.hs + c);
+            const float rstd = a.rstd[row];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = fmaf(g.get(j), h.get(j) * rstd, s[j]);
+        }
+    }
+    join[slice][threadIdx.x % 8 * 2] = f32x4{s[0], s[1], s[2], s[3]};
+    join[slice][threadIdx.x % 8 * 2 + 1] = f32x4{s[4], s[5], s[6], s[7]};
+    __syncthreads();
+    const int one = block * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && one < a.H) {
+        float t = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < kSlices; ++i) t += reinterpret_cast<const float *>(join[i])[threadIdx.x];
+        a.dw[one] = t;
+    }
+}
 
 // dh of every row, and the workgroup's sum of grad * u over its rows, which stays in
 // registers from the first row to the last.
@@ -272,10 +304,14 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm_grad(NormGr
 {
     constexpr int kRows = WPR >= 4 ? 1 : 4 / WPR;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = (wave % WPR) * kWave + lane, runs = a.H / 8;
+    if (a.dw && int(blockIdx.x) >= a.groups) {
+        norm_grad_columns<H32, (WPR > 4 ? WPR * kWave : 256)>(a, int(blockIdx.x) - a.groups);
+        return;
+    }
     __shared__ float sum[2][WPR];
     float dw[C][8] = {};
     int turn = 0;
-    for (int64_t row = int64_t(blockIdx.x) * kRows + wave / WPR; row < a.rows; row += int64_t(gridDim.x) * kRows) {
+    for (int64_t row = int64_t(blockIdx.x) * kRows + wave / WPR; row < a.rows; row += int64_t(a.groups) * kRows) {
         Eight<false> g[C];
         Eight<H32> h[C], gr[C];
         Weights w[C];
@@ -1327,9 +1363,20 @@ int norm_out(const NormArgs &a, bool out8, hipStream_t st)
 }
 
 template <bool H32, int WPR, int C>
-int norm_grad_as(const NormGradArgs &a, int groups, hipStream_t st)
+int norm_grad_as(NormGradArgs a, int groups, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_norm_grad<H32, WPR, C>), dim3(unsigned(groups)), dim3(WPR > 4 ? WPR * kWave : 256), 0, st, a);
+    constexpr int each = WPR >= 4 ? 1 : 4 / WPR;
+    a.groups = a.part ? groups : std::min((a.rows + each - 1) / each, kNormGradGroups * 4 / each);
+    const int columns = a.dw ? (a.H + 63) / 64 : 0;
+    const dim3 threads(WPR > 4 ? WPR * kWave : 256);
+    if (columns > 0 && a.dh == a.g) {   // dh in grad's place: dweight first
+        NormGradArgs c = a;
+        c.groups = 0;
+        hipLaunchKernelGGL((k_norm_grad<H32, WPR, C>), dim3(unsigned(columns)), threads, 0, st, c);
+        a.dw = nullptr;
+        if (launched() != 0) return 1;
+    }
+    hipLaunchKernelGGL((k_norm_grad<H32, WPR, C>), dim3(unsigned(a.groups + (a.dw ? columns : 0))), threads, 0, st, a);
     return launched();
 }
 
@@ -1449,12 +1496,12 @@ int be_launch_norm(const NormPlan &p, void *stream)
 int be_launch_norm_grad(const NormGradPlan &p, void *stream)
 {
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (p.groups > 0) {
-        NormGradArgs a{p.g, p.gr, p.h, p.w, p.rstd, p.dh, p.dw ? p.part : nullptr, p.hs, int(p.rows), p.H, p.w32};
+    const bool join = p.dw && p.groups > 0;   // else the workgroups of the first launch have dweight as well
+    if (p.rows > 0) {
+        NormGradArgs a{p.g, p.gr, p.h, p.w, p.rstd, p.dh, join ? p.part : nullptr, join ? nullptr : p.dw, p.hs, int(p.rows), p.H, 0, p.w32};
         const int rc = p.h32 ? norm_grad_of<true>(a, p.groups, st) : norm_grad_of<false>(a, p.groups, st);
-        if (rc != 0) return rc;
+        if (rc != 0 || !join) return rc;
     }
-    if (!p.dw) return 0;
     hipLaunchKernelGGL(k_norm_grad_join, dim3(unsigned((p.H + 63) / 64)), dim3(1024), 0, st, p.part, p.dw, p.H, p.groups);
     return launched();
 }

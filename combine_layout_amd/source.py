@@ -288,8 +288,11 @@ def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight
         out = _like(h, h.dtype)
     dw = ws = pd = pw = None
     if weight_grad:
-        dw, ws = torch.empty(H, dtype=torch.float32, device=dev), torch.empty(need, dtype=torch.uint8, device=dev)
-        pd, pw = dw.data_ptr(), ws.data_ptr()
+        dw = torch.empty(H, dtype=torch.float32, device=dev)
+        pd = dw.data_ptr()
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            pw = ws.data_ptr()
     st = _launch(dev, nat.load().afd_norm_grad, cfg, T, grad.data_ptr(),
                  None if grad_residual is None else grad_residual.data_ptr(), h.data_ptr(), hs, weight.data_ptr(),
                  rstd.data_ptr(), out.data_ptr(), pd, pw, need if weight_grad else 0)

@@ -638,8 +638,8 @@ afd_status afd_norm(const afd_norm_config *cfg, int64_t rows, const void *x, int
                     int64_t residual_stride, const void *weight, void *out, float *out_scales, void *residual_out,
                     int64_t residual_out_stride, float *rstd, void *stream);
 
-/* afd_norm_grad_query: workspace bytes of afd_norm_grad with a dweight (without, it
- * takes none).  Pure host computation.  Errors: AFD_E_ARG, AFD_E_SHAPE. */
+/* afd_norm_grad_query: workspace bytes of afd_norm_grad with a dweight (0 for few rows;
+ * without a dweight it takes none).  Pure host computation.  Errors: AFD_E_ARG, AFD_E_SHAPE. */
 afd_status afd_norm_grad_query(const afd_norm_config *cfg, int64_t rows, size_t *workspace_bytes);
 
 /*

@@ -31,7 +31,7 @@ def norm(x, weight, residual, eps):
     return h, rstd, h * rstd[:, None] * weight.double(), rel
 
 
-def norm_grad(grad, h, weight, rstd, grad_residual, groups):
+def norm_grad(grad, h, weight, rstd, grad_residual):
     """(dh, its bound, dweight, its bound) of float64 inputs."""
     H = h.shape[1]
     u, a = h * rstd[:, None], grad * weight
@@ -44,8 +44,9 @@ def norm_grad(grad, h, weight, rstd, grad_residual, groups):
         dh = dh + grad_residual
     tol = tol + 3 * U * dh.abs()
     rows = grad.shape[0]
-    # a workgroup's rows one after another, four wavefronts, then the workgroups
-    terms = rows / max(groups, 1) + 1 + 4 + groups / 16 + 1 + 16
+    # up to 512 rows: every 32nd row in a thread, then 32 threads (128th and 128 where wide); more: a
+    # workgroup's rows (of up to 512) one after another, four wavefronts, every 64th workgroup, then 64 sums
+    terms = rows / 32 + 1 + 128 if rows <= 512 else rows / min(-(-rows // 4), 512) + 1 + 4 + 512 / 64 + 64
     return dh, tol, (grad * u).sum(0), (terms + 3) * U * (grad * u).abs().sum(0)
 
 

@@ -180,7 +180,7 @@ def test_norm_grad(H, ht, wt, T, res):
     dh, dw = afd.rms_norm_grad(dy.cuda(), h.cuda(), w.cuda(), rstd.cuda(),
                                grad_residual=None if dr is None else dr.cuda())
     want, tol, wantw, tolw = ref.norm_grad(dy.double(), h.double(), w.double(), rstd.double(),
-                                           None if dr is None else dr.double(), -(-T // 4))
+                                           None if dr is None else dr.double())
     ref.check(dh, want, ref.rounded(want, tol, ht), "dh")
     ref.check(dw, wantw, tolw + ref.U * wantw.abs(), "dweight")
     assert dh.dtype is ht and dw.dtype is F32
@@ -191,7 +191,8 @@ def test_norm_grad(H, ht, wt, T, res):
     assert none is None and torch.equal(alone, dh)
 
 
-@pytest.mark.parametrize("T,H", [(4097, 2048), (2500, 4096), (3001, 264), (600, 16384)])
+@pytest.mark.parametrize("T,H", [(4097, 2048), (2500, 4096), (3001, 264), (600, 16384), (512, 2048), (513, 2048), (512, 16384),
+                                 (301, 40), (511, 4104)])
 def test_norm_grad_many_rows(T, H):
     afd = _afd()
     _print("norm grad rows", T, H)
@@ -199,7 +200,7 @@ def test_norm_grad_many_rows(T, H):
     h, w, dy = _rand(g, T, H, dtype=BF), 1 + _rand(g, H, std=0.3), _rand(g, T, H, dtype=BF)
     rstd = (1 / torch.sqrt(h.double().square().mean(1) + 1e-6)).float()
     dh, dw = afd.rms_norm_grad(dy.cuda(), _gapped(h, 8), w.cuda(), rstd.cuda())
-    want, tol, wantw, tolw = ref.norm_grad(dy.double(), h.double(), w.double(), rstd.double(), None, min(-(-T // 4), 512))
+    want, tol, wantw, tolw = ref.norm_grad(dy.double(), h.double(), w.double(), rstd.double(), None)
     ref.check(dh, want, ref.rounded(want, tol, BF), "dh")
     ref.check(dw, wantw, tolw + ref.U * wantw.abs(), "dweight")
 

@@ -399,7 +399,7 @@ afd_status check_norm(const afd_norm_config *c, int64_t rows)
 
 size_t norm_grad_workspace(const afd_norm_config &c, int64_t rows)
 {
-    return align256(size_t(norm_grad_groups(rows)) * size_t(c.hidden) * 4);
+    return align256(size_t(norm_grad_groups(rows, c.hidden)) * size_t(c.hidden) * 4);
 }
 
 afd_status check_route(const afd_route_config *c, int64_t rows)
@@ -987,7 +987,7 @@ afd_status afd_norm_grad(const afd_norm_config *cfg, int64_t rows, const void *g
     p.dh = dh;
     p.dw = dweight;
     p.part = static_cast<float *>(workspace);
-    p.groups = norm_grad_groups(rows);
+    p.groups = norm_grad_groups(rows, cfg->hidden);
     return be_launch_norm_grad(p, stream) == 0 ? AFD_OK : AFD_E_HIP;
 }
 

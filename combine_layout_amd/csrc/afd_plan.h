@@ -245,11 +245,14 @@ struct NormPlan {
 
 // Workgroups of the norm's gradient: each sums dweight over its rows in registers and
 // leaves one partial row of float32, and a second launch adds these up.  Few rows (0 here)
-// take one launch, in which other workgroups read them again for dweight.
-constexpr int kNormGradGroups = 512, kNormGradFew = 512;
-inline int norm_grad_groups(int64_t rows)
+// take one launch, in which other workgroups read them again for dweight (us, one and two
+// launches, BF16: 2048 columns, 512 rows 4.0 and 7.3, 1024 6.4 and 9.0, 2048 14.8 and 12.2;
+// 8192, 1024 rows 15.9 and 18.8, 1500 24.8 and 21.1; 16384, 512 rows 18.3 and 18.4, 700 22.9
+// and 21.1).
+constexpr int kNormGradGroups = 512;
+inline int norm_grad_groups(int64_t rows, int H)
 {
-    return rows <= kNormGradFew ? 0 : int(std::min<int64_t>((rows + 3) / 4, kNormGradGroups));
+    return rows <= (H <= 8192 ? 1024 : 512) ? 0 : int(std::min<int64_t>((rows + 3) / 4, kNormGradGroups));
 }
 
 struct NormGradPlan {

@@ -44,9 +44,9 @@ def norm_grad(grad, h, weight, rstd, grad_residual):
         dh = dh + grad_residual
     tol = tol + 3 * U * dh.abs()
     rows = grad.shape[0]
-    # up to 512 rows: every 32nd row in a thread, then 32 threads (128th and 128 where wide); more: a
+    # up to 1024 rows: every 32nd row in a thread, then 32 threads (128th and 128 where wide); more: a
     # workgroup's rows (of up to 512) one after another, four wavefronts, every 64th workgroup, then 64 sums
-    terms = rows / 32 + 1 + 128 if rows <= 512 else rows / min(-(-rows // 4), 512) + 1 + 4 + 512 / 64 + 64
+    terms = rows / 32 + 1 + 128 if rows <= 1024 else rows / min(-(-rows // 4), 512) + 1 + 4 + 512 / 64 + 64
     return dh, tol, (grad * u).sum(0), (terms + 3) * U * (grad * u).abs().sum(0)
 
 

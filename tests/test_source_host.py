@@ -118,14 +118,14 @@ def test_norm_without_rows(lib):
     assert lib.afd_norm_grad_query(ctypes.byref(ncfg()), 1, None) == nat.AFD_E_ARG
 
 
-@pytest.mark.parametrize("rows", [1, 100, 512, 513, 2049, ROWS])
+@pytest.mark.parametrize("rows", [1, 100, 512, 513, 1024, 1025, 2049, ROWS])
 @pytest.mark.parametrize("kw", [dict(), dict(hidden=16384), dict(hidden=8), dict(residual_dtype=FP32), dict(residual_dtype=NONE),
                                 dict(residual_dtype=NONE, x_dtype=FP32)])
 def test_norm_grad_workspace(lib, rows, kw):
     log(lib)
     c, need = ncfg(**kw), ctypes.c_size_t()
     assert lib.afd_norm_grad_query(ctypes.byref(c), rows, ctypes.byref(need)) == 0
-    groups = 0 if rows <= 512 else min(-(-rows // 4), 512)
+    groups = 0 if rows <= (1024 if c.hidden <= 8192 else 512) else min(-(-rows // 4), 512)
     assert need.value == -(-groups * c.hidden * 4 // 256) * 256
     if groups:
         assert grad(lib, c, rows, wsb=need.value - 1) == nat.AFD_E_CAPACITY and log(lib) == []
@@ -139,8 +139,8 @@ def test_norm_grad_workspace(lib, rows, kw):
 @pytest.mark.parametrize("args", [
     dict(rows=-1), dict(rows=1 << 24), dict(g=None), dict(g=X + 8), dict(gr=R + 4), dict(h=None), dict(h=OUT + 8),
     dict(hs=255), dict(hs=260), dict(w=None), dict(w=W + 2), dict(rstd=None), dict(rstd=RSTD + 2), dict(dh=None),
-    dict(dh=RO + 8), dict(dw=DW + 2), dict(rows=600, ws=None), dict(rows=600, ws=WS + 16), dict(dh=OUT), dict(dh=X + 16), dict(dh=R - 16),
-    dict(dw=RO), dict(dw=W), dict(rows=600, ws=RO), dict(rows=600, ws=X), dict(dh=RSTD)])
+    dict(dh=RO + 8), dict(dw=DW + 2), dict(rows=1100, ws=None), dict(rows=1100, ws=WS + 16), dict(dh=OUT), dict(dh=X + 16), dict(dh=R - 16),
+    dict(dw=RO), dict(dw=W), dict(rows=1100, ws=RO), dict(rows=1100, ws=X), dict(dh=RSTD)])
 def test_norm_grad_arguments_refused(lib, args):
     log(lib)
     assert grad(lib, ncfg(), **args) == nat.AFD_E_ARG

@@ -422,16 +422,10 @@ __global__ __launch_bounds__(1024) void k_norm_grad_join(const float *part, floa
 
 constexpr float kMinusInf = -__builtin_inff();
 
-// exp(x) for x <= 0, to about one float32 step; the argument's product with log2(e) is
-// kept in two parts, since its rounding alone would cost |x| steps.  Below -120, and for
-// a NaN, it is 0.
-__device__ __forceinline__ float exp_neg(float x)
-{
-    x = fmaxf(x, -120.f);
-    const float hi = x * 1.44269504f, lo = fmaf(x, 1.92596300e-8f, fmaf(x, 1.44269504f, -hi));
-    const float e = __builtin_amdgcn_exp2f(hi);
-    return fmaf(e, lo * 0.693147181f, e);
-}
+// exp(x) for x <= 0.  The argument's rounding costs |x| roundings of the result, which
+// terms that are small beside 1 can bear; a second part of the product with log2(e) would
+// be three instructions more of every logit, where the arithmetic bounds.
+__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 // 1 / d for d in [1, 2]: the hardware's reciprocal and one step of Newton's.
 __device__ __forceinline__ float inverse(float d)
@@ -439,6 +433,15 @@ __device__ __forceinline__ float inverse(float d)
     const float r = __builtin_amdgcn_rcpf(d);
     return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
+
+// Integers in the order of the floats they stand for (the two zeros are one).
+constexpr int kNoKey = int(0x807FFFFF);   // minus infinity
+__device__ __forceinline__ int key_of(float v)
+{
+    const int b = __builtin_bit_cast(int, v + 0.f);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7FFFFFFF)); }
 
 struct RouteArgs {
     const void *l;
@@ -507,7 +510,8 @@ struct Row {
                 float x;
                 if constexpr (L32) x = q[i / 4][i & 3];
                 else x = from_bf16(i & 1 ? q[i / 4][(i & 3) / 2] >> 16 : q[i / 4][(i & 3) / 2] & 0xFFFFu);
-                v[i] = expert(i) < a.E && x == x ? x : kMinusInf;
+                // (whole runs of four are inside or behind where they are loaded whole)
+                v[i] = expert(VEC ? i & ~3 : i) < a.E && x == x ? x : kMinusInf;
             }
         }
     };
@@ -547,7 +551,7 @@ struct Row {
         float m = v[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-        return across<LANES>(m, Max());
+        return of_key(across<LANES>(key_of(m), MaxInt()));   // as integers: no step has to look for NaNs
     }
 
     __device__ static __forceinline__ float total(const float *v)
@@ -566,7 +570,7 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float e = exp_neg(v[i] - top);
-            t[i] = v[i] == top ? 1.f : e;
+            t[i] = v[i] == -kMinusInf ? 1.f : e;
         }
         return total(t);
     }
@@ -583,9 +587,10 @@ struct Row {
             left[i] = (v[i] >= 0.f ? z : 1.f) * d;
         }
         if (__any(m < -40.f)) {
+            const float top = m == kMinusInf ? -kMinusInf : m;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float e = exp_neg(v[i] - m);   // 1 - sigmoid is 1 here; of no expert 0
+                const float e = exp_neg(v[i] - top);   // 1 - sigmoid is 1 here
                 t[i] = m < -40.f ? e : t[i];
             }
         }
@@ -593,8 +598,8 @@ struct Row {
     }
 };
 
-// The weights of a token's chosen logits, one a lane and slot (NaN: none), and their
-// relation to the scores: w = scale * weight.
+// The weights, but for the scale, of a token's chosen logits, one a lane and slot; m and sum
+// of the softmax's terms where it is over all experts.
 template <int LANES, int SLOTS>
 __device__ __forceinline__ void weights_of(const RouteArgs &a, const float *l, const bool *on, float m, float sum, float *w)
 {
@@ -626,15 +631,6 @@ __device__ __forceinline__ void weights_of(const RouteArgs &a, const float *l, c
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) w[s] = t > 0.f ? w[s] / t : 0.f;
 }
-
-// Integers in the order of the floats they stand for (the two zeros are one).
-constexpr int kNoKey = int(0x807FFFFF);   // minus infinity
-__device__ __forceinline__ int key_of(float v)
-{
-    const int b = __builtin_bit_cast(int, v + 0.f);
-    return b ^ ((b >> 31) & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7FFFFFFF)); }
 
 // A lane's keys in falling order, and the place that each came from, four bits each.  Only
 // neighbours change places, and only where the second is larger: equal keys stay in order.

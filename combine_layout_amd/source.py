@@ -167,7 +167,7 @@ def _norm_plan(x, weight, residual, eps, dtype, out, out_scales, residual_out):
         raise TypeError(f"dtype must be bfloat16 or float8_e4m3fn, got {dtype}")
     _want(weight, "weight", weight.dtype, (H,), dev)
     cfg = _norm_config(H, _code(x, "x"), rc, _code(weight, "weight"),
-                       nat.AFD_BF16 if dtype is torch.bfloat16 else nat.AFD_FP8_E4M3, float(eps))
+                       nat.AFD_BF16 if dtype is torch.bfloat16 else nat.AFD_FP8_E4M3, eps)
     if out is not None:
         _want(out, "out", dtype, (T, H), dev)
     if out_scales is not None:
@@ -213,7 +213,10 @@ class _RmsNorm(torch.autograd.Function):
     def forward(ctx, x, weight, residual, eps):
         n = _norm(x, weight, residual, eps, torch.bfloat16, None, None, None, True)
         ctx.set_materialize_grads(False)
-        ctx.mark_non_differentiable(n.rstd)
+        if residual is None or x.requires_grad or residual.requires_grad:
+            ctx.mark_non_differentiable(n.rstd)
+        else:
+            ctx.mark_non_differentiable(n.rstd, n.residual)      # only the weight asks
         ctx.save_for_backward(x if residual is None else n.residual, weight, n.rstd)
         ctx.types = x.dtype, None if residual is None else residual.dtype
         return n.rows, n.residual, n.rstd
@@ -261,6 +264,7 @@ def rms_norm(x, weight, residual=None, *, eps=1e-6, dtype=torch.bfloat16, out=No
     Differentiable by x, residual and weight with bfloat16 rows in new memory, outside of
     a capture; the rounding of h counts as none, and x and residual share one gradient.
     Runs on x's device and its current stream."""
+    eps = float(eps)
     if out is not None or out_scales is not None or residual_out is not None:
         _plain("rms_norm", out, out_scales, residual_out)
     if _asks(x, weight, residual):
@@ -342,7 +346,7 @@ def _route_plan(logits, topk, scoring, bias, renormalize, scale, live, ids, weig
     """(configuration, row stride) of a choice whose arguments' layouts fit."""
     ls = _rows(logits, "logits")
     (T, E), dev = logits.shape, logits.device
-    cfg = _route_config(E, operator.index(topk), _code(logits, "logits"), scoring, bool(renormalize), float(scale))
+    cfg = _route_config(E, topk, _code(logits, "logits"), scoring, renormalize, scale)
     if bias is not None:
         _want(bias, "bias", torch.float32, (E,), dev)
     if live is not None:
@@ -409,6 +413,7 @@ def route_tokens(logits, topk, *, scoring="softmax", bias=None, renormalize=True
 
     The weights are differentiable by the logits, outside of a capture; the choice has no
     gradient.  Runs on the logits' device and its current stream."""
+    topk, renormalize, scale = operator.index(topk), bool(renormalize), float(scale)
     if bias is not None or live is not None or ids is not None or weights is not None:
         _plain("route_tokens", bias, live, ids, weights)
     if _asks(logits):
@@ -420,6 +425,7 @@ def route_tokens(logits, topk, *, scoring="softmax", bias=None, renormalize=True
 def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True, scale=1.0, out=None):
     """The logits' gradient, [T, E] of their type, through the weights of route_tokens: grad float32
     [T, topk], ids as they were chosen (any outside [0, E) takes no part)."""
+    renormalize, scale = bool(renormalize), float(scale)
     _plain("route_tokens_grad", grad, logits, ids, out)
     key = (logits.dtype, logits.shape, logits.stride(), logits.device, scoring, renormalize, scale, _layout(grad), _layout(ids),
            _layout(out))
@@ -439,24 +445,23 @@ def _route_grad_plan(grad, logits, ids, scoring, renormalize, scale, out):
     _want(grad, "grad", torch.float32, tuple(ids.shape), logits.device)
     if out is not None:
         _want(out, "out", logits.dtype, tuple(logits.shape), logits.device)
-    return _route_config(logits.shape[1], topk, _code(logits, "logits"), scoring, bool(renormalize), float(scale)), ls
+    return _route_config(logits.shape[1], topk, _code(logits, "logits"), scoring, renormalize, scale), ls
 
 
 def _balance_plan(logits, ids, scoring, coefficient):
-    """(configuration, row stride, workspace bytes, coefficient) of a loss whose arguments' layouts fit."""
+    """(configuration, row stride, workspace bytes) of a loss whose arguments' layouts fit."""
     ls, topk = _rows(logits, "logits"), _ids_of(ids, logits)
     cfg, ws = _route_config(logits.shape[1], topk, _code(logits, "logits"), scoring, False, 1.0), ctypes.c_size_t(0)
-    coefficient = float(coefficient)
     if not abs(coefficient) <= torch.finfo(torch.float32).max:
         raise ValueError(f"coefficient must be a finite float32, got {coefficient}")
     nat.check(nat.load().afd_balance_query(ctypes.byref(cfg), logits.shape[0], ctypes.byref(ws)), "balance_loss")
-    return cfg, ls, ws.value, coefficient
+    return cfg, ls, ws.value
 
 
 def _balance(logits, ids, scoring, coefficient):
     key = logits.dtype, logits.shape, logits.stride(), logits.device, _layout(ids), scoring, coefficient
     plan = _balances.get(key) or _keep(_balances, key, _balance_plan(logits, ids, scoring, coefficient))
-    cfg, ls, need, coefficient = plan
+    cfg, ls, need = plan
     (T, E), dev = logits.shape, logits.device
     loss = torch.empty((), dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int32, device=dev)
@@ -503,6 +508,7 @@ def balance_loss(logits, ids, *, scoring="softmax", coefficient=1.0) -> Balance:
 
     The loss is differentiable by the logits, through the shares, outside of a capture.
     Runs on the logits' device and its current stream."""
+    coefficient = float(coefficient)
     _plain("balance_loss", ids)
     if _asks(logits):
         _recorded("balance_loss", logits.device)

@@ -535,6 +535,7 @@ def test_autograd():
         (n.rows if rows else n.residual).sum().backward()
         assert x.grad is not None and r.grad is not None and (w.grad is not None) == rows
     n = afd.rms_norm(x.detach(), w, r.detach())
+    assert n.rows.requires_grad and not n.residual.requires_grad
     w.grad = None
     n.rows.float().sum().backward()
     assert w.grad.shape == (H,)

@@ -181,10 +181,8 @@ struct NormArgs {
 
 // h = x + residual, y = h * rstd * weight, rstd = 1 / sqrt(mean(h^2) + eps).  A row is held
 // by WPR wavefronts, C runs of eight columns a lane, from its one load to its last store, so
-// that the bytes are the floor's; a wavefront of its own (to 2048 columns) needs no barrier,
-// and four or sixteen keep C, and with it the registers, small on wider rows.  RES: 0 no
-// residual, 1 bf16, 2 float32.  Bound by HBM: 59 MB in 13.6 us (4096 rows of 2048, FP8), 805
-// MB in 147 (16381 of 4096, float32 stream), where a copy takes 11.4 and 155; one row 2.7 us,
+// that the bytes are the floor's.  RES: 0 no residual, 1 bf16, 2 float32.  Bound by HBM: 59 MB in 11.7 us (4096 rows of 2048, FP8), 805
+// MB in 146 (16381 of 4096, float32 stream), where a copy takes 11.4 and 155; one row 2.2 us,
 // the launch and a trip to memory.
 template <bool X32, int RES, bool OUT8, int WPR, int C>
 __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm(NormArgs a)
@@ -305,8 +303,8 @@ __device__ __forceinline__ void norm_grad_columns(const NormGradArgs &a, int blo
 
 // dh = rstd * (a - u * mean(a * u)) + grad_residual of every row, a = grad * weight and u =
 // h * rstd, and the workgroup's sum of grad * u over its rows, which stays in registers from
-// the first row to the last: dweight costs no second reading of many rows.  101 MB in 19.6 us
-// (6144 rows of 2048, BF16; a copy's 19.4) and 4.1 for the launch behind it.
+// the first row to the last: dweight costs no second reading of many rows.  101 MB in 18.8 us
+// (6144 rows of 2048, BF16; a copy's 19.4) and 4.2 for the launch behind it.
 template <bool H32, int WPR, int C>
 __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm_grad(NormGradArgs a)
 {
@@ -1353,14 +1351,18 @@ int norm_as(NormArgs a, hipStream_t st)
     return 0;
 }
 
+// One run of eight columns a lane as far as it goes, which has the most loads on the way for
+// few rows and costs many none (2048 columns, bf16, one wavefront with four runs and four with
+// one: 256 rows 3.5 and 2.8 us, 4096 9.8 and 9.7; 4096 columns, four with two and eight with
+// one: 64 rows 2.9 and 2.7, 4096 16.4 and 16.9; 8192, 16 with one: 3.5 and 3.2, 30.9 and 31.3).
 template <bool X32, int RES, bool OUT8>
 int norm_of(const NormArgs &a, hipStream_t st)
 {
     if (a.H <= 512) return norm_as<X32, RES, OUT8, 1, 1>(a, st);
     if (a.H <= 1024) return norm_as<X32, RES, OUT8, 1, 2>(a, st);
-    if (a.H <= 2048) return norm_as<X32, RES, OUT8, 1, 4>(a, st);
-    if (a.H <= 4096) return norm_as<X32, RES, OUT8, 4, 2>(a, st);
-    if (a.H <= 8192) return norm_as<X32, RES, OUT8, 4, 4>(a, st);
+    if (a.H <= 2048) return norm_as<X32, RES, OUT8, 4, 1>(a, st);
+    if (a.H <= 4096) return norm_as<X32, RES, OUT8, 8, 1>(a, st);
+    if (a.H <= 8192) return norm_as<X32, RES, OUT8, 16, 1>(a, st);
     static_assert(AFD_MAX_NORM_HIDDEN == 16 * kWave * 2 * 8, "the widest row");
     return norm_as<X32, RES, OUT8, 16, 2>(a, st);
 }
@@ -1394,7 +1396,10 @@ int norm_grad_of(const NormGradArgs &a, int groups, hipStream_t st)
 {
     if (a.H <= 512) return norm_grad_as<H32, 1, 1>(a, groups, st);
     if (a.H <= 1024) return norm_grad_as<H32, 1, 2>(a, groups, st);
-    if (a.H <= 2048) return norm_grad_as<H32, 1, 4>(a, groups, st);
+    // a wavefront with four runs, or four with one: bf16 64 rows 3.3 and 2.6 us, 1024 6.2 and 6.7,
+    // 16384 37.0 and 39.8; float32 3.5 and 2.6, 10.3 and 11.8, 93.9 and 86.2
+    if (a.H <= 2048)
+        return a.rows <= 512 || (H32 && a.part) ? norm_grad_as<H32, 4, 1>(a, groups, st) : norm_grad_as<H32, 1, 4>(a, groups, st);
     if (a.H <= 4096) return norm_grad_as<H32, 4, 2>(a, groups, st);
     if (a.H <= 8192) return norm_grad_as<H32, 4, 4>(a, groups, st);
     return norm_grad_as<H32, 16, 2>(a, groups, st);

@@ -181,9 +181,9 @@ struct NormArgs {
 
 // h = x + residual, y = h * rstd * weight, rstd = 1 / sqrt(mean(h^2) + eps).  A row is held
 // by WPR wavefronts, C runs of eight columns a lane, from its one load to its last store, so
-// that the bytes are the floor's.  RES: 0 no residual, 1 bf16, 2 float32.  Bound by HBM: 59 MB in 11.7 us (4096 rows of 2048, FP8), 805
-// MB in 146 (16381 of 4096, float32 stream), where a copy takes 11.4 and 155; one row 2.2 us,
-// the launch and a trip to memory.
+// that the bytes are the floor's.  RES: 0 no residual, 1 bf16, 2 float32.  Bound by HBM: 59
+// MB in 11.7 us (4096 rows of 2048, FP8), 805 MB in 146 (16381 of 4096, float32 stream), where
+// a copy takes 11.4 and 155; one row 2.2 us, the launch and a trip to memory.
 template <bool X32, int RES, bool OUT8, int WPR, int C>
 __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm(NormArgs a)
 {

@@ -225,7 +225,10 @@ class Buffer:
         self._round_refs[("reply", f)] = rows
 
     # -- the source's side, between its collect and its dispatch -----------------
-    def _source_rows(self, s, t, columns, what):
+    def _source_rows(self, s, t, columns, what, *others):
+        if _source._asks(t, *others):
+            raise ValueError("a round carries no gradients: detach what source_norm and source_route take, or call under "
+                             "no_grad(); rms_norm, route_tokens and balance_loss have them")
         if not 0 <= s < self.N:
             raise ValueError(f"source {s} of {self.N}")
         if t.dim() != 2 or t.shape[1] != columns or t.shape[0] > self.capacity:
@@ -236,16 +239,17 @@ class Buffer:
     def source_norm(self, s, x, weight, residual=None, *, eps=1e-6, residual_out=None) -> _source.Normed:
         """The rows that source_dispatch takes, from what source_collect gave: rms_norm in the
         buffer's format.  In FP8 its rows and scales are source_dispatch's x and x_scale.
-        residual: the stream that x joins; residual_out as in rms_norm."""
-        self._source_rows(s, x, self.H, "x")
+        residual: the stream that x joins; residual_out as in rms_norm.  Forward only, as the
+        round that follows (what asks for a gradient is refused unless gradients are off)."""
+        self._source_rows(s, x, self.H, "x", weight, residual)
         return _source.rms_norm(x, weight, residual, eps=eps, residual_out=residual_out,
                                 dtype=torch.float8_e4m3fn if self.fp8 else torch.bfloat16)
 
     def source_route(self, s, logits, *, scoring="softmax", bias=None, renormalize=True, scale=1.0,
                      live=None) -> _source.Routes:
         """The ids and weights that source_dispatch takes, from the router's logits [T, E]:
-        route_tokens with the buffer's topk."""
-        self._source_rows(s, logits, self.E, "logits")
+        route_tokens with the buffer's topk.  Forward only, as the round that follows."""
+        self._source_rows(s, logits, self.E, "logits", bias)
         return _source.route_tokens(logits, self.K, scoring=scoring, bias=bias, renormalize=renormalize, scale=scale,
                                     live=live)
 

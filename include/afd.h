@@ -609,6 +609,7 @@ afd_status afd_worker_tags(afd_ctx *ctx, int32_t f, const int32_t *const *tags, 
  *                   scale below 2^-126 counts as 0 and gives codes 0.  A block with an
  *                   infinity has the scale infinity, NaN codes for its infinities and 0 for the rest.
  *   eps             at least float32's smallest normal number
+ * A row whose sum of squares passes float32's range has rstd 0.
  */
 typedef struct {
     int32_t hidden;

@@ -866,4 +866,12 @@ def test_refusals():
                  lambda: buf.source_route(-1, l), lambda: buf.source_route(0, l.cpu())):
         with pytest.raises(ValueError):
             call()
+    asks = lambda t: t.clone().requires_grad_()  # noqa: E731
+    for call in (lambda: buf.source_norm(0, asks(x), w), lambda: buf.source_norm(0, x, asks(w)),
+                 lambda: buf.source_norm(0, x, w, asks(x)), lambda: buf.source_route(0, asks(l)),
+                 lambda: buf.source_route(0, l, bias=asks(z(8)))):
+        with pytest.raises(ValueError, match="no gradients"):
+            call()
+    with torch.no_grad():
+        assert not buf.source_route(0, asks(l)).weights.requires_grad
     assert buf.source_norm(0, x, w).rows.shape == (4, 256) and buf.source_route(0, l).ids.shape == (4, 2)

@@ -682,8 +682,8 @@ template <int LANES>
 constexpr int kMost = LANES == 16 ? 48 : 64;
 
 // Whether two keys with biases may be out of order.  A sigmoid is off by less than 4
-// roundings of 1, a softmax by less than 25 (its sum's 14, the exponential's and the
-// division's); the sum with the bias by one of its own size.  Two keys that are 64 of both
+// roundings of 1, a softmax by less than 25 (its sum's 14, the exponential's, the division's
+// and the product's); the sum with the bias by one of its own size.  Two keys that are 64 of both
 // apart are in order (2^-18 = 64 U).
 __device__ __forceinline__ bool too_near(int larger, int smaller)
 {
@@ -824,10 +824,11 @@ __device__ __forceinline__ void take_exactly(const RouteArgs &a, int64_t row, Pi
 }
 
 // The choice of a wavefront with one token: a border that at least K of the lanes' largest
-// keys reach is found by halving, the keys that reach it (about K and a few) are brought
-// together, one a lane, and each counts the larger ones.  Returns the lane's key and its
-// rank, or false where more than 64 reach the border (many equal keys), with `k` as it was.
-template <typename R, int V>
+// keys reach is found by halving, the keys that reach it (about K and a few; with NEAR those
+// too that are too near to it) are brought together, one a lane, and each counts the larger
+// ones.  Returns the lane's key and its rank, or false where more than 64 reach the border
+// (many equal keys), with `k` as it was.
+template <typename R, int V, bool NEAR>
 __device__ __forceinline__ bool take_above(const int *k, int K, Pick *picks, Pick &mine, int &rank, int &count)
 {
     int head = k[0];
@@ -844,6 +845,10 @@ __device__ __forceinline__ bool take_above(const int *k, int K, Pick *picks, Pic
         } else {
             hi = mid - 1;
         }
+    }
+    if constexpr (NEAR) {
+        const float f = of_key(lo);
+        if (f - f == 0.f) lo = key_of(f - 0x1p-17f * (1.f + fabsf(f)));   // (twice what too_near allows)
     }
     lo = max(lo, kNoKey + 1);
     count = 0;
@@ -890,31 +895,57 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
     const bool live = !a.live || a.live[row] != 0;
     float m = 0.f, sum = 1.f;
     int key[V];
-    if (BIAS ? !a.sigmoid : !a.sigmoid && !a.renorm) {
-        float t[V];
-        m = R::largest(v);
-        sum = R::terms(v, m, t);
-        if constexpr (BIAS) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = __builtin_bit_cast(int, t[i] / sum);
-        }
-    }
     if constexpr (BIAS) {
+        float b[V], t[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = R::expert(i) < a.E ? a.bias[R::expert(i)] : 0.f;
+        if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float z = exp_neg(-fabsf(v[i]));
+                t[i] = (v[i] >= 0.f ? 1.f : z) * inverse(1.0f + z);
+            }
+        } else {
+            m = R::largest(v);
+            sum = R::terms(v, m, t);
+            const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) t[i] *= inv;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = R::expert(i);
-            const float z = exp_neg(-fabsf(v[i])), s = (v[i] >= 0.f ? 1.f : z) * inverse(1.0f + z);
-            const float x = (a.sigmoid ? s : __builtin_bit_cast(float, key[i])) + (e < a.E ? a.bias[e] : 0.f);
+            const float x = t[i] + b[i];
             key[i] = v[i] == kMinusInf || !(x == x) ? kNoKey : key_of(x);
         }
     } else {
+        if (!a.sigmoid && !a.renorm) {
+            float t[V];
+            m = R::largest(v);
+            sum = R::terms(v, m, t);
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = key_of(v[i]);
+    }
+    bool done = false;
+    if constexpr (BIAS && LANES == kWave) {
+        Pick mine;
+        int rank, count;
+        done = take_above<R, V, true>(key, a.K, picks, mine, rank, count);
+        if (done) {
+            wave_sync();
+            picks[lane < count ? rank : lane] = mine;   // in order by the 32-bit scores
+            wave_sync();
+            const int below = lane + 1 < kWave ? picks[lane + 1].key : kNoKey;
+            if (__any(lane < a.K && too_near(picks[lane].key, below))) {
+                wave_sync();
+                order_exactly<R>(a, row, count, picks);
+            }
+        }
     }
     if constexpr (!BIAS && LANES == kWave) {
         Pick mine;
         int rank, count;
-        if (take_above<R, V>(key, a.K, picks, mine, rank, count)) {
+        if (take_above<R, V, false>(key, a.K, picks, mine, rank, count)) {
             const bool on = lane < count && rank < a.K;
             const float l = of_key(mine.key);
             float w;
@@ -932,15 +963,17 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
             return;
         }
     }
+    if (!done) {
 #pragma unroll
-    for (int s = 0; s < kMost<LANES> / LANES; ++s) picks[s * LANES + lane] = Pick{-1, kNoKey};
-    wave_sync();
-    const Taken taken = take<R, LANES, V, BIAS>(key, a.K, picks);
-    if constexpr (BIAS) {
-        if (__any(taken.close)) {
-            wave_sync();
-            if (__any(taken.open)) take_exactly<R>(a, row, picks);
-            else order_exactly<R>(a, row, taken.count, picks);
+        for (int s = 0; s < kMost<LANES> / LANES; ++s) picks[s * LANES + lane] = Pick{-1, kNoKey};
+        wave_sync();
+        const Taken taken = take<R, LANES, V, BIAS>(key, a.K, picks);
+        if constexpr (BIAS) {
+            if (__any(taken.close)) {
+                wave_sync();
+                if (__any(taken.open)) take_exactly<R>(a, row, picks);
+                else order_exactly<R>(a, row, taken.count, picks);
+            }
         }
     }
     wave_sync();

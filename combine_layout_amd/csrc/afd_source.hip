@@ -682,13 +682,13 @@ template <int LANES>
 constexpr int kMost = LANES == 16 ? 48 : 64;
 
 // Whether two keys with biases may be out of order.  A sigmoid is off by less than 4
-// roundings of 1, a softmax by less than 25 (its sum's 14, the exponential's, the division's
-// and the product's); the sum with the bias by one of its own size.  Two keys that are 64 of both
-// apart are in order (2^-18 = 64 U).
-__device__ __forceinline__ bool too_near(int larger, int smaller)
+// roundings of 1 (the exponential's argument and result, the sum, the reciprocal and the
+// product), a softmax by less than 25 (its sum's 14 more); the sum with the bias by one of its
+// own size.  Two keys that are 16, or 64, of both apart are in order (2^-20 = 16 roundings).
+__device__ __forceinline__ bool too_near(int larger, int smaller, bool sigmoid)
 {
     const float lo = of_key(smaller);
-    return smaller != kNoKey && !(of_key(larger) - lo > 0x1p-18f * (1.f + fabsf(lo)));
+    return smaller != kNoKey && !(of_key(larger) - lo > (sigmoid ? 0x1p-20f : 0x1p-18f) * (1.f + fabsf(lo)));
 }
 
 struct Taken {
@@ -702,7 +702,7 @@ struct Taken {
 // with the lowest expert.  `rounds` of them, with NEAR one more for the border behind the
 // last place, and as many as are too near to it.
 template <typename R, int LANES, int V, bool NEAR>
-__device__ __forceinline__ Taken take(int *k, int rounds, Pick *picks)
+__device__ __forceinline__ Taken take(int *k, int rounds, bool sigmoid, Pick *picks)
 {
     uint32_t order = sort_keys<V>(k);
     Taken t{0, false, false};
@@ -725,7 +725,7 @@ __device__ __forceinline__ Taken take(int *k, int rounds, Pick *picks)
 #pragma unroll
         for (int i = 0; i < V; ++i) k[i] = (pop & (i + 1 < V ? k[i + 1] : kNoKey)) | (~pop & k[i]);
         if constexpr (NEAR) {
-            t.open = r > 0 && too_near(before, m);
+            t.open = r > 0 && too_near(before, m, sigmoid);
             t.close = t.close || t.open;
             before = m;
         }
@@ -757,10 +757,14 @@ template <typename R>
 __device__ __forceinline__ void order_exactly(const RouteArgs &a, int64_t row, int count, Pick *picks)
 {
     constexpr int LANES = R::kLanes, kEach = kMost<LANES> / LANES;
-    float v[R::kV];
-    R::load(a, row, v);   // again, rather than held by all who need none of this
-    const float m = R::largest(v);
-    const double sum = score_sum<R>(a, v, m);
+    float m = 0.f;
+    double sum = 1.0;
+    if (!a.sigmoid) {
+        float v[R::kV];
+        R::load(a, row, v);   // again, rather than held by all who need none of this
+        m = R::largest(v);
+        sum = score_sum<R>(a, v, m);
+    }
     double key[kEach];
     int id[kEach], rank[kEach];
 #pragma unroll
@@ -881,7 +885,7 @@ __device__ __forceinline__ bool take_above(const int *k, int K, Pick *picks, Pic
 // the lanes, so a lane's logits are sorted once and only the first of them takes part; with
 // a wavefront for a token a border is cheaper (take_above: 38 -> 29 us).  32768 tokens of 512
 // experts, 8 chosen: 24 us, of which the logits' 67 MB are 13; 6144 tokens of 96 with a bias
-// 8.6; 256 of 128 4.6, the launch, a trip to memory and the chain of eight rounds.
+// 8.2; 256 of 128 4.4, the launch, a trip to memory and the chain of eight rounds.
 template <bool L32, int LANES, int V, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a)
 {
@@ -936,7 +940,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
             picks[lane < count ? rank : lane] = mine;   // in order by the 32-bit scores
             wave_sync();
             const int below = lane + 1 < kWave ? picks[lane + 1].key : kNoKey;
-            if (__any(lane < a.K && too_near(picks[lane].key, below))) {
+            if (__any(lane < a.K && too_near(picks[lane].key, below, a.sigmoid))) {
                 wave_sync();
                 order_exactly<R>(a, row, count, picks);
             }
@@ -967,7 +971,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
 #pragma unroll
         for (int s = 0; s < kMost<LANES> / LANES; ++s) picks[s * LANES + lane] = Pick{-1, kNoKey};
         wave_sync();
-        const Taken taken = take<R, LANES, V, BIAS>(key, a.K, picks);
+        const Taken taken = take<R, LANES, V, BIAS>(key, a.K, a.sigmoid, picks);
         if constexpr (BIAS) {
             if (__any(taken.close)) {
                 wave_sync();

@@ -205,6 +205,32 @@ def test_norm_grad_many_rows(T, H):
     ref.check(dw, wantw, tolw + ref.U * wantw.abs(), "dweight")
 
 
+def test_norm_gradient_by_differences():
+    """The gradients against differences of the 64-bit norm itself, not of a formula for them."""
+    afd = _afd()
+    g = _gen(17)
+    T, H, step = 3, 64, 2.0 ** -10
+    x, w, dy = _rand(g, T, H, std=1.5), 1 + _rand(g, H, std=0.3), _rand(g, T, H, dtype=BF)
+    with torch.no_grad():
+        n = afd.rms_norm(x.cuda(), w.cuda(), keep_rstd=True)
+        dh, dw = (t.double().cpu() for t in afd.rms_norm_grad(dy.cuda(), x.cuda(), w.cuda(), n.rstd))
+    d = dy.double()
+    _, rstd, _, _ = ref.norm(x.double(), w, None, 1e-6)
+    _, tol, _, tolw = ref.norm_grad(d, x.double(), w.double(), rstd, None)
+    for i in range(H):
+        e = torch.zeros(H, dtype=torch.float64)
+        e[i] = step
+        up, down = (ref.norm(x.double() + s * e, w, None, 1e-6)[2] for s in (1, -1))
+        diff = ((up - down) * d).sum(1) / (2 * step)
+        # |x_j| is at most sqrt(H) / rstd, so a third derivative at most 36 rstd^3 / H of the sum of sizes;
+        # rstd moves by less than a factor 1.1 over the step; 4 roundings of the given rstd
+        third = 36 * 1.1 ** 3 * rstd ** 3 / H * (d * w.double()).abs().sum(1)
+        assert ((diff - dh[:, i]).abs() <= tol[:, i] + 4 * ref.U * dh[:, i].abs() + step ** 2 / 6 * third).all(), i
+        up, down = (ref.norm(x.double(), w.double() + s * e, None, 1e-6)[2] for s in (1, -1))
+        diff = ((up - down) * d).sum() / (2 * step)
+        assert (diff - dw[i]).abs() <= tolw[i] + 8 * ref.U * (d * x.double() * rstd[:, None])[:, i].abs().sum(), i
+
+
 def test_norm_grad_in_place_and_empty():
     afd = _afd()
     g = _gen(1)

@@ -82,7 +82,7 @@ def _launch(device, call, *args):
 
 def _layout(t):
     """What the checks of a tensor look at, but for its address."""
-    return None if t is None else (t.dtype, t.shape, t.stride(), t.device)
+    return t.dtype, t.shape, t.stride(), t.device
 
 
 _CHECKED = 1024      # layouts of arguments that the calls keep as checked
@@ -185,7 +185,8 @@ def _norm_plan(x, weight, residual, eps, dtype, out, out_scales, residual_out):
 
 def _norm(x, weight, residual, eps, dtype, out, out_scales, residual_out, keep_rstd):
     key = (x.dtype, x.shape, x.stride(), x.device, weight.dtype, weight.shape, weight.stride(), weight.device,
-           _layout(residual), eps, dtype, _layout(out), _layout(out_scales), _layout(residual_out))
+           None if residual is None else _layout(residual), eps, dtype, None if out is None else _layout(out),
+           None if out_scales is None else _layout(out_scales), None if residual_out is None else _layout(residual_out))
     plan = _norms.get(key) or _keep(_norms, key, _norm_plan(x, weight, residual, eps, dtype, out, out_scales, residual_out))
     cfg, xs, rs, hs = plan
     (T, H), dev = x.shape, x.device
@@ -284,7 +285,8 @@ def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight
     grad of h's type.  dweight is float32 [H], None without weight_grad."""
     _plain("rms_norm_grad", grad, h, weight, rstd, grad_residual, out)
     key = (h.dtype, h.shape, h.stride(), h.device, weight.dtype, weight.shape, weight.stride(), weight.device,
-           _layout(grad), _layout(grad_residual), _layout(rstd), _layout(out))
+           _layout(grad), None if grad_residual is None else _layout(grad_residual), _layout(rstd),
+           None if out is None else _layout(out))
     plan = _norm_grads.get(key) or _keep(_norm_grads, key, _norm_grad_plan(grad, h, weight, rstd, grad_residual, out))
     cfg, hs, need = plan
     (T, H), dev = h.shape, h.device
@@ -359,8 +361,9 @@ def _route_plan(logits, topk, scoring, bias, renormalize, scale, live, ids, weig
 
 
 def _route(logits, topk, scoring, bias, renormalize, scale, live, ids, weights):
-    key = (logits.dtype, logits.shape, logits.stride(), logits.device, topk, scoring, renormalize, scale, _layout(bias),
-           _layout(live), _layout(ids), _layout(weights))
+    key = (logits.dtype, logits.shape, logits.stride(), logits.device, topk, scoring, renormalize, scale,
+           None if bias is None else _layout(bias), None if live is None else _layout(live),
+           None if ids is None else _layout(ids), None if weights is None else _layout(weights))
     plan = _routes.get(key) or _keep(_routes, key, _route_plan(logits, topk, scoring, bias, renormalize, scale, live, ids,
                                                                weights))
     cfg, ls = plan
@@ -428,7 +431,7 @@ def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True,
     renormalize, scale = bool(renormalize), float(scale)
     _plain("route_tokens_grad", grad, logits, ids, out)
     key = (logits.dtype, logits.shape, logits.stride(), logits.device, scoring, renormalize, scale, _layout(grad), _layout(ids),
-           _layout(out))
+           None if out is None else _layout(out))
     plan = _routes.get(key) or _keep(_routes, key, _route_grad_plan(grad, logits, ids, scoring, renormalize, scale, out))
     cfg, ls = plan
     if out is None:
@@ -521,7 +524,7 @@ def balance_loss_grad(grad, logits, ids, slope, *, scoring="softmax", out=None):
     ids and slope as balance_loss had and gave them.  Tokens that do not count have 0."""
     _plain("balance_loss_grad", grad, logits, ids, slope, out)
     key = (logits.dtype, logits.shape, logits.stride(), logits.device, _layout(ids), scoring, _layout(grad), _layout(slope),
-           _layout(out))
+           None if out is None else _layout(out))
     plan = _balances.get(key) or _keep(_balances, key, _balance_grad_plan(grad, logits, ids, slope, scoring, out))
     cfg, ls = plan
     if out is None:

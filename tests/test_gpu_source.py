@@ -192,16 +192,17 @@ def test_norm_grad(H, ht, wt, T, res):
 
 
 @pytest.mark.parametrize("T,H", [(4097, 2048), (2500, 4096), (3001, 264), (600, 16384), (1024, 2048), (1025, 2048), (512, 16384),
-                                 (301, 40), (511, 4104)])
-def test_norm_grad_many_rows(T, H):
+                                 (301, 40), (511, 4104), (900, 1504)])
+@pytest.mark.parametrize("ht", [BF, F32])
+def test_norm_grad_many_rows(T, H, ht):
     afd = _afd()
-    _print("norm grad rows", T, H)
+    _print("norm grad rows", T, H, ht)
     g = _gen(T)
-    h, w, dy = _rand(g, T, H, dtype=BF), 1 + _rand(g, H, std=0.3), _rand(g, T, H, dtype=BF)
+    h, w, dy = _rand(g, T, H, dtype=ht), 1 + _rand(g, H, std=0.3), _rand(g, T, H, dtype=BF)
     rstd = (1 / torch.sqrt(h.double().square().mean(1) + 1e-6)).float()
     dh, dw = afd.rms_norm_grad(dy.cuda(), _gapped(h, 8), w.cuda(), rstd.cuda())
     want, tol, wantw, tolw = ref.norm_grad(dy.double(), h.double(), w.double(), rstd.double(), None)
-    ref.check(dh, want, ref.rounded(want, tol, BF), "dh")
+    ref.check(dh, want, ref.rounded(want, tol, ht), "dh")
     ref.check(dw, wantw, tolw + ref.U * wantw.abs(), "dweight")
 
 
@@ -278,6 +279,26 @@ def test_route(E, K, dtype, scoring, bias, renormalize, scale, T):
         ref.check(r.weights, w, tol, "weights")
         if mask is not None:
             assert (r.weights.cpu()[~mask] == 0).all()
+
+
+@pytest.mark.parametrize("T,E,K", [(8193, 128, 8), (9000, 65, 17), (8200, 100, 32), (20001, 40, 3), (9001, 300, 6), (40000, 12, 2)])
+@pytest.mark.parametrize("dtype,scoring,bias,renormalize", [(F32, "softmax", False, False), (BF, "sigmoid", True, True),
+                                                            (F32, "sigmoid", True, False), (BF, "softmax", False, True)])
+def test_route_many_rows(T, E, K, dtype, scoring, bias, renormalize):
+    """More tokens than the forms for few take, and than the gradient's workgroups hold at once."""
+    afd = _afd()
+    _print("route rows", T, E, K, dtype, scoring, bias, renormalize)
+    g = _gen(T + E)
+    logits, b = _logits(g, T, E, dtype), _rand(g, E, std=0.2) if bias else None
+    logits[7::11, ::2] = -INF
+    r = afd.route_tokens(logits.cuda(), K, scoring=scoring, bias=None if b is None else b.cuda(), renormalize=renormalize)
+    ids = ref.choose(logits, K, scoring, b, None)
+    assert torch.equal(r.ids.cpu().long(), ids)
+    ref.check(r.weights, *ref.weights(logits, ids, scoring, renormalize, 1.0), "weights")
+    dw = _rand(g, T, K)
+    d = afd.route_tokens_grad(dw.cuda(), logits.cuda(), r.ids, scoring=scoring, renormalize=renormalize)
+    want, tol = ref.route_grad(dw, logits, ids, scoring, renormalize, 1.0)
+    ref.check(d, want, ref.rounded(want, tol, dtype), "dlogits")
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
@@ -464,7 +485,8 @@ def _check_balance(afd, logits, ids, scoring, coefficient):
     return b
 
 
-@pytest.mark.parametrize("T,E,K", [(5000, 96, 6), (9001, 128, 8), (4097, 512, 8), (70000, 16, 2)])
+@pytest.mark.parametrize("T,E,K", [(5000, 96, 6), (9001, 128, 8), (4097, 512, 8), (70000, 16, 2), (5000, 200, 8),
+                                   (20000, 300, 4)])
 def test_balance_many_rows(T, E, K):
     afd = _afd()
     _print("balance rows", T, E, K)

@@ -885,7 +885,7 @@ __device__ __forceinline__ bool take_above(const int *k, int K, Pick *picks, Pic
 // the lanes, so a lane's logits are sorted once and only the first of them takes part; with
 // a wavefront for a token a border is cheaper (take_above: 38 -> 29 us).  32768 tokens of 512
 // experts, 8 chosen: 24 us, of which the logits' 67 MB are 13; 6144 tokens of 96 with a bias
-// 8.2; 256 of 128 4.4, the launch, a trip to memory and the chain of eight rounds.
+// 6.9; 256 of 128 4.0, the launch, a trip to memory and the chain of eight rounds.
 template <bool L32, int LANES, int V, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a)
 {

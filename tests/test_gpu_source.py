@@ -233,14 +233,19 @@ def test_norm_gradient_by_differences():
 
 
 def test_norm_grad_in_place_and_empty():
+    """dh in place of either gradient, with few rows (where other workgroups read grad for dweight) and many."""
     afd = _afd()
     g = _gen(1)
-    h, w, dy, dr = (_rand(g, *s, dtype=BF).cuda() for s in ((33, 2048), (2048,), (33, 2048), (33, 2048)))
-    rstd = torch.rand(33, generator=g).cuda() + 0.5
-    want, dw = afd.rms_norm_grad(dy, h, w, rstd, grad_residual=dr)
-    a, b = dr.clone(), dy.clone()
-    assert torch.equal(afd.rms_norm_grad(dy, h, w, rstd, grad_residual=a, out=a)[0], want)
-    assert torch.equal(afd.rms_norm_grad(b, h, w, rstd, grad_residual=dr, out=b)[0], want)
+    for T, H in ((33, 2048), (700, 4096), (1024, 512), (1500, 2048)):
+        h, w, dy, dr = (_rand(g, *s, dtype=BF).cuda() for s in ((T, H), (H,), (T, H), (T, H)))
+        rstd = torch.rand(T, generator=g).cuda() + 0.5
+        want = afd.rms_norm_grad(dy, h, w, rstd, grad_residual=dr)
+        for _ in range(5):
+            a, b = dr.clone(), dy.clone()
+            got = afd.rms_norm_grad(dy, h, w, rstd, grad_residual=a, out=a)
+            assert got[0] is a and torch.equal(a, want[0]) and torch.equal(got[1], want[1])
+            got = afd.rms_norm_grad(b, h, w, rstd, grad_residual=dr, out=b)
+            assert got[0] is b and torch.equal(b, want[0]) and torch.equal(got[1], want[1])
     dh, dw = afd.rms_norm_grad(dy[:0], h[:0], w, rstd[:0])
     assert dh.shape == (0, 2048) and torch.equal(dw, torch.zeros(2048, device="cuda"))
     assert afd.rms_norm(h[:0], w).rows.shape == (0, 2048)

@@ -16,6 +16,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _native as nat
 from .experts import SCALE_BLOCK, on_device, raw_stream
@@ -70,6 +71,12 @@ def _recorded(call, device, *given):
             if torch.cuda.is_current_stream_capturing():
                 raise ValueError(f"{call}: autograd does not record a captured call: call it under no_grad(), and "
                                  f"{call}_grad for the gradient")
+
+
+def _wrote(*given):
+    """The kernels write by address, which autograd does not see: a graph that saved one of the
+    given outputs has to find it changed.  (Tensors of inference mode have no counter.)"""
+    increment_version([t for t in given if t is not None])
 
 
 def _launch(device, call, *args):
@@ -266,14 +273,18 @@ def rms_norm(x, weight, residual=None, *, eps=1e-6, dtype=torch.bfloat16, out=No
     a capture; the rounding of h counts as none, and x and residual share one gradient.
     Runs on x's device and its current stream."""
     eps = float(eps)
-    if out is not None or out_scales is not None or residual_out is not None:
+    given = out is not None or out_scales is not None or residual_out is not None
+    if given:
         _plain("rms_norm", out, out_scales, residual_out)
     if _asks(x, weight, residual):
         _recorded("rms_norm", x.device, out is not None, out_scales is not None, residual_out is not None,
                   dtype is not torch.bfloat16)
         rows, h, rstd = _RmsNorm.apply(x, weight, residual, eps)
         return Normed(rows, None, h, rstd if keep_rstd else None)
-    return _norm(x, weight, residual, eps, dtype, out, out_scales, residual_out, keep_rstd)
+    n = _norm(x, weight, residual, eps, dtype, out, out_scales, residual_out, keep_rstd)
+    if given:
+        _wrote(out, out_scales, residual_out)
+    return n
 
 
 def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight_grad=True):
@@ -290,6 +301,7 @@ def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight
     plan = _norm_grads.get(key) or _keep(_norm_grads, key, _norm_grad_plan(grad, h, weight, rstd, grad_residual, out))
     cfg, hs, need = plan
     (T, H), dev = h.shape, h.device
+    given = out
     if out is None:
         out = _like(h, h.dtype)
     dw = ws = pd = pw = None
@@ -304,6 +316,8 @@ def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight
                  rstd.data_ptr(), out.data_ptr(), pd, pw, need if weight_grad else 0)
     if st:
         _check(st, "rms_norm_grad", grad=grad, grad_residual=grad_residual, h=h, weight=weight, out=out)
+    if given is not None:
+        _wrote(given)
     return out, dw
 
 
@@ -422,7 +436,10 @@ def route_tokens(logits, topk, *, scoring="softmax", bias=None, renormalize=True
     if _asks(logits):
         _recorded("route_tokens", logits.device, ids is not None, weights is not None)
         return Routes(*_RouteTokens.apply(logits, topk, scoring, bias, renormalize, scale, live))
-    return _route(logits, topk, scoring, bias, renormalize, scale, live, ids, weights)
+    r = _route(logits, topk, scoring, bias, renormalize, scale, live, ids, weights)
+    if ids is not None or weights is not None:
+        _wrote(ids, weights)
+    return r
 
 
 def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True, scale=1.0, out=None):
@@ -434,12 +451,15 @@ def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True,
            None if out is None else _layout(out))
     plan = _routes.get(key) or _keep(_routes, key, _route_grad_plan(grad, logits, ids, scoring, renormalize, scale, out))
     cfg, ls = plan
+    given = out
     if out is None:
         out = _like(logits, logits.dtype)
     st = _launch(logits.device, nat.load().afd_route_grad, cfg, logits.shape[0], grad.data_ptr(), logits.data_ptr(), ls,
                  ids.data_ptr(), out.data_ptr())
     if st:
         nat.check(st, "route_tokens_grad")
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -527,12 +547,15 @@ def balance_loss_grad(grad, logits, ids, slope, *, scoring="softmax", out=None):
            None if out is None else _layout(out))
     plan = _balances.get(key) or _keep(_balances, key, _balance_grad_plan(grad, logits, ids, slope, scoring, out))
     cfg, ls = plan
+    given = out
     if out is None:
         out = _like(logits, logits.dtype)
     st = _launch(logits.device, nat.load().afd_balance_grad, cfg, logits.shape[0], grad.data_ptr(), logits.data_ptr(), ls,
                  ids.data_ptr(), slope.data_ptr(), out.data_ptr())
     if st:
         nat.check(st, "balance_loss_grad")
+    if given is not None:
+        _wrote(given)
     return out
 
 

@@ -1,0 +1,116 @@
+"""The source's calls and autograd on the GPU: what a recorded call saved and another
+call then writes over is found by the backward pass."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+T, H, E, K = 40, 256, 16, 4
+
+
+def _afd():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import combine_layout_amd as afd
+    return afd
+
+
+def _rand(*shape, dtype=torch.float32):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(sum(shape))).to(dtype).cuda()
+
+
+def _asks(t):
+    return t.clone().requires_grad_()
+
+
+def _projection(afd):
+    """A product that saves the stream; the next norm then adds to the stream in place."""
+    stream, wq = _rand(T, H, dtype=BF), _asks(_rand(H, 32, dtype=BF))
+    return (stream @ wq).sum(), lambda: afd.rms_norm(_rand(T, H, dtype=BF), _rand(H), stream, residual_out=stream)
+
+
+def _norm_of_x(afd):
+    x, w = _rand(T, H, dtype=BF), _asks(_rand(H))
+    return afd.rms_norm(x, w).rows.float().sum(), lambda: afd.rms_norm(_rand(T, H, dtype=BF) + 1, _rand(H), out=x)
+
+
+def _norm_of_the_stream(afd):
+    """With only the weight asking, the stream that the call returns is what it saved."""
+    n = afd.rms_norm(_rand(T, H, dtype=BF), _asks(_rand(H)), _rand(T, H, dtype=BF))
+    assert not n.residual.requires_grad
+    return n.rows.float().sum(), lambda: afd.rms_norm(_rand(T, H, dtype=BF), _rand(H), n.residual, residual_out=n.residual)
+
+
+def _norm_by_its_gradient(afd):
+    x, w = _rand(T, H, dtype=BF), _asks(_rand(H))
+    y, h = _rand(T, H, dtype=BF), _rand(T, H, dtype=BF)
+    return afd.rms_norm(x, w).rows.float().sum(), lambda: afd.rms_norm_grad(y, h, w.detach(), torch.ones(T, device="cuda"), out=x)
+
+
+def _routes_of_logits(afd):
+    l = _asks(_rand(T, E))
+    ids = afd.route_tokens(_rand(T, E), K).ids
+    r = afd.route_tokens(l, K)
+    return r.weights.sum(), lambda: afd.route_tokens_grad(_rand(T, K), _rand(T, E), ids, out=l.detach())
+
+
+def _routes_ids(afd):
+    r = afd.route_tokens(_asks(_rand(T, E)), K)
+    return r.weights.sum(), lambda: afd.route_tokens(_rand(T, E), K, ids=r.ids)
+
+
+def _balance_of_logits(afd):
+    l = _asks(_rand(T, E))
+    ids = afd.route_tokens(l.detach(), K).ids
+    slope = torch.ones(E, device="cuda")
+    return afd.balance_loss(l, ids).loss, lambda: afd.balance_loss_grad(slope[0].clone(), _rand(T, E), ids, slope, out=l.detach())
+
+
+def _balance_ids(afd):
+    """The next batch's routes in the buffer of the last one's."""
+    l, ids = _asks(_rand(T, E)), torch.empty(T, K, dtype=torch.int32, device="cuda")
+    afd.route_tokens(l.detach(), K, ids=ids)
+    return afd.balance_loss(l, ids).loss, lambda: afd.route_tokens(_rand(T, E), K, ids=ids)
+
+
+def _weights(afd):
+    w = torch.empty(T, K, device="cuda")
+    afd.route_tokens(_rand(T, E), K, weights=w)
+    return (w * _asks(_rand(K))).sum(), lambda: afd.route_tokens(_rand(T, E) * 2, K, weights=w)
+
+
+def _source_norm(afd):
+    buf = afd.Buffer(1, 1, E, K, H, capacity=T)
+    stream, wq = _rand(T, H, dtype=BF), _asks(_rand(H, 32, dtype=BF))
+    return (stream @ wq).sum(), lambda: buf.source_norm(0, _rand(T, H, dtype=BF), _rand(H), stream, residual_out=stream)
+
+
+CASES = [_projection, _norm_of_x, _norm_of_the_stream, _norm_by_its_gradient, _routes_of_logits, _routes_ids, _balance_of_logits,
+         _balance_ids, _weights, _source_norm]
+
+
+@pytest.mark.parametrize("off", [False, True])
+@pytest.mark.parametrize("case", CASES)
+def test_a_saved_tensor_that_is_overwritten_is_found(case, off):
+    afd = _afd()
+    loss, over = case(afd)
+    loss.backward(retain_graph=True)          # whole before, refused behind
+    with torch.set_grad_enabled(not off):
+        over()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_graphs_of_new_memory_stand():
+    """Calls that make their own outputs, and outputs that no graph saved, disturb no graph."""
+    afd = _afd()
+    x, w, l = _asks(_rand(T, H, dtype=BF)), _asks(_rand(H)), _asks(_rand(T, E))
+    n, r = afd.rms_norm(x, w, x), afd.route_tokens(l, K)
+    b = afd.balance_loss(l, r.ids)
+    with torch.no_grad():
+        other = afd.rms_norm(x, w, x, residual_out=torch.empty_like(x), out=torch.empty_like(x))
+        again = afd.route_tokens(l, K, ids=torch.empty_like(r.ids))
+    (n.rows.float().sum() + r.weights.sum() + b.loss).backward()
+    assert x.grad is not None and l.grad is not None
+    assert torch.equal(other.residual, n.residual) and torch.equal(again.ids, r.ids)

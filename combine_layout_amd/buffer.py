@@ -105,6 +105,7 @@ class Buffer:
         self._bind()
         self._round_refs = {}
         self._out = [None] * num_sources
+        self._given = [False] * num_sources      # whether the caller gave it
         self._T = [0] * num_sources
 
     def _bind(self):
@@ -174,6 +175,7 @@ class Buffer:
             if x_scale.dtype != torch.float32 or tuple(x_scale.shape) != (T, self.H // 128):
                 raise ValueError("x_scale must be float32 [T, H/128]")
             sst, ssg = x_scale.stride()
+        given = out is not None
         if out is None and T > 0:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         if cached:
@@ -189,6 +191,7 @@ class Buffer:
         nat.check(st, "source_dispatch")
         self._round_refs[("src", s)] = (x, ids, weights, x_scale, out)
         self._out[s] = out
+        self._given[s] = given
         self._T[s] = T
 
     def worker_receive(self, f, *, bucket, read_host_counts=False) -> Received:
@@ -271,6 +274,7 @@ class Buffer:
                     raise ValueError("tags must be contiguous int32 [T] tensors on the buffer's device")
                 ptrs[s] = t.data_ptr()
         n = received.receive_rows
+        given = out
         if out is None:
             out = torch.full((n,), -1, dtype=torch.int32, device=dev)
         elif out.dtype is not torch.int32 or out.shape != (n,) or out.device != dev or not out.is_contiguous():
@@ -279,6 +283,8 @@ class Buffer:
             st = self.lib.afd_worker_tags(self.ctx, f, ptrs, out.data_ptr(), n, received.receipt,
                                           _experts.raw_stream(dev))
         nat.check(st, "worker_tags")
+        if given is not None:
+            _experts.wrote(given)
         self._round_refs[("tags", f)] = (tags, out)
         return out
 
@@ -309,6 +315,8 @@ class Buffer:
             return torch.empty((0, self.H), dtype=torch.bfloat16, device=self.device)
         out = self._out[s]
         if out is not None and res.value == out.data_ptr():
+            if self._given[s]:
+                _experts.wrote(out)
             return out
         return self._ws_view(res.value, T * self.H * 2).view(torch.bfloat16).view(T, self.H)
 

@@ -15,6 +15,7 @@ from typing import NamedTuple, Optional
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import _native as nat
 
@@ -89,6 +90,12 @@ def raw_stream(device):
     """The device's current stream as a hipStream_t, without the Stream object
     that torch.cuda.current_stream makes (about 2 us of a call's 10)."""
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def wrote(*given):
+    """The kernels write by address, which autograd does not see: a graph that saved one of the
+    given outputs has to find it changed.  (Tensors of inference mode have no counter.)"""
+    increment_version([t for t in given if t is not None])
 
 
 def _config(kind, *values):
@@ -233,6 +240,7 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
                               nat.ACTIVATIONS[activation], S, rank,
                               nat.WEIGHTS_PACKED if isinstance(weight, PackedWeights) else nat.WEIGHTS_ROWS,
                               rows_per_expert)
+    given = out
     if out is None:
         out = torch.empty((R, n), dtype=torch.bfloat16, device=dev)
     po = _want(out, "out", torch.float8_e4m3fn if out8 else torch.bfloat16, (R, n), dev)
@@ -247,6 +255,8 @@ def expert_product(x, ends, weight, *, alignment=1, x_scales=None, weight_scales
                                            ws.data_ptr() if need else None, need,
                                            raw_stream(dev))
     nat.check(st, "expert_product")
+    if given is not None:
+        wrote(given, out_scales)
     return out
 
 
@@ -276,6 +286,7 @@ def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapter
     wu = _weights("up", experts.up, experts.up_scales, lu, E, 2 * inner, hidden, code, dtype, True, dev)
     wd = _weights("down", experts.down, experts.down_scales, ld, E, hidden, inner, code, dtype, False, dev)
     cfg, need = _ffn_plan(R, E, alignment, hidden, inner, code, S, rank, nat.WEIGHTS_PACKED, rows_per_expert)
+    given = out
     if out is None:
         out = torch.empty((R, hidden), dtype=torch.bfloat16, device=dev)
     po = _want(out, "out", torch.bfloat16, (R, hidden), dev)
@@ -284,4 +295,6 @@ def expert_ffn(x, ends, experts: Experts, *, alignment=1, x_scales=None, adapter
         st = nat.load().afd_expert_ffn(cfg, R, x.data_ptr(), ps, pe, pa, wu, wd, po, ws.data_ptr() if need else None, need,
                                        raw_stream(dev))
     nat.check(st, "expert_ffn")
+    if given is not None:
+        wrote(given)
     return out

@@ -16,10 +16,9 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
-from torch.autograd.graph import increment_version
 
 from . import _native as nat
-from .experts import SCALE_BLOCK, on_device, raw_stream
+from .experts import SCALE_BLOCK, on_device, raw_stream, wrote
 
 _CODES = {torch.bfloat16: nat.AFD_BF16, torch.float32: nat.AFD_FP32}
 
@@ -71,12 +70,6 @@ def _recorded(call, device, *given):
             if torch.cuda.is_current_stream_capturing():
                 raise ValueError(f"{call}: autograd does not record a captured call: call it under no_grad(), and "
                                  f"{call}_grad for the gradient")
-
-
-def _wrote(*given):
-    """The kernels write by address, which autograd does not see: a graph that saved one of the
-    given outputs has to find it changed.  (Tensors of inference mode have no counter.)"""
-    increment_version([t for t in given if t is not None])
 
 
 def _launch(device, call, *args):
@@ -283,7 +276,7 @@ def rms_norm(x, weight, residual=None, *, eps=1e-6, dtype=torch.bfloat16, out=No
         return Normed(rows, None, h, rstd if keep_rstd else None)
     n = _norm(x, weight, residual, eps, dtype, out, out_scales, residual_out, keep_rstd)
     if given:
-        _wrote(out, out_scales, residual_out)
+        wrote(out, out_scales, residual_out)
     return n
 
 
@@ -317,7 +310,7 @@ def rms_norm_grad(grad, h, weight, rstd, *, grad_residual=None, out=None, weight
     if st:
         _check(st, "rms_norm_grad", grad=grad, grad_residual=grad_residual, h=h, weight=weight, out=out)
     if given is not None:
-        _wrote(given)
+        wrote(given)
     return out, dw
 
 
@@ -438,7 +431,7 @@ def route_tokens(logits, topk, *, scoring="softmax", bias=None, renormalize=True
         return Routes(*_RouteTokens.apply(logits, topk, scoring, bias, renormalize, scale, live))
     r = _route(logits, topk, scoring, bias, renormalize, scale, live, ids, weights)
     if ids is not None or weights is not None:
-        _wrote(ids, weights)
+        wrote(ids, weights)
     return r
 
 
@@ -459,7 +452,7 @@ def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True,
     if st:
         nat.check(st, "route_tokens_grad")
     if given is not None:
-        _wrote(given)
+        wrote(given)
     return out
 
 
@@ -555,7 +548,7 @@ def balance_loss_grad(grad, logits, ids, slope, *, scoring="softmax", out=None):
     if st:
         nat.check(st, "balance_loss_grad")
     if given is not None:
-        _wrote(given)
+        wrote(given)
     return out
 
 

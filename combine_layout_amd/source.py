@@ -440,6 +440,7 @@ def route_tokens_grad(grad, logits, ids, *, scoring="softmax", renormalize=True,
     [T, topk], ids as they were chosen (any outside [0, E) takes no part)."""
     renormalize, scale = bool(renormalize), float(scale)
     _plain("route_tokens_grad", grad, logits, ids, out)
+    grad = grad.resolve_neg()       # autograd may hold back a sign, which the memory then lacks
     key = (logits.dtype, logits.shape, logits.stride(), logits.device, scoring, renormalize, scale, _layout(grad), _layout(ids),
            None if out is None else _layout(out))
     plan = _routes.get(key) or _keep(_routes, key, _route_grad_plan(grad, logits, ids, scoring, renormalize, scale, out))
@@ -536,6 +537,7 @@ def balance_loss_grad(grad, logits, ids, slope, *, scoring="softmax", out=None):
     """The logits' gradient, [T, E] of their type: grad float32 [], of the loss on the GPU;
     ids and slope as balance_loss had and gave them.  Tokens that do not count have 0."""
     _plain("balance_loss_grad", grad, logits, ids, slope, out)
+    grad = grad.resolve_neg()
     key = (logits.dtype, logits.shape, logits.stride(), logits.device, _layout(ids), scoring, _layout(grad), _layout(slope),
            None if out is None else _layout(out))
     plan = _balances.get(key) or _keep(_balances, key, _balance_grad_plan(grad, logits, ids, slope, scoring, out))

@@ -114,3 +114,39 @@ def test_graphs_of_new_memory_stand():
     (n.rows.float().sum() + r.weights.sum() + b.loss).backward()
     assert x.grad is not None and l.grad is not None
     assert torch.equal(other.residual, n.residual) and torch.equal(again.ids, r.ids)
+
+
+def _negated(t):
+    """t as the imaginary part of a conjugate: its sign stands beside the memory."""
+    n = torch.complex(torch.zeros_like(t), -t).conj().imag
+    assert n.is_neg() and torch.equal(n, t)
+    return n
+
+
+def test_a_gradient_whose_sign_is_not_in_memory():
+    """Gradients that pass a complex number arrive with their sign held back."""
+    afd = _afd()
+    l = _asks(_rand(T, E))
+    with torch.no_grad():
+        r = afd.route_tokens(l, K)
+        b = afd.balance_loss(l, r.ids)
+        want = afd.balance_loss_grad(torch.full((), 2.0, device="cuda"), l, r.ids, b.slope)
+    seen = []
+    loss = afd.balance_loss(l, r.ids).loss
+    loss.register_hook(lambda g: seen.append(g.is_neg()))
+    (torch.complex(torch.ones_like(loss), loss).conj() * (1 + 2j)).real.backward()     # the loss times 2
+    assert seen == [True]
+    assert torch.equal(l.grad, want)
+    assert torch.equal(afd.balance_loss_grad(_negated(torch.full((), 2.0, device="cuda")), l.detach(), r.ids, b.slope), want)
+    # every element of the weights' gradient, and a gradient of one element, which any stride makes contiguous
+    for tokens, k in ((T, K), (1, 1)):
+        x, g = l.detach()[:tokens].requires_grad_(), _rand(tokens, k)
+        ids = afd.route_tokens(x.detach(), k, renormalize=False).ids
+        (d,) = torch.autograd.grad(afd.route_tokens(x, k, renormalize=False).weights, x, _negated(g))
+        assert torch.equal(d, afd.route_tokens_grad(g, x.detach(), ids, renormalize=False))
+    assert torch.equal(afd.route_tokens_grad(_negated(g), x.detach(), ids, renormalize=False), d)
+    x, w, r = _asks(_rand(T, H)), _asks(_rand(H)), _asks(_rand(T, H))
+    n = afd.rms_norm(x, w, r)
+    grad = _rand(T, H)
+    (d,) = torch.autograd.grad(n.residual, x, _negated(grad))
+    assert torch.equal(d, grad)

@@ -419,7 +419,8 @@ def route_tokens(logits, topk, *, scoring="softmax", bias=None, renormalize=True
     divided by the sum of the token's chosen scores; the bias is not in them.  live (bool
     [T]): tokens that are False have ids -1 and weights 0.  An expert whose logit (or score
     + bias) is minus infinity or NaN is never chosen; ids that are left over are -1, with
-    weight 0.  ids and weights: memory for the results.
+    weight 0.  Weights are within 32 float32 roundings (2^-24 each) of their definition.  ids and
+    weights: memory for the results.
 
     The weights are differentiable by the logits, outside of a capture; the choice has no
     gradient.  Runs on the logits' device and its current stream."""

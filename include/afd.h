@@ -702,6 +702,8 @@ typedef struct {
  * An expert whose logit is minus infinity or NaN, or whose score + bias is, is never
  * chosen; where fewer than K are left, the remaining ids are -1 with weight 0.  Among the
  * softmax's terms a NaN counts as minus infinity; experts at plus infinity share it evenly.
+ * A weight is within 32 float32 roundings (2^-24 each, relative) of its definition however far
+ * the logits lie apart; before the scale it may be 0 where it is below 2^-126.
  * logits need the alignment of their type alone (16 bytes and a stride in multiples of four
  * elements are faster).
  * Errors: AFD_E_ARG (pointers, alignment, rows, stride), AFD_E_SHAPE, AFD_E_HIP.
@@ -714,6 +716,8 @@ afd_status afd_route(const afd_route_config *cfg, int64_t rows, const void *logi
  *   grad     device [rows, K] FP32, of the weights
  *   ids      device [rows, K], from afd_route; any outside [0, E) takes no part
  *   dlogits  device [rows, E], contiguous, of the logits' type; not overlapping an input
+ * Of a softmax over all experts (renormalize 0) the factors have the error of afd_balance's
+ * shares, else that of the weights.
  * Errors: as afd_route.
  */
 afd_status afd_route_grad(const afd_route_config *cfg, int64_t rows, const float *grad, const void *logits,
@@ -739,6 +743,9 @@ afd_status afd_balance_query(const afd_route_config *cfg, int64_t rows, size_t *
  *   workspace  device, at least afd_balance_query bytes, 256-byte aligned; in use until the
  *              call's work has run (NULL where there are none)
  * loss, counts and slope are written also where rows is 0.
+ * A share is within 32 float32 roundings and 2.3 for every unit by which its logit lies below
+ * the token's largest (with AFD_SCORE_SIGMOID 80, and 2.3 for every unit of the logit's size); the
+ * loss has the mean of these and rows / 256 + 70 for its sum.
  * Errors: AFD_E_ARG (pointers, alignment, rows, stride, coefficient not finite), AFD_E_SHAPE,
  * AFD_E_CAPACITY (workspace), AFD_E_HIP.
  */

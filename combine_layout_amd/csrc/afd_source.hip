@@ -1453,9 +1453,10 @@ int norm_grad_of(const NormGradArgs &a, int groups, hipStream_t st)
     if (a.H <= 512) return norm_grad_as<H32, 1, 1>(a, groups, st);
     if (a.H <= 1024) return norm_grad_as<H32, 1, 2>(a, groups, st);
     // a wavefront with four runs, or four with one: bf16 64 rows 3.3 and 2.6 us, 1024 6.2 and 6.7,
-    // 16384 37.0 and 39.8; float32 3.5 and 2.6, 10.3 and 11.8, 93.9 and 86.2
+    // 16384 37.0 and 39.8; float32 3.5 and 2.6, 10.3 and 11.8, 93.9 and 86.2.  By the rows and the type
+    // alone, as the two add a row's products in another order: dh has the same bits without dweight.
     if (a.H <= 2048)
-        return a.rows <= 512 || (H32 && a.part) ? norm_grad_as<H32, 4, 1>(a, groups, st) : norm_grad_as<H32, 1, 4>(a, groups, st);
+        return a.rows <= 512 || (H32 && groups > 0) ? norm_grad_as<H32, 4, 1>(a, groups, st) : norm_grad_as<H32, 1, 4>(a, groups, st);
     if (a.H <= 4096) return norm_grad_as<H32, 4, 2>(a, groups, st);
     if (a.H <= 8192) return norm_grad_as<H32, 4, 4>(a, groups, st);
     return norm_grad_as<H32, 16, 2>(a, groups, st);

@@ -583,8 +583,10 @@ afd_status afd_worker_tags(afd_ctx *ctx, int32_t f, const int32_t *const *tags, 
  * The calls take no context, keep no state and enqueue on `stream` (of the
  * current device); calls on several streams may run at the same time, with
  * different workspaces.  rows is below 2^24; a row stride counts elements, is
- * at least the row's length and below 2^31.  Every sum is float32, in an order
- * that the sizes alone decide: the same inputs give the same bits.
+ * at least the row's length and below 2^31.  Sums are float32 (the loss is joined,
+ * and biased scores that are too near to order are compared, in 64 bits), in an
+ * order that sizes and types alone decide: the same inputs give the same bits,
+ * whichever of a call's outputs are asked for.
  *
  * The gradients are calls of their own.  They end at the exchange: a round
  * carries none.

@@ -3,8 +3,8 @@ with the distance.  In U, half a float32 step, relative to the value:
 
 an exponential is 3 off (its instruction a step, the correction of its argument one
 rounding), a reciprocal of 1 + z 4 (z's own error counts 1.5 at most, as z falls faster than
-it grows; the sum, Newton's step with a margin), a sum of chosen terms 6 more than a term (two slots, then up to 64 lanes), a
-division 1, the scale 1."""
+it grows; the sum, Newton's step with a margin), a sum of chosen terms 6 more than a term (two
+slots, then up to 64 lanes), a division 1, the scale 1."""
 import pytest
 import torch
 

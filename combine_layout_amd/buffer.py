@@ -106,6 +106,7 @@ class Buffer:
         self._round_refs = {}
         self._out = [None] * num_sources
         self._given = [False] * num_sources      # whether the caller gave it
+        self._replies = (-1, 0)                  # the round of the last reply, and how many it has
         self._T = [0] * num_sources
 
     def _bind(self):
@@ -226,6 +227,11 @@ class Buffer:
                                        _stream(self.device))
         nat.check(st, "worker_reply")
         self._round_refs[("reply", f)] = rows
+        if self.F > 1:      # the last one's launch writes every source's sum (one partition's: source_collect)
+            last, n = self._replies
+            self._replies = (receipt.round, n + 1 if last == receipt.round else 1)
+            if self._replies[1] == self.F and any(self._given):
+                _experts.wrote(*(o for o, given in zip(self._out, self._given) if given))
 
     # -- the source's side, between its collect and its dispatch -----------------
     def _source_rows(self, s, t, columns, what, *others):
@@ -315,7 +321,7 @@ class Buffer:
             return torch.empty((0, self.H), dtype=torch.bfloat16, device=self.device)
         out = self._out[s]
         if out is not None and res.value == out.data_ptr():
-            if self._given[s]:
+            if self._given[s] and self.F == 1:
                 _experts.wrote(out)
             return out
         return self._ws_view(res.value, T * self.H * 2).view(torch.bfloat16).view(T, self.H)

@@ -58,6 +58,17 @@ def test_collected(F):
     loss = afd.rms_norm(got, weight).rows.float().sum()
     loss.backward(retain_graph=True)
     before = out._version
+    buf.source_dispatch(0, x, ids, w, bucket=T, out=out)
+    recs = [buf.worker_receive(f, bucket=T) for f in range(F)]
+    replies = [buf.worker_experts(f, rec, experts[f][0]) for f, rec in enumerate(recs)]
+    for f, rec in enumerate(recs):
+        assert out._version == before         # not written yet: the graph stands
+        buf.worker_reply(f, replies[f], rec.receipt)
+    assert (out._version > before) == (F > 1)
+    buf.source_collect(0)
+    assert out._version > before
+    _found(loss)
+    loss, before = afd.rms_norm(got, weight).rows.float().sum(), out._version
     other = a_round(None)                     # new memory: the saved sum stands
     assert out._version == before and torch.equal(other, out) and other._version == 0
     loss.backward(retain_graph=True)

@@ -287,9 +287,10 @@ inline int lanes_of(int E) { return E <= 128 ? 16 : E <= 256 ? 32 : 64; }
 // Workgroups of the balance loss's first launch: each leaves its sums of the shares, its
 // counts, and its numbers of counting tokens and of choices.  Few tokens are one
 // workgroup's of 1024 threads, which has the results without a second launch, up to six
-// turns of it (384 tokens of 128 experts).  On the GPU one turn takes 4.1 us, three 6.7 and
-// six 10.4, and two launches 7.2 to 7.7 (512 experts: two turns 5.5, six 10.9, two launches
-// 10.4); the eager call, which the host bounds, 10 instead of 14.
+// turns of it (384 tokens of 128 experts).  The eager call, which the host bounds, takes 10 us
+// instead of 14 by it.  A captured one, in us: one turn to six 3.9, 4.9, 6.0, 7.0, 8.1 and 9.2
+// with up to 128 experts, where two launches take 7.1 to 7.6 (512 experts: four turns 7.3, two
+// launches 10.3): turns five and six cost it 1 to 2, less than they save the eager one.
 constexpr int kBalanceGroups = 256;
 constexpr int kBalanceSolo = 6;
 inline int balance_groups(int64_t rows, int E)

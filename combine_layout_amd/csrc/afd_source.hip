@@ -303,8 +303,8 @@ __device__ __forceinline__ void norm_grad_columns(const NormGradArgs &a, int blo
 
 // dh = rstd * (a - u * mean(a * u)) + grad_residual of every row, a = grad * weight and u =
 // h * rstd, and the workgroup's sum of grad * u over its rows, which stays in registers from
-// the first row to the last: dweight costs no second reading of many rows.  101 MB in 18.8 us
-// (6144 rows of 2048, BF16; a copy's 19.4) and 4.2 for the launch behind it.
+// the first row to the last: dweight costs no second reading of many rows.  101 MB in 19 us
+// (6144 rows of 2048, BF16; a copy's 19.4) and 4.1 for the launch behind it.
 template <bool H32, int WPR, int C>
 __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 256) void k_norm_grad(NormGradArgs a)
 {
@@ -430,7 +430,7 @@ constexpr float kMinusInf = -__builtin_inff();
 
 // exp(x) for x <= 0.  The argument's rounding costs 1.2 |x| roundings of the result, which
 // summands that are small beside 1 can bear; a second part of the product with log2(e) would
-// be four instructions more of every logit, where the arithmetic bounds (balance loss of 32768
+// be five instructions more of every logit, where the arithmetic bounds (balance loss of 32768
 // tokens and 512 experts 20.5 -> 21.9 us, with sigmoids 22.2 -> 24.7; of 256 tokens and 128
 // experts 7.0 -> 7.8).
 __device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
@@ -901,8 +901,10 @@ __device__ __forceinline__ bool take_above(const int *k, int K, Pick *picks, Pic
 // the choice, which is arithmetic and not memory: a round of `take` is one reduction over
 // the lanes, so a lane's logits are sorted once and only the first of them takes part; with
 // a wavefront for a token a border is cheaper (take_above: 38 -> 29 us).  32768 tokens of 512
-// experts, 8 chosen: 24 us, of which the logits' 67 MB are 13; 6144 tokens of 96 with a bias
-// 6.9; 256 of 128 4.0, the launch, a trip to memory and the chain of eight rounds.
+// experts, 8 chosen: 24 us, of which the logits' 67 MB are 13 and the vector instructions 18;
+// 65536 tokens of 128: 19, 7 and 16, of 256: 34, 14 and 33 (with a bias 29, 7 and 25; 50, 14 and
+// 50); 6144 tokens of 96 with a bias 7.1; 256 of 128 4.0, the launch, a trip to memory and the
+// chain of eight rounds.
 template <bool L32, int LANES, int V, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a)
 {
@@ -1030,8 +1032,10 @@ __device__ __forceinline__ T slot(T v, int k)
 }
 
 // The weights' gradient by the chosen logits, and with DENSE (a softmax over all experts) by
-// every other one.  Persistent, with the next token on its way: 26 -> 25 us for 32768 tokens
-// of 512 experts (dense).
+// every other one.  Persistent, with the next token's logits (dense), ids and gradients on their
+// way: 26 -> 24 us for 32768 tokens of 512 experts (dense; 137 MB, a copy's 26).  The chosen
+// logits alone are gathered behind their ids: 65536 tokens of 128 experts 10.8 us, of 512 38,
+// where the bytes that are written take 7 and 26.
 template <bool L32, int LANES, int V, bool VEC, bool DENSE>
 __global__ __launch_bounds__(256) void k_route_grad(RouteArgs a)
 {
@@ -1197,7 +1201,7 @@ __device__ __forceinline__ float slope_of(float coefficient, int E, int count, i
 
 // Sums of the shares over tokens in registers, counts in LDS; a token's logits and ids are
 // on their way while the one before is worked on.  SOLO: one workgroup has all tokens, and
-// ends with the results.  67 MB of logits in 14 us (32768 tokens of 512 experts; a copy's 13),
+// ends with the results.  67 MB of logits in 15 us (32768 tokens of 512 experts; a copy's 13),
 // with 1024 threads; 7 more for the launch that joins 256 workgroups' sums.
 template <bool L32, int LANES, int V, bool VEC, int THREADS, bool SOLO>
 __global__ __launch_bounds__(THREADS) void k_balance(BalanceArgs b)

@@ -5,6 +5,8 @@ Argument checks and marshalling only: the arithmetic runs in the HIP library.
 rms_norm, route_tokens and balance_loss are differentiable where an input asks
 for a gradient; their gradients are also calls of their own (rms_norm_grad,
 route_tokens_grad, balance_loss_grad), which is how a captured graph has them.
+An output that is given counts as changed in place: a graph that saved it refuses
+its backward pass.
 """
 from __future__ import annotations
 

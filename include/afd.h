@@ -610,6 +610,9 @@ afd_status afd_worker_tags(afd_ctx *ctx, int32_t f, const int32_t *const *tags, 
  *                   and code = e4m3(y * (1 / scale)) to nearest even, from the float32 y; a
  *                   scale below 2^-126 counts as 0 and gives codes 0.  A block with an
  *                   infinity has the scale infinity, NaN codes for its infinities and 0 for the rest.
+ *                   The float32 y is this call's own, off by the roundings of its row's sum and
+ *                   reciprocal root: where y / scale lies half-way between two codes, as ratios
+ *                   of BF16 products often do exactly, either may come.
  *   eps             at least float32's smallest normal number
  * A row whose sum of squares passes float32's range has rstd 0.
  */

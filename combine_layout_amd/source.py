@@ -92,10 +92,19 @@ _norms, _norm_grads, _routes, _balances = {}, {}, {}, {}
 
 
 def _keep(plans, key, plan):
+    if key[1][1] == 1:       # one column: _signed has to look at every call's tensors
+        return plan
     if len(plans) >= _CHECKED:
         plans.clear()
     plans[key] = plan
     return plan
+
+
+def _signed(t, what):
+    """The imaginary part of a conjugate is the conjugated memory and a sign beside it.  Its elements
+    lie two apart, so that the checks of strides pass those of one element or column alone."""
+    if t.is_neg():
+        raise ValueError(f"{what}: its sign is not in its memory: call resolve_neg() on it")
 
 
 def _rows(t, what, device=None):
@@ -106,6 +115,7 @@ def _rows(t, what, device=None):
                          f"other, got {list(t.shape)} with strides {t.stride()} on {t.device}")
     if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
         raise ValueError(f"{what}: rows that share memory (row stride {t.stride(0)} of {t.shape[1]} columns)")
+    _signed(t, what)
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
@@ -136,6 +146,7 @@ def _want(t, what, dtype, shape, device):
     if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}, got " + (
             "None" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}"))
+    _signed(t, what)
     return t.data_ptr()
 
 

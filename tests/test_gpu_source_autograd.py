@@ -150,3 +150,26 @@ def test_a_gradient_whose_sign_is_not_in_memory():
     grad = _rand(T, H)
     (d,) = torch.autograd.grad(n.residual, x, _negated(grad))
     assert torch.equal(d, grad)
+
+
+def test_one_expert_whose_sign_is_not_in_memory():
+    """Logits of one expert, which any stride lets pass: refused at every call, as before and behind those
+    of the same layout that are taken."""
+    afd = _afd()
+    l, ids, one = _rand(T, 1), torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones((), device="cuda")
+    b, dw, slope = torch.full((1,), 0.25, device="cuda"), _rand(T, 1), torch.ones(1, device="cuda")
+    wide = torch.empty(T, 2, device="cuda")[:, :1].copy_(l)
+    kw = dict(scoring="sigmoid", renormalize=False)
+    for _ in range(2):
+        x = _negated(l)
+        for call in (lambda: afd.route_tokens(x, 1, **kw), lambda: afd.route_tokens(l, 1, bias=_negated(b), **kw),
+                     lambda: afd.route_tokens(x.detach().requires_grad_(), 1, **kw), lambda: afd.route_tokens_grad(dw, x, ids, **kw),
+                     lambda: afd.balance_loss(x, ids), lambda: afd.balance_loss_grad(one, x, ids, slope),
+                     lambda: afd.balance_loss_grad(one, l, ids, _negated(slope))):
+            with pytest.raises(ValueError, match="resolve_neg"):
+                call()
+        r = afd.route_tokens(x.resolve_neg(), 1, bias=b, **kw)
+        for y in (l, wide):
+            assert torch.equal(afd.route_tokens(y, 1, bias=b, **kw).weights, r.weights)
+            afd.balance_loss_grad(one, y, ids, afd.balance_loss(y, ids).slope)
+            afd.route_tokens_grad(dw, y, ids, **kw)
